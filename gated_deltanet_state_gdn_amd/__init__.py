@@ -18,10 +18,15 @@ import torch
 from . import _lib
 from ._lib import (GDN_BF16, GDN_F32, GdnDesc, GdnError, GDN_ERR_DEVICE_INPUT, GDN_OK,
                    LIB_PATH, load)
+from ._ops import (gdn_conv, gdn_conv_step, gdn_paged_attn, gdn_paged_workspace_bytes, gdn_qk_norm_rope,
+                   gdn_ssm_scan, gdn_ssm_step, gdn_ssm_workspace_bytes, gdn_step, make_paged_desc, make_ssm_desc)
 
 __all__ = ["gdn_replay", "gdn_prefill", "gdn_state_relerr", "gdn_device_status",
            "gdn_replay_segmented", "gdn_segmented_workspace_bytes",
            "gdn_adaptive_replay_len", "gdn_adaptive_replay_len_static",
+           "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_ssm_workspace_bytes",
+           "gdn_step", "gdn_qk_norm_rope", "gdn_paged_attn", "gdn_paged_workspace_bytes",
+           "make_ssm_desc", "make_paged_desc",
            "gdn_workspace_bytes", "gdn_replay_len", "gdn_status_str", "gdn_abi_version",
            "GdnError", "make_desc", "workspace", "LIB_PATH", "load"]
 

@@ -18,7 +18,9 @@ ABI_VERSION = 3
 EXPORTS = ("gdn_abi_version", "gdn_status_str", "gdn_replay_len", "gdn_workspace_bytes",
            "gdn_replay", "gdn_prefill", "gdn_state_relerr", "gdn_device_status",
            "gdn_adaptive_replay_len", "gdn_adaptive_replay_len_static",
-           "gdn_segmented_workspace_bytes", "gdn_replay_segmented")
+           "gdn_segmented_workspace_bytes", "gdn_replay_segmented",
+           "gdn_conv", "gdn_conv_step", "gdn_ssm_workspace_bytes", "gdn_ssm_scan", "gdn_ssm_step",
+           "gdn_step", "gdn_qk_norm_rope", "gdn_paged_workspace_bytes", "gdn_paged_attn")
 
 
 class GdnDesc(ctypes.Structure):
@@ -26,6 +28,28 @@ class GdnDesc(ctypes.Structure):
                 ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("qkv_dtype", ctypes.c_int32),
                 ("o_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("total_tokens", ctypes.c_int64), ("total_out_tokens", ctypes.c_int64)]
+
+
+_I32, _I64, _F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class GdnConvDesc(ctypes.Structure):
+    _fields_ = [(f, _I32) for f in ("n_seqs", "n_slots", "channels", "width", "dtype", "silu")] + [
+        (f, _I64) for f in ("total_tokens", "x_stride", "y_stride")]
+
+
+class GdnSsmDesc(ctypes.Structure):
+    _fields_ = [(f, _I32) for f in ("n_seqs", "n_slots", "h_qk", "h_v", "d_k", "d_v", "dtype", "softplus")] + [
+        (f, _I64) for f in ("total_tokens", "total_out_tokens", "x_stride", "b_stride", "c_stride",
+                            "dt_stride", "y_stride")]
+
+
+class GdnPagedDesc(ctypes.Structure):
+    _fields_ = [(f, _I32) for f in ("n_seqs", "h_q", "h_kv", "d", "dtype", "page_size", "n_pages", "max_pages",
+                                    "max_kv_len", "rot_dim", "interleaved", "norm", "max_pos")] + [
+        ("eps", _F32), ("scale", _F32)] + [
+        (f, _I64) for f in ("total_tokens", "q_stride", "k_stride", "v_stride", "o_stride", "page_stride",
+                            "token_stride", "head_stride")]
 
 
 class GdnError(RuntimeError):
@@ -73,6 +97,19 @@ def load() -> ctypes.CDLL:
     lib.gdn_segmented_workspace_bytes.restype = sz
     lib.gdn_replay_segmented.argtypes = [dptr, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     lib.gdn_replay_segmented.restype = i32
+    cptr, sptr, pptr = (ctypes.POINTER(t) for t in (GdnConvDesc, GdnSsmDesc, GdnPagedDesc))
+    for name, desc, pointers in (("gdn_conv", cptr, 7), ("gdn_conv_step", cptr, 6), ("gdn_ssm_scan", sptr, 13),
+                                 ("gdn_ssm_step", sptr, 10), ("gdn_qk_norm_rope", pptr, 13),
+                                 ("gdn_paged_attn", pptr, 8)):
+        f = getattr(lib, name)
+        f.argtypes = [desc] + [vp] * pointers + [vp, sz, vp]
+        f.restype = i32
+    lib.gdn_step.argtypes = [dptr] + [vp] * 6 + [i32, vp, vp, vp, sz, vp]
+    lib.gdn_step.restype = i32
+    lib.gdn_ssm_workspace_bytes.argtypes = [sptr]
+    lib.gdn_ssm_workspace_bytes.restype = sz
+    lib.gdn_paged_workspace_bytes.argtypes = [pptr]
+    lib.gdn_paged_workspace_bytes.restype = sz
     if lib.gdn_abi_version() != ABI_VERSION:
         raise ImportError("libgdn.so ABI version mismatch")
     _lib = lib

@@ -16,7 +16,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
-SOURCES = ["gdn_api.hip", "gdn_chunk_ws.hip", "gdn_relerr.hip", "gdn_adaptive.hip", "gdn_segment.hip"]
+SOURCES = ["gdn_api.hip", "gdn_chunk_ws.hip", "gdn_relerr.hip", "gdn_adaptive.hip", "gdn_segment.hip",
+           "gdn_ops_api.hip", "gdn_conv.hip", "gdn_scan.hip", "gdn_step.hip", "gdn_rope.hip", "gdn_paged_attn.hip"]
+# host-only sources: argument validation and launches
+API_SOURCES = ["gdn_api.hip", "gdn_ops_api.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 
@@ -58,7 +61,7 @@ def build(jobs: int = 4, verbose: bool = True) -> str:
     return LIB
 
 
-# Host-side sanitizers for the argument validation in gdn_api.hip: only host code is
+# Host-side sanitizers for the argument validation in API_SOURCES: only host code is
 # instrumented (each -fsanitize= follows -Xarch_host); device code is built as usual.
 HOST_SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                  "-Xarch_host", "-fno-sanitize-recover=undefined",
@@ -66,7 +69,7 @@ HOST_SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize
 
 
 def build_host_sanitized(out_dir: str = os.path.join(BUILD, "hostsan")) -> str:
-    """libgdn with an ASan+UBSan-instrumented gdn_api.hip, for CPU-only validation tests.
+    """libgdn with ASan+UBSan-instrumented API_SOURCES, for CPU-only validation tests.
 
     The process that loads it must preload clang's ASan runtime
     (``clang_asan_runtime()``).  The other objects are the regular build's.
@@ -74,18 +77,19 @@ def build_host_sanitized(out_dir: str = os.path.join(BUILD, "hostsan")) -> str:
     os.makedirs(out_dir, exist_ok=True)
     objs = []
     for src in SOURCES:
-        if src == "gdn_api.hip":
+        if src in API_SOURCES:
             continue
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         if not os.path.exists(obj) or os.path.getmtime(obj) < os.path.getmtime(os.path.join(CSRC, src)):
             os.makedirs(BUILD, exist_ok=True)
             _compile(src)
         objs.append(obj)
-    api = os.path.join(out_dir, "gdn_api.o")
-    subprocess.check_call([hipcc()] + flags() + HOST_SANITIZE +
-                          ["-c", os.path.join(CSRC, "gdn_api.hip"), "-o", api])
+    for src in API_SOURCES:
+        obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
+        subprocess.check_call([hipcc()] + flags() + HOST_SANITIZE + ["-c", os.path.join(CSRC, src), "-o", obj])
+        objs.append(obj)
     lib = os.path.join(out_dir, "libgdn_hostsan.so")
-    subprocess.check_call([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", lib, api] + objs)
+    subprocess.check_call([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", lib] + objs)
     return lib
 
 

@@ -1,0 +1,491 @@
+// Selective state space scan over packed sequences, in chunks of C = 64 tokens.
+//
+//     S_t = a_t S_{t-1} + dt_t B_t x_t^T,   y_t = S_t^T C_t + D x_t,   a_t = exp(dt_t A)
+//
+// per (sequence, head), B and C shared by the heads of a group.  With G the running sum of log a
+// inside a chunk and S the state in front of it,
+//     M_ij = (C_i . B_j) exp(G_i - G_j) dt_j   (j <= i),
+//     Y    = M X + diag(exp G) C S + D X,
+//     S   <- exp(G_last) S + B^T diag(exp(G_last - G_j) dt_j) X,
+// which is the recurrence exactly in exact arithmetic.  All exponents are sums of the log a of a
+// stretch of tokens, formed as differences of a 64-bit running sum kept as two floats: strong
+// decays in front of weak ones cost the weak ones nothing.
+//
+// Work decomposition: a workgroup of four waves takes HB heads of one group over one segment of
+// one sequence, chunk by chunk.  The columns of S (d_v of every head) do not mix, so a wave owns
+// some 16-column tiles of S whole, in its accumulators; M is the only product the waves share, and
+// goes through LDS.  Y is formed transposed (Y^T = S^T C^T + X^T M^T): accumulators of S become
+// operands where they are, and a lane ends with four consecutive entries of one token's y.
+//
+// The decay is one number per head and token, so segments join elementwise: with more than one
+// segment, a first launch forms every segment's state from zero and its decay, a second chains
+// them (S_start(s+1) = decay_s S_start(s) + local_s), and a third forms the outputs.
+//
+// Precision: S, G and every sum are fp32 or wider.  bf16 inputs enter the matrix products as they
+// are; M, and S in C S, are rounded to bf16 once (half a bf16 step, as the output itself is).  The
+// state is an fp32 output: there diag(w) X is split into three bf16 terms, 24 bits, and multiplied
+// with B exactly as B is.  fp32 inputs use fp32 products throughout.
+#include "gdn_mfma.h"
+
+namespace gdn {
+namespace {
+
+constexpr int CH = 64;      // tokens of a chunk
+constexpr int NT = 256;
+constexpr int MODE_FULL = 0, MODE_STATE = 1, MODE_OUT = 2;
+
+// The window of sequence n: its tokens [beg, end), false if cu or r is bad.
+__device__ __forceinline__ bool window(const ScanArgs &a, int n, int64_t &beg, int64_t &end) {
+    const int32_t b = a.cu[n], e = a.cu[n + 1];
+    if (!range_ok(b, e, a.total)) return false;
+    int32_t len = e - b;
+    if (a.r) {
+        const int32_t r = a.r[n];
+        if (r < 0 || r > len) return false;
+        len = r;
+    }
+    beg = e - len;
+    end = e;
+    return true;
+}
+// Output row of sequence n's first token: its own token, or with replay lengths the sum of those
+// before it (a wave's sum; -1 if it does not fit).
+__device__ __forceinline__ int64_t out_row(const ScanArgs &a, int n, int64_t beg, int64_t len) {
+    int64_t row = beg;
+    if (a.r) {
+        int64_t s = 0;
+        for (int i = threadIdx.x & 63; i < n; i += 64) {
+            int64_t b, e;
+            if (window(a, i, b, e)) s += e - b;
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+        row = s;
+    }
+    return row + len <= a.total_out ? row : -1;
+}
+__device__ __forceinline__ int chunks_per_segment(int64_t len, int segs) {
+    const int64_t c = (len + CH - 1) / CH;
+    return (int)((c + segs - 1) / segs);
+}
+
+template <class M, int DK, int DV, int HB>
+struct Lds {
+    typedef typename M::T T;
+    static constexpr int SK = DK + M::PAD, SV = HB * DV + M::PAD, SM = CH + M::PAD;
+    alignas(16) T B[CH * SK];
+    alignas(16) T C[CH * SK];
+    alignas(16) T X[CH * SV];
+    alignas(16) T Mx[HB][CH * SM];       // M, row i
+    float hi[HB][CH], lo[HB][CH];        // G log2 e in two floats
+    float dt[HB][CH], w[HB][CH];         // dt_j and exp(G_last - G_j) dt_j
+    float e[HB][CH];                     // exp(G_i)
+    float last[HB];                      // exp(G_last)
+    double total[HB];                    // log2 of the decay since the segment's start
+};
+
+template <class M, int DK, int DV, int HB, int MODE>
+__global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
+{
+    typedef typename M::T T;
+    typedef typename M::Frag Frag;
+    typedef Lds<M, DK, DV, HB> L;
+    constexpr int V = M::V;
+    constexpr int TILES = HB * DV / 16 / 4;          // 16-column tiles of a wave
+    constexpr bool Y = MODE != MODE_STATE;
+    extern __shared__ __align__(16) char smem[];
+    L &s = *reinterpret_cast<L *>(smem);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane >> 4, col = lane & 15;
+
+    if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
+    const int hblocks = a.h_v / HB;
+    const int hb = blockIdx.x % hblocks;
+    const int seg = (blockIdx.x / hblocks) % a.segs;
+    const int n = blockIdx.x / hblocks / a.segs;
+    const int h0 = hb * HB;
+    int64_t beg, end;
+    if (!window(a, n, beg, end)) {
+        if (threadIdx.x == 0) set_status(a.status);
+        return;
+    }
+    const int64_t len = end - beg;
+    int64_t row0 = 0;
+    if (Y) {
+        row0 = out_row(a, n, beg, len);
+        if (row0 < 0) {
+            if (threadIdx.x == 0) set_status(a.status);
+            return;
+        }
+    }
+    const int cps = chunks_per_segment(len, a.segs);
+    const int64_t sbeg = beg + (int64_t)seg * cps * CH;
+    const int64_t send = sbeg + (int64_t)cps * CH < end ? sbeg + (int64_t)cps * CH : end;
+    if (a.segs > 1 && sbeg >= end) return;           // an empty segment: nothing reads its state
+    const int nch = sbeg < send ? (int)((send - sbeg + CH - 1) / CH) : 0;
+
+    // this wave's column tiles all belong to one head
+    const int hl = wave * TILES * 16 / DV;           // head within the block
+    const int h = h0 + hl;
+    const int c0 = wave * TILES * 16;                // first column within the block's HB * DV
+    const int p0 = c0 - hl * DV;                     // and within the head
+    const int64_t state = (((int64_t)n * a.segs + seg) * a.h_v + h) * DK * DV;
+    const float *Sin = nullptr;
+    if (MODE == MODE_OUT) Sin = a.seg_state + state;
+    else if (a.segs == 1 && a.S0) Sin = a.S0 + state;
+
+    f32x4 S[DK / 16][TILES];
+#pragma unroll
+    for (int kt = 0; kt < DK / 16; ++kt)
+#pragma unroll
+        for (int pt = 0; pt < TILES; ++pt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                S[kt][pt][i] = Sin ? Sin[(int64_t)(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col] : 0.0f;
+
+    if (Y) {   // the tiles right of the diagonal that share a 32-deep step with it stay zero
+        for (int i = threadIdx.x; i < HB * CH * L::SM; i += NT) (&s.Mx[0][0])[i] = 0;
+    }
+    if (threadIdx.x < HB) s.total[threadIdx.x] = 0.0;
+
+    const int gq = h0 / (a.h_v / a.h_qk);            // the group's B and C
+    const T *Bp = static_cast<const T *>(a.B) + (int64_t)gq * DK;
+    const T *Cp = static_cast<const T *>(a.C) + (int64_t)gq * DK;
+    const T *Xp = static_cast<const T *>(a.x) + (int64_t)h0 * DV;
+    const T *dtp = static_cast<const T *>(a.dt) + h0;
+    constexpr int NBK = CH * DK / V / NT, NX = CH * HB * DV / V / NT;
+    u32x4 rb[NBK], rc[NBK], rx[NX];
+    float rdt = 0.0f;
+
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < NBK; ++i) {
+            const int e = (threadIdx.x + i * NT) * V, row = e / DK;
+            const bool in = t0 + row < send;
+            rb[i] = in ? load16(Bp + (t0 + row) * a.bs + e % DK) : u32x4{0, 0, 0, 0};
+            if (Y) rc[i] = in ? load16(Cp + (t0 + row) * a.cs + e % DK) : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = (threadIdx.x + i * NT) * V, row = e / (HB * DV);
+            rx[i] = t0 + row < send ? load16(Xp + (t0 + row) * a.xs + e % (HB * DV)) : u32x4{0, 0, 0, 0};
+        }
+        if (wave < HB) rdt = t0 + lane < send ? M::one(dtp + (t0 + lane) * a.dts + wave) : 0.0f;
+    };
+    if (nch > 0) fetch(sbeg);
+
+    for (int ch = 0; ch < nch; ++ch) {
+        const int64_t t0 = sbeg + (int64_t)ch * CH;
+        __syncthreads();                             // the last chunk's readers are done
+#pragma unroll
+        for (int i = 0; i < NBK; ++i) {
+            const int e = (threadIdx.x + i * NT) * V, row = e / DK;
+            store16(&s.B[row * L::SK + e % DK], rb[i]);
+            if (Y) store16(&s.C[row * L::SK + e % DK], rc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = (threadIdx.x + i * NT) * V, row = e / (HB * DV);
+            store16(&s.X[row * L::SV + e % (HB * DV)], rx[i]);
+        }
+        if (wave < HB) {                             // the gates of head h0 + wave
+            const bool in = t0 + lane < send;
+            float dt = rdt + (a.dt_bias ? a.dt_bias[h0 + wave] : 0.0f);
+            if (a.softplus) dt = softplus(dt);
+            dt = in ? dt : 0.0f;
+            // log2 a; below -1000 it is 0 in fp32 whatever follows, and stays finite here
+            double G = in ? fmax((double)dt * (double)a.A[h0 + wave] * 1.4426950408889634, -1000.0) : 0.0;
+#pragma unroll
+            for (int off = 1; off < 64; off *= 2) {
+                const double up = __shfl_up(G, off);
+                if (lane >= off) G += up;
+            }
+            const double all = __shfl(G, 63);
+            const float hi = (float)G;
+            s.hi[wave][lane] = hi;
+            s.lo[wave][lane] = (float)(G - (double)hi);
+            s.dt[wave][lane] = dt;
+            s.w[wave][lane] = exp2f((float)(all - G)) * dt;
+            s.e[wave][lane] = exp2f((float)G);
+            if (lane == 0) {
+                s.last[wave] = exp2f((float)all);
+                s.total[wave] += all;
+            }
+        }
+        __syncthreads();
+        if (ch + 1 < nch) fetch(t0 + CH);
+
+        if (Y) {
+            // M: the ten 16 x 16 tiles on and below the diagonal, shared out among the waves;
+            // C B^T is the same for the block's heads.  Rows j in the accumulator, column i.
+#pragma unroll
+            for (int tt = 0; tt < 3; ++tt) {
+                const int t = wave + 4 * tt;
+                if (t >= 10) break;
+                const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
+                const int jt = t - it * (it + 1) / 2;
+                f32x4 cb = {0, 0, 0, 0};
+#pragma unroll
+                for (int kb = 0; kb < DK / 32; ++kb)
+                    cb = M::mma(cb, M::row_nat(&s.B[16 * jt * L::SK + 32 * kb], L::SK, lane),
+                                M::row_nat(&s.C[16 * it * L::SK + 32 * kb], L::SK, lane));
+                const int i = 16 * it + col, j0 = 16 * jt + 4 * g;
+#pragma unroll
+                for (int q = 0; q < HB; ++q) {
+                    const float hi = s.hi[q][i], lo = s.lo[q][i];
+                    float m[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = j0 + k;
+                        const float d = (hi - s.hi[q][j]) + (lo - s.lo[q][j]);
+                        m[k] = j <= i ? cb[k] * (exp2f(d) * s.dt[q][j]) : 0.0f;
+                    }
+                    M::store4(&s.Mx[q][i * L::SM + j0], m);
+                }
+            }
+        }
+        f32x4 yt[4][TILES];
+        if (Y) {
+            // exp(G_i) (S^T C^T)
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int pt = 0; pt < TILES; ++pt) yt[it][pt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < DK / 32; ++kb) {
+                Frag St[TILES];
+#pragma unroll
+                for (int pt = 0; pt < TILES; ++pt) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = S[2 * kb + (i >> 2)][pt][i & 3];
+                    St[pt] = M::from_floats(f);
+                }
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const Frag cf = M::row_acc(&s.C[16 * it * L::SK + 32 * kb], L::SK, lane);
+#pragma unroll
+                    for (int pt = 0; pt < TILES; ++pt) yt[it][pt] = M::mma(yt[it][pt], St[pt], cf);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const float e = s.e[hl][16 * it + col];
+#pragma unroll
+                for (int pt = 0; pt < TILES; ++pt) yt[it][pt] *= e;
+            }
+            __syncthreads();                         // M is whole
+        }
+        // X^T: rows p for Y^T, and (the same registers) columns p for the state
+        Frag xf[2][TILES];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int pt = 0; pt < TILES; ++pt)
+                xf[kb][pt] = M::col_acc(&s.X[32 * kb * L::SV + c0 + 16 * pt], L::SV, lane);
+        if (Y) {
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int kb = 0; kb <= it / 2; ++kb) {
+                    const Frag mf = M::row_acc(&s.Mx[hl][16 * it * L::SM + 32 * kb], L::SM, lane);
+#pragma unroll
+                    for (int pt = 0; pt < TILES; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
+                }
+            const float D = a.D ? a.D[h] : 0.0f;
+            T *yp = static_cast<T *>(a.y);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int i = 16 * it + col;
+                if (t0 + i >= send) continue;
+#pragma unroll
+                for (int pt = 0; pt < TILES; ++pt) {
+                    float x[4], o[4];
+                    M::load4(&s.X[i * L::SV + c0 + 16 * pt + 4 * g], x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
+                    M::store4(yp + (row0 + (t0 - beg) + i) * a.ys + (int64_t)h * DV + p0 + 16 * pt + 4 * g, o);
+                }
+            }
+        }
+        // the state; the outputs alone (MODE_OUT) only need it to the precision of C S
+        if (MODE == MODE_OUT && ch + 1 == nch) continue;
+        const float last = s.last[hl];
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt)
+#pragma unroll
+            for (int pt = 0; pt < TILES; ++pt) S[kt][pt] *= last;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            constexpr int TERMS = V == 4 || MODE == MODE_OUT ? 1 : 3;
+            Frag wx[TILES][TERMS];
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = s.w[hl][32 * kb + 4 * g + (j & 3) + 16 * (j >> 2)];
+#pragma unroll
+            for (int pt = 0; pt < TILES; ++pt) {
+                float x[8];
+                M::to_floats(xf[kb][pt], x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= w[j];
+#pragma unroll
+                for (int term = 0; term < TERMS; ++term) {
+                    wx[pt][term] = M::from_floats(x);
+                    if (term + 1 < TERMS) {
+                        float got[8];
+                        M::to_floats(wx[pt][term], got);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] -= got[j];
+                    }
+                }
+            }
+#pragma unroll
+            for (int kt = 0; kt < DK / 16; ++kt) {
+                const Frag bf = M::col_acc(&s.B[32 * kb * L::SK + 16 * kt], L::SK, lane);
+#pragma unroll
+                for (int pt = 0; pt < TILES; ++pt)
+#pragma unroll
+                    for (int term = TERMS - 1; term >= 0; --term) S[kt][pt] = M::mma(S[kt][pt], bf, wx[pt][term]);
+            }
+        }
+    }
+    if (MODE == MODE_OUT) return;
+    float *So = a.segs > 1 ? a.seg_state + state : a.S_out + state;
+#pragma unroll
+    for (int kt = 0; kt < DK / 16; ++kt)
+#pragma unroll
+        for (int pt = 0; pt < TILES; ++pt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                So[(int64_t)(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col] = S[kt][pt][i];
+    if (a.segs > 1 && threadIdx.x < HB)
+        a.seg_decay[((int64_t)n * a.segs + seg) * a.h_v + h0 + threadIdx.x] = (float)exp2(s.total[threadIdx.x]);
+}
+
+// Chains the segments of a state: every segment's local state is replaced by the state in front
+// of it, and the last one goes to S_out.  One thread per four entries.
+__global__ void __launch_bounds__(NT) chain_kernel(ScanArgs a, int elems)
+{
+    const int64_t q = (int64_t)blockIdx.x * NT + threadIdx.x;
+    const int per = elems / 4;
+    const int64_t chain = q / per;
+    if (chain >= (int64_t)a.n_seqs * a.h_v) return;
+    const int n = (int)(chain / a.h_v), h = (int)(chain % a.h_v);
+    const int64_t at = (q % per) * 4;
+    int64_t beg, end;
+    if (!window(a, n, beg, end)) return;
+    const int cps = chunks_per_segment(end - beg, a.segs);
+    const int act = cps > 0 ? (int)(((end - beg + CH - 1) / CH + cps - 1) / cps) : 0;
+    f32x4 run = {0, 0, 0, 0};
+    if (a.S0) run = *reinterpret_cast<const f32x4 *>(a.S0 + chain * elems + at);
+    float *p = a.seg_state + ((int64_t)n * a.segs * a.h_v + h) * elems + at;
+    const float *d = a.seg_decay + (int64_t)n * a.segs * a.h_v + h;
+    const int64_t next = (int64_t)a.h_v * elems;
+    constexpr int U = 4;                              // loads in flight: the chain itself is short
+    for (int s0 = 0; s0 < act; s0 += U) {
+        f32x4 l[U];
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u < act ? s0 + u : act - 1;
+            l[u] = *reinterpret_cast<const f32x4 *>(p + s * next);
+            f[u] = d[(int64_t)s * a.h_v];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s0 + u >= act) break;
+            *reinterpret_cast<f32x4 *>(p + (s0 + u) * next) = run;
+            run = run * f[u] + l[u];
+        }
+    }
+    *reinterpret_cast<f32x4 *>(a.S_out + chain * elems + at) = run;
+}
+
+// Output row offsets of replay windows, for a caller that asks for them.
+__global__ void __launch_bounds__(64) offsets_kernel(ScanArgs a)
+{
+    int64_t run = 0;
+    for (int n0 = 0; n0 <= a.n_seqs; n0 += 64) {
+        const int n = n0 + threadIdx.x;
+        int64_t v = 0;
+        if (n < a.n_seqs) {
+            int64_t b = 0, e = 0;
+            if (window(a, n, b, e)) v = e - b;
+        }
+        int64_t sum = v;
+#pragma unroll
+        for (int off = 1; off < 64; off *= 2) {
+            const int64_t up = __shfl_up(sum, off);
+            if ((int)threadIdx.x >= off) sum += up;
+        }
+        if (n <= a.n_seqs) a.cu_out[n] = (int32_t)(run + sum - v);
+        run += __shfl(sum, 63);
+    }
+}
+
+template <class M, int DK, int DV, int HB, int MODE>
+hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
+{
+    constexpr int bytes = sizeof(Lds<M, DK, DV, HB>);
+    static_assert(bytes <= 160 * 1024, "one workgroup's LDS");
+    const int64_t blocks = (int64_t)a.n_seqs * a.segs * (a.h_v / HB);
+    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
+    auto k = scan_kernel<M, DK, DV, HB, MODE>;
+    if (bytes > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(NT), bytes, stream, a);
+    return hipGetLastError();
+}
+
+template <class M, int DK, int DV, int HB>
+hipError_t scan_h(const ScanArgs &a, hipStream_t stream)
+{
+    if (a.cu_out) {
+        hipLaunchKernelGGL(offsets_kernel, dim3(1), dim3(64), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.segs == 1) return a.y ? scan_m<M, DK, DV, HB, MODE_FULL>(a, stream) : scan_m<M, DK, DV, HB, MODE_STATE>(a, stream);
+    hipError_t e = scan_m<M, DK, DV, HB, MODE_STATE>(a, stream);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = ((int64_t)a.n_seqs * a.h_v * (DK * DV / 4) + NT - 1) / NT;
+    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(chain_kernel, dim3((unsigned)blocks), dim3(NT), 0, stream, a, DK * DV);
+    e = hipGetLastError();
+    if (e != hipSuccess || !a.y) return e;
+    return scan_m<M, DK, DV, HB, MODE_OUT>(a, stream);
+}
+
+template <class M, int DK>
+hipError_t scan_v(const ScanArgs &a, int d_v, hipStream_t stream)
+{
+    if (d_v == 128) return scan_h<M, DK, 128, 1>(a, stream);
+    // two heads of a group side by side halve the reads of B and C; fp32 tiles fill the LDS alone
+    if constexpr (M::V == 8)
+        if ((a.h_v / a.h_qk) % 2 == 0) return scan_h<M, DK, 64, 2>(a, stream);
+    return scan_h<M, DK, 64, 1>(a, stream);
+}
+
+}  // namespace
+
+// Enough segments that a launch has about 1024 workgroups, of eight chunks or more each.
+int32_t scan_segments(int32_t n_seqs, int32_t h_qk, int32_t h_v, int32_t d_v, int bf16, int64_t tokens)
+{
+    if (n_seqs <= 0) return 1;
+    const int hb = bf16 && d_v == 64 && (h_v / h_qk) % 2 == 0 ? 2 : 1;
+    const int64_t chains = (int64_t)n_seqs * (h_v / hb);
+    const int64_t chunks = (tokens / n_seqs + CH - 1) / CH;
+    int64_t s = 1024 / chains;
+    if (chunks / 8 < s) s = chunks / 8;
+    return (int32_t)(s < 1 ? 1 : s);
+}
+
+hipError_t launch_scan(const ScanArgs &a, int bf16, int d_k, int d_v, hipStream_t stream)
+{
+    if (bf16) return d_k == 128 ? scan_v<MfmaBF16, 128>(a, d_v, stream) : scan_v<MfmaBF16, 64>(a, d_v, stream);
+    return d_k == 128 ? scan_v<MfmaF32, 128>(a, d_v, stream) : scan_v<MfmaF32, 64>(a, d_v, stream);
+}
+
+}  // namespace gdn

@@ -228,6 +228,147 @@ int32_t gdn_replay_segmented(const gdn_desc *desc, const void *q, const void *k,
  * wait, the copy or the clear failed. */
 int32_t gdn_device_status(const void *workspace, void *stream, int32_t *status_host);
 
+/* ---------------------------------------------------------------------------------------
+ * The rest of a hybrid model's step after a cache hit.  The matched prefix's recurrent states
+ * are rebuilt by gdn_replay and its full-attention keys and values are kept exactly; the
+ * unmatched suffix is then prefilled from both and tokens follow one by one (technical summary,
+ * "Mecanismos Principais" and "Resultados").  Beside gdn_prefill that takes the short causal
+ * convolution in front of a recurrent layer, the scan of a state space layer, single-token
+ * steps, and for the full-attention layers the norm and rotation of q and k with the append to
+ * a paged cache, and attention of the new tokens over that cache.
+ *
+ * They follow the conventions above: caller-owned buffers, asynchronous on `stream`, host
+ * errors before anything is enqueued, device-resident integers checked by the kernels into the
+ * workspace's status word.  A workspace starts zero-filled; its first 256 bytes are the status
+ * word.  Two calls that may run at the same time (two streams, two graphs) need a workspace
+ * each.  Rows of x, y, q, k, v may be columns of a wider buffer: a stride field gives the
+ * elements from one token's row to the next, the rows themselves are contiguous and start on
+ * 16 bytes.  Outputs must not overlap inputs except where it is said.  Rows behind the last
+ * sequence (tokens at or after cu_seqlens[n_seqs]) are left as they were.  Non-finite inputs
+ * are not checked; what a cache holds behind a sequence's kv_len is never read.
+ *
+ * Single-token calls: row i uses state slots[i] of a pool of n_slots states, updated in place;
+ * slots NULL: state i.  slots[i] = -1 marks a padded row: neither its state nor its output is
+ * touched.  A slot out of range, or equal to an earlier row's, sets the status bit and leaves
+ * that row's output and state as they were.
+ * --------------------------------------------------------------------------------------- */
+
+/* Short causal convolution, one filter of `width` taps (2, 3 or 4) per channel:
+ *     y[t, c] = act(bias[c] + sum_j weight[c, j] x[t - (width - 1) + j, c]),
+ * act = SiLU or none.  weight [channels, width] and bias [channels] (nullable) are fp32; x, y and
+ * the states [., width - 1, channels] (the last inputs, oldest first) have `dtype`.
+ * channels * element size must be a multiple of 16 bytes. */
+typedef struct {
+    int32_t n_seqs;            /* packed sequences; gdn_conv_step: rows */
+    int32_t n_slots;           /* gdn_conv_step: states of the pool */
+    int32_t channels, width;
+    int32_t dtype;             /* gdn_dtype */
+    int32_t silu;              /* 1: SiLU behind the sum, 0: none */
+    int64_t total_tokens;      /* rows of x and y; gdn_conv_step: n_seqs */
+    int64_t x_stride, y_stride;
+} gdn_conv_desc;
+
+/* Prompts: state0 (nullable: zero) [n_seqs, width - 1, channels] are the inputs in front of each
+ * sequence, state_out (nullable, may be state0) those behind it. */
+int32_t gdn_conv(const gdn_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                 const int32_t *cu_seqlens, const void *state0, void *state_out, void *y,
+                 void *workspace, size_t workspace_bytes, void *stream);
+/* One token per row; state [n_slots, width - 1, channels]. */
+int32_t gdn_conv_step(const gdn_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                      void *state, const int32_t *slots, void *y, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Selective state space recurrence, per (sequence, head h), group q = floor(h h_qk / h_v):
+ *     dt'_t = softplus(dt[t, h] + dt_bias[h])   (softplus = 0: the sum itself),
+ *     S_t = exp(dt'_t A[h]) S_{t-1} + dt'_t B[t, q] x[t, h]^T,   y_t = S_t^T C[t, q] + D[h] x[t, h],
+ * S [d_k, d_v] as in gdn_prefill.  x, y [T, h_v, d_v], B, C [T, h_qk, d_k], dt [T, h_v] have
+ * `dtype`; A, dt_bias, D [h_v] are fp32 (the last two nullable); states are fp32.  A is finite
+ * and not positive, dt finite.  d_k and d_v in {64, 128}. */
+typedef struct {
+    int32_t n_seqs;            /* packed sequences; gdn_ssm_step: rows */
+    int32_t n_slots;           /* gdn_ssm_step: states of the pool */
+    int32_t h_qk, h_v;         /* heads of B and C, heads of x: h_v % h_qk == 0 */
+    int32_t d_k, d_v;          /* state size, head size */
+    int32_t dtype;             /* gdn_dtype */
+    int32_t softplus;          /* 1: softplus over dt + dt_bias, 0: the sum itself */
+    int64_t total_tokens;      /* rows of x, B, C, dt; gdn_ssm_step: n_seqs */
+    int64_t total_out_tokens;  /* rows of y: total_tokens, or sum r[n] with replay lengths */
+    int64_t x_stride, b_stride, c_stride, dt_stride, y_stride;   /* dt_stride: any >= h_v */
+} gdn_ssm_desc;
+
+/* Bytes of gdn_ssm_scan's workspace: 256, and for few long sequences the states of the segments
+ * that they are cut into (0 for a descriptor that is refused). */
+size_t gdn_ssm_workspace_bytes(const gdn_ssm_desc *desc);
+/* Prompts.  r NULL: whole sequences from S0 (nullable: zero).  r [n_seqs]: the last r[n] tokens of
+ * each, as gdn_replay takes them (S0 is then the state in front of the window), y's rows packed
+ * per window and cu_out (nullable) [n_seqs + 1] their offsets.  y is nullable; S_out may be S0.
+ * bf16: products take bf16 operands with fp32 sums; M and S are rounded to bf16 once in y, and
+ * S_out is accurate to fp32 (its operands enter in three bf16 terms). */
+int32_t gdn_ssm_scan(const gdn_ssm_desc *desc, const void *x, const void *B, const void *C, const void *dt,
+                     const float *A, const float *dt_bias, const float *D, const int32_t *cu_seqlens,
+                     const int32_t *r, const float *S0, float *S_out, void *y, int32_t *cu_out,
+                     void *workspace, size_t workspace_bytes, void *stream);
+/* One token per row; S [n_slots, h_v, d_k, d_v]. */
+int32_t gdn_ssm_step(const gdn_ssm_desc *desc, const void *x, const void *B, const void *C, const void *dt,
+                     const float *A, const float *dt_bias, const float *D, float *S, const int32_t *slots,
+                     void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of the gated delta rule per row, fp32 arithmetic throughout; layouts and fields as
+ * gdn_prefill with n_seqs = total_tokens = total_out_tokens rows, S [n_slots, h_v, d_k, d_v]. */
+int32_t gdn_step(const gdn_desc *desc, const void *q, const void *k, const void *v, const float *g,
+                 const float *beta, float *S, int32_t n_slots, const int32_t *slots, void *o,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* A paged cache and the new tokens that meet it.  k_cache and v_cache hold n_pages pages of
+ * page_size tokens; entry e of head h, token j of page p is at p page_stride + j token_stride +
+ * h head_stride + e (elements, both caches alike, multiples of 16 bytes).  block_table
+ * [n_seqs, max_pages] gives each sequence's pages in order; entries behind its last page are not
+ * read.  kv_len [n_seqs] counts a sequence's cached tokens, its new ones among them:
+ * token i of L new ones is at position kv_len - L + i. */
+typedef struct {
+    int32_t n_seqs;
+    int32_t h_q, h_kv;         /* query heads, cache heads: h_q % h_kv == 0 */
+    int32_t d;                 /* head dim: 64, 128 or 256 */
+    int32_t dtype;             /* gdn_dtype of q, k, v, the caches and the outputs */
+    int32_t page_size, n_pages, max_pages;
+    int32_t max_kv_len;        /* no kv_len is larger (host copy), at most 2^30 */
+    int32_t rot_dim;           /* gdn_qk_norm_rope: entries that turn, a multiple of 16, <= d */
+    int32_t interleaved;       /* pairs (2 i, 2 i + 1) instead of (i, i + rot_dim / 2) */
+    int32_t norm;              /* 1: root-mean-square norm in front of the rotation */
+    int32_t max_pos;           /* rows of cos_sin */
+    float eps;                 /* of the norm */
+    float scale;               /* gdn_paged_attn: of the scores */
+    int64_t total_tokens;      /* new tokens: rows of q, k, v and the outputs */
+    int64_t q_stride, k_stride, v_stride, o_stride;
+    int64_t page_stride, token_stride, head_stride;
+} gdn_paged_desc;
+
+/* q_out = rot(q / rms(q) * q_weight), and k likewise and v as it is into the caches at the
+ * tokens' positions; rms(x)^2 = mean of x^2 over the head + eps, weights [d] fp32 (NULL: ones).
+ * cos_sin [max_pos, rot_dim] fp32: the rot_dim / 2 cosines, then sines, of a position; pair i
+ * turns (a, b) to (a cos - b sin, b cos + a sin).  positions (nullable) [T]: rotate by these
+ * instead of the place in the cache.  q_out may be q.  A token without a place in the cache, or a
+ * page or position out of range, sets the status bit; nothing is stored for it in the caches (nor
+ * in q_out for a bad position).  Tokens of one call have places of their own. */
+int32_t gdn_qk_norm_rope(const gdn_paged_desc *desc, const void *q, const void *k, const void *v,
+                         const float *q_weight, const float *k_weight, const float *cos_sin,
+                         const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *kv_len,
+                         const int32_t *positions, void *k_cache, void *v_cache, void *q_out,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of gdn_paged_attn's workspace: 256, and the parts of rows whose keys are split over
+ * workgroups (0 for a descriptor that is refused). */
+size_t gdn_paged_workspace_bytes(const gdn_paged_desc *desc);
+/* Each new token attends to the cached tokens at its position and before:
+ *     o = sum_j softmax_j(scale q . k_j) v_j,  lse = ln sum_j exp(scale q . k_j)  (nullable, [T, h_q] fp32),
+ * query head h with cache head floor(h h_kv / h_q).  A token in front of the cache's first one
+ * (kv_len < L) sees nothing: o = 0, lse = -inf.  A bad cu_seqlens, kv_len or page sets the status
+ * bit; the outputs of those sequences are unspecified.  bf16: products take q, k, v as they are,
+ * probabilities rounded to bf16 once, with fp32 scores, sums and outputs before the final rounding. */
+int32_t gdn_paged_attn(const gdn_paged_desc *desc, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *kv_len,
+                       void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
