@@ -84,6 +84,7 @@ struct AttnArgs {
 // How a call is cut: the host's choice from sizes alone, the same for the workspace query.
 struct AttnPlan {
     bool decode;
+    int32_t rows;               // rows of a workgroup
     int32_t splits, split_keys;
 };
 AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int32_t d, int32_t max_kv, int bf16);

@@ -69,7 +69,8 @@ __device__ __forceinline__ int64_t key_offset(const AttnArgs &a, const int32_t *
     return at;
 }
 
-// Q^T operands of 16 NB rows: row l % 16 of tile b, entries in the nat map.
+// Q^T operands of 16 NB rows: row l % 16 of tile b, entries in the nat map; negated for a negative
+// scale, which the kernels then take as a positive one.
 template <class M, int D, int NB>
 __device__ __forceinline__ void load_q(const AttnArgs &a, const Rows &r, int hk, int first, int lane,
                                        typename M::Frag (&q)[NB][D / 32])
@@ -81,44 +82,83 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, const Rows &r, int hk,
         const typename M::T *p = static_cast<const typename M::T *>(a.q) + (int64_t)(r.beg + mm / r.G) * a.qs +
                                  (int64_t)(hk * r.G + mm % r.G) * D;
 #pragma unroll
-        for (int kb = 0; kb < D / 32; ++kb) q[b][kb] = M::row_nat(p + 32 * kb, 0, lane);
+        for (int kb = 0; kb < D / 32; ++kb) {
+            q[b][kb] = M::row_nat(p + 32 * kb, 0, lane);
+            if (a.scale < 0.0f) {
+                float f[8];
+                M::to_floats(q[b][kb], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = -f[i];
+                q[b][kb] = M::from_floats(f);
+            }
+        }
     }
 }
 
-// One step of the running softmax over 32 keys (two accumulator tiles of 16) for one tile of 16
-// rows: scores to probabilities, O^T and the lane's share of l rescaled.
-template <class M, int D>
-__device__ __forceinline__ typename M::Frag soft_step(f32x4 (&st)[2], float scale, int32_t key0, int32_t limit, bool masked,
-                                                      float &m, float &l, f32x4 (&o)[D / 16])
-{
-    float s[8];
+// The running softmax of NB tiles of 16 rows, a step being 32 keys (two accumulator tiles of 16):
+// scores to probabilities exp2(s - base).  base is the row's maximum of some step, not always the
+// running one: it moves only when a score passes it by more than 8, so that probabilities stay
+// below 2^8 (their relative accuracy is the same there) and most steps neither exchange maxima
+// between lanes nor rescale O.
+template <int NB>
+struct Soft {
+    // -base, and the lane's share of the sum.  Before a row's first key base is lower than any score
+    // (-3e38): masked scores (-inf) still give 0, and the first key moves it.
+    float neg[NB], l[NB];
+    __device__ __forceinline__ Soft() {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float v = st[t][i] * scale;
-            s[4 * t + i] = masked && key0 + 16 * t + i >= limit ? -INFINITY : v;
-        }
-    float top = s[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float mn = fmaxf(m, top);
-    const float base = mn == -INFINITY ? 0.0f : mn;      // a row that has seen nothing yet
-    const float f = exp2f(m - base);
-    m = mn;
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        s[i] = exp2f(s[i] - base);
-        sum += s[i];
+        for (int b = 0; b < NB; ++b) { neg[b] = 3e38f; l[b] = 0.0f; }
     }
-    l = l * f + sum;
+    // The whole row's base (-inf if it has seen nothing) and sum.
+    __device__ __forceinline__ void whole(int b, float &m, float &sum) const {
+        sum = l[b] + __shfl_xor(l[b], 16);
+        sum += __shfl_xor(sum, 32);
+        m = sum > 0.0f ? -neg[b] : -INFINITY;
+    }
+    // scale > 0; the lane's keys are key0 + i and key0 + 16 + i, i = 0..3
+    template <class M, int D>
+    __device__ __forceinline__ void step(f32x4 (&st)[NB][2], float scale, int32_t key0, const int32_t (&limit)[NB],
+                                         bool masked, f32x4 (&o)[NB][D / 16], typename M::Frag (&p)[NB]) {
+        float top[NB], over = -INFINITY;
+        if (masked) {
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) o[d] *= f;
-    return M::from_floats(s);
-}
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st[b][t][i] = key0 + 16 * t + i >= limit[b] ? -INFINITY : st[b][t][i];
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            top[b] = fmaxf(fmaxf(fmaxf(st[b][0][0], st[b][0][1]), fmaxf(st[b][0][2], st[b][0][3])),
+                           fmaxf(fmaxf(st[b][1][0], st[b][1][1]), fmaxf(st[b][1][2], st[b][1][3])));
+            over = fmaxf(over, fmaf(top[b], scale, neg[b]));
+        }
+        if (__any(over > 8.0f)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float t = fmaxf(top[b], __shfl_xor(top[b], 16));
+                t = fmaxf(t, __shfl_xor(t, 32)) * scale;
+                const float base = fmaxf(t, -neg[b]);
+                const float f = exp2f(-neg[b] - base);   // 0 at the first key
+                neg[b] = -base;
+                l[b] *= f;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) o[b][d] *= f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float s[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[i] = __builtin_amdgcn_exp2f(fmaf(st[b][i >> 2][i & 3], scale, neg[b]));
+                l[b] += s[i];
+            }
+            p[b] = M::from_floats(s);
+        }
+    }
+};
 
 // The finished rows: normalised outputs, or a split's share.
 template <class M, int D>
@@ -174,16 +214,13 @@ __global__ void __launch_bounds__(NT) decode_kernel(AttnArgs a)
 #pragma unroll
     for (int b = 0; b < NB; ++b) limit[b] = row_limit(r, r.m0 + 16 * b + col);
     const int32_t least = row_limit(r, r.m0);
-    const float scale = a.scale * kLog2e;
-    float m[NB], l[NB];
+    const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // 0: every score is as good as 0
+    Soft<NB> sf;
     f32x4 o[NB][D / 16];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        m[b] = -INFINITY;
-        l[b] = 0.0f;
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[b][d] = f32x4{0, 0, 0, 0};
-    }
     constexpr int NV = KT * D / M::V / 64;
     for (int32_t k0 = k_beg + wave * KT; k0 < k_end; k0 += 4 * KT) {
         // V: rows to LDS, 16 bytes a lane
@@ -218,9 +255,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(AttnArgs a)
         }
         wave_sync();
         Frag p[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            p[b] = soft_step<M, D>(st[b], scale, k0 + 4 * g, limit[b], k0 + KT > least, m[b], l[b], o[b]);
+        sf.template step<M, D>(st, scale, k0 + 4 * g, limit, k0 + KT > least, o, p);
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
             const Frag vf = M::col_acc(Vs + 16 * d, SD, lane);
@@ -233,9 +268,9 @@ __global__ void __launch_bounds__(NT) decode_kernel(AttnArgs a)
     float *Os = reinterpret_cast<float *>(smem + wave * WB);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        l[b] += __shfl_xor(l[b], 16);
-        l[b] += __shfl_xor(l[b], 32);
-        if (g == 0) { sm[wave][16 * b + col] = m[b]; sl[wave][16 * b + col] = l[b]; }
+        float mx, l;
+        sf.whole(b, mx, l);
+        if (g == 0) { sm[wave][16 * b + col] = mx; sl[wave][16 * b + col] = l; }
 #pragma unroll
         for (int d = 0; d < D / 16; ++d)
             *reinterpret_cast<f32x4 *>(Os + (16 * b + col) * (D + 4) + 16 * d + 4 * g) = o[b][d];
@@ -260,16 +295,83 @@ __global__ void __launch_bounds__(NT) decode_kernel(AttnArgs a)
 }
 
 // ------------------------------------------------------------- many rows: waves over the rows
-template <class M, int D, int NB, int KT>
-__global__ void __launch_bounds__(NT) prefill_kernel(AttnArgs a)
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+// A tile of KT keys or values in LDS, rows of D elements without padding: 16-byte chunk c of row r
+// sits at chunk c ^ sw(r), so that the fragment reads spread over the banks.  It is filled by loads
+// that go from memory to LDS by themselves (64 lanes x 16 bytes in a row of LDS; the lane picks
+// its chunk's source).
+template <class M, int D>
+struct Tile {
+    typedef typename M::T T;
+    static constexpr int RB = D * sizeof(T), CPR = RB / 16;
+    // keys are read 16 rows at one chunk: the low four row bits
+    static __device__ __forceinline__ int sw_k(int r) { return r & (CPR < 16 ? CPR - 1 : 15); }
+    // values are read 4 rows at a time (lane group g, rows 4 g ..): bf16 2 chunks wide, fp32 4 wide
+    static __device__ __forceinline__ int sw_v(int r) {
+        return M::V == 8 ? (2 * r) & (CPR - 1) & 31 : (4 * ((r >> 2) & 3)) & (CPR - 1);
+    }
+    // The lane's part of the addresses; the rest of a fragment's address is an XOR of bits that the
+    // row does not reach and a constant.
+    static __device__ __forceinline__ uint32_t key_lane(int lane) {
+        const int r = lane & 15, g = lane >> 4;
+        return r * RB + 16 * ((M::V == 8 ? g : 2 * g) ^ sw_k(r));
+    }
+    static __device__ __forceinline__ uint32_t value_lane(int lane) {
+        const int g = lane >> 4, c = lane & 15, r = 4 * g + (M::V == 8 ? c >> 2 : 0);
+        return r * RB + (M::V == 8 ? 8 * (c & 3) : 4 * c) + 16 * sw_v(r);
+    }
+    // K, 32 entries from 32 kb of the 16 rows from 16 t: row l % 16, nat map
+    static __device__ __forceinline__ typename M::Frag key(const char *K, int t, int kb, uint32_t at) {
+        const char *p = K + 16 * t * RB;
+        if constexpr (M::V == 8) {
+            return __builtin_bit_cast(typename M::Frag, load16(p + (at ^ (64 * kb))));
+        } else {
+            typename M::Frag f;
+            M::unpack(load16(p + (at ^ (128 * kb))), f.x);
+            M::unpack(load16(p + (at ^ (128 * kb) ^ 16)), f.x + 4);
+            return f;
+        }
+    }
+    // V^T, entries 16 d + l % 16 of the 32 rows from k, acc map
+    static __device__ __forceinline__ typename M::Frag value(const char *Vt, int k, int d, uint32_t at) {
+        if constexpr (M::V == 8) {
+            const char *p = Vt + k * RB + (at ^ (32 * d));
+            return frag_of(read_tr(reinterpret_cast<const uint16_t *>(p)),
+                           read_tr(reinterpret_cast<const uint16_t *>(p + 16 * RB)));
+        } else {                                       // rows 4 g + j: one swizzle for all of them
+            typename M::Frag f;
+            const char *p = Vt + k * RB + (at ^ (64 * d));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f.x[j] = *reinterpret_cast<const float *>(p + ((j & 3) + 16 * (j >> 2)) * RB);
+            return f;
+        }
+    }
+};
+// The value, in a register of its own: what is computed from it in a loop stays in the loop instead
+// of being kept in registers over it.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// KT: keys of a tile.  Two tiles of K and V each: the next one comes in while this one is used, one
+// barrier a tile.
+template <class M, int D, int NB, int WAVES, int KT>
+__global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 {
     typedef typename M::T T;
     typedef typename M::Frag Frag;
-    constexpr int ROWS = 64 * NB, SD = D + M::PAD;
-    extern __shared__ __align__(16) char smem[];
-    T *Ks = reinterpret_cast<T *>(smem), *Vs = Ks + KT * SD;
-    __shared__ int64_t off[KT];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
+    typedef Tile<M, D> Tl;
+    constexpr bool FENCE = D == 256;
+    constexpr int ROWS = 16 * NB * WAVES, RB = Tl::RB, CPR = Tl::CPR;
+    constexpr int NI = KT * RB / 1024 / WAVES;           // 1 KB loads of a wave for one tile of K or V
+    static_assert(NI >= 1, "a tile has work for every wave");
+    __shared__ __align__(1024) char K0[KT * RB], V0[KT * RB], K1[KT * RB], V1[KT * RB];
+    __shared__ int64_t off[2][KT];                       // byte offsets of the keys' rows
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
     const int hk = blockIdx.x % a.h_kv;
     const int split = (blockIdx.x / a.h_kv) % a.splits;
@@ -281,9 +383,10 @@ __global__ void __launch_bounds__(NT) prefill_kernel(AttnArgs a)
     if (split > 0 && k_beg >= most) return;
     const int32_t k_end = most < k_beg + a.split_keys ? most : k_beg + a.split_keys;
     const int32_t *table = a.table + (int64_t)r.n * a.max_pages;
-    const T *kc = static_cast<const T *>(a.kc) + hk * a.head_stride;
-    const T *vc = static_cast<const T *>(a.vc) + hk * a.head_stride;
+    const char *kc = reinterpret_cast<const char *>(static_cast<const T *>(a.kc) + hk * a.head_stride);
+    const char *vc = reinterpret_cast<const char *>(static_cast<const T *>(a.vc) + hk * a.head_stride);
     const int first = wave * 16 * NB;
+    const uint32_t key_at = Tl::key_lane(lane), value_at = Tl::value_lane(lane);
 
     Frag q[NB][D / 32];
     load_q<M, D, NB>(a, r, hk, first, lane, q);
@@ -291,63 +394,101 @@ __global__ void __launch_bounds__(NT) prefill_kernel(AttnArgs a)
 #pragma unroll
     for (int b = 0; b < NB; ++b) limit[b] = row_limit(r, r.m0 + first + 16 * b + col);
     const int32_t least = row_limit(r, r.m0 + first);
-    const float scale = a.scale * kLog2e;
-    float m[NB], l[NB];
+    const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // 0: every score is as good as 0
+    Soft<NB> sf;
     f32x4 o[NB][D / 16];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        m[b] = -INFINITY;
-        l[b] = 0.0f;
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[b][d] = f32x4{0, 0, 0, 0};
-    }
-    constexpr int NV = KT * D / M::V / NT;
-    for (int32_t k0 = k_beg; k0 < k_end; k0 += KT) {
-        __syncthreads();                                 // the last tile's readers are done
-        if (threadIdx.x < KT) off[threadIdx.x] = key_offset(a, table, k0 + threadIdx.x, k_end);
-        __syncthreads();
+
+    const int nt = k_end > k_beg ? (k_end - k_beg + KT - 1) / KT : 0;
+    // The row of a key behind the end is the last key's (its score is masked), that of a bad page the
+    // first page's (recorded): every address is one of the cache's, and P = 0 meets numbers.
+    auto row_of = [&](int t) -> int64_t {
+        int32_t j = k_beg + t * KT + (int)threadIdx.x;
+        j = j < k_end ? j : k_end - 1;
+        bool bad = false;
+        const int64_t at = cache_offset(table, j, a.page_size, a.n_pages, a.page_stride, a.token_stride, bad);
+        if (bad) set_status(a.status);
+        return bad ? 0 : at * (int64_t)sizeof(T);
+    };
+    auto stage = [&](int t, char *Kb, char *Vb) {
+        const int ln = (int)here(lane);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (threadIdx.x + i * NT) * M::V;
-            const int64_t at = off[e / D];
-            store16(Ks + e / D * SD + e % D, at >= 0 ? load16(kc + at + e % D) : u32x4{0, 0, 0, 0});
-            store16(Vs + e / D * SD + e % D, at >= 0 ? load16(vc + at + e % D) : u32x4{0, 0, 0, 0});
+        for (int i = 0; i < NI; ++i) {
+            const int at = (wave * NI + i) * 64 + ln, row = at / CPR, pc = at % CPR;
+            const int64_t src = off[t & 1][row];
+            __builtin_amdgcn_global_load_lds((global_void *)(kc + src + 16 * (pc ^ Tl::sw_k(row))),
+                                             (lds_void *)(Kb + (wave * NI + i) * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((global_void *)(vc + src + 16 * (pc ^ Tl::sw_v(row))),
+                                             (lds_void *)(Vb + (wave * NI + i) * 1024), 16, 0, 0);
         }
-        __syncthreads();
+    };
+    auto compute = [&](int t, const char *Kb, const char *Vb) {
+        const int32_t k0 = k_beg + t * KT;
 #pragma unroll
         for (int k = 0; k < KT; k += 32) {
+            const uint32_t ka = here(key_at), va = here(value_at);
             f32x4 st[NB][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) st[b][t] = f32x4{0, 0, 0, 0};
+                for (int b = 0; b < NB; ++b) st[b][h] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int kb = 0; kb < D / 32; ++kb) {
-                    const Frag kf = M::row_nat(Ks + (k + 16 * t) * SD + 32 * kb, SD, lane);
+                    const Frag kf = Tl::key(Kb, k / 16 + h, kb, ka);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) st[b][t] = M::mma(st[b][t], kf, q[b][kb]);
+                    for (int b = 0; b < NB; ++b) st[b][h] = M::mma(st[b][h], kf, q[b][kb]);
+                    if (FENCE && kb % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
             Frag p[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-                p[b] = soft_step<M, D>(st[b], scale, k0 + k + 4 * g, limit[b], k0 + k + 32 > least, m[b], l[b], o[b]);
+            sf.template step<M, D>(st, scale, k0 + k + 4 * g, limit, k0 + k + 32 > least, o, p);
+            if (FENCE) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
-                const Frag vf = M::col_acc(Vs + k * SD + 16 * d, SD, lane);
+                const Frag vf = Tl::value(Vb, k, d, va);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], vf, p[b]);
+                if (FENCE && d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
+        }
+    };
+    auto turn = [&](int t, char *Kb, char *Vb, char *Kn, char *Vn) {
+        __syncthreads();                                 // this tile is here, the other buffer is free
+        const bool ahead = t + 2 < nt && threadIdx.x < KT;
+        int64_t row = 0;
+        if (ahead) row = row_of(t + 2);
+        if (t + 1 < nt) stage(t + 1, Kn, Vn);
+        if (FENCE) __builtin_amdgcn_sched_barrier(0);
+        compute(t, Kb, Vb);
+        if (ahead) off[t & 1][threadIdx.x] = row;
+    };
+    if (nt > 0) {
+        if (a.n_pages == 0) {                            // no page at all: nothing can be read
+            if (threadIdx.x == 0) set_status(a.status);
+            return;
+        }
+        if (threadIdx.x < KT) {
+            off[0][threadIdx.x] = row_of(0);
+            if (nt > 1) off[1][threadIdx.x] = row_of(1);
+        }
+        __syncthreads();
+        stage(0, K0, V0);
+        for (int t = 0; t < nt; t += 2) {
+            turn(t, K0, V0, K1, V1);
+            if (t + 1 < nt) turn(t + 1, K1, V1, K0, V0);
         }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        l[b] += __shfl_xor(l[b], 16);
-        l[b] += __shfl_xor(l[b], 32);
+        float mx, l;
+        sf.whole(b, mx, l);
         const int row = first + 16 * b + col;
         if (row >= r.count) continue;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) store_share<M, D>(a, r, hk, split, row, 16 * d + 4 * g, o[b][d], m[b], l[b]);
+        for (int d = 0; d < D / 16; ++d) store_share<M, D>(a, r, hk, split, row, 16 * d + 4 * g, o[b][d], mx, l);
     }
 }
 
@@ -397,7 +538,7 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
 }
 
 template <class K>
-hipError_t start(K k, int64_t blocks, int lds, const AttnArgs &a, hipStream_t stream)
+hipError_t start(K k, int64_t blocks, int lds, const AttnArgs &a, hipStream_t stream, int threads = NT)
 {
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     if (blocks <= 0) return hipSuccess;
@@ -405,7 +546,7 @@ hipError_t start(K k, int64_t blocks, int lds, const AttnArgs &a, hipStream_t st
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(NT), lds, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(threads), lds, stream, a);
     return hipGetLastError();
 }
 
@@ -420,9 +561,13 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
         const int64_t blocks = (a.total * G / 16 + a.n_seqs) * a.splits * a.h_kv;
         e = start(decode_kernel<M, D, 1>, blocks, 4 * (VW > OW ? VW : OW), a, stream);
     } else {
-        constexpr int NB = 2, KT = M::V == 8 ? 64 : 32;
-        const int64_t blocks = (a.total * G / (64 * NB) + a.n_seqs) * a.splits * a.h_kv;
-        e = start(prefill_kernel<M, D, NB, KT>, blocks, 2 * KT * SD * (int)sizeof(typename M::T), a, stream);
+        // fp32 rows of 256 entries: the operands and sums of 16 rows fill a wave's registers
+        constexpr bool WIDE = D * sizeof(typename M::T) > 512;
+        constexpr int NB = WIDE ? 1 : 2, KT = WIDE ? 32 : 64;
+        const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
+        if constexpr (WIDE) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, 0, a, stream, 512);
+        else if (p.rows == 256) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, 0, a, stream, 512);
+        else e = start(prefill_kernel<M, D, NB, 4, KT>, blocks, 0, a, stream, 256);
     }
     if (e != hipSuccess || a.splits == 1) return e;
     return start(join_kernel<M, D>, (a.total * a.h_q + 3) / 4, 0, a, stream);
@@ -446,9 +591,9 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     const int64_t G = h_q / h_kv;
     AttnPlan p;
     p.decode = total * G <= 32 * (int64_t)n_seqs;
-    const int rows = p.decode ? 16 : 128;
-    const int64_t tiles = (total * G / rows + n_seqs) * h_kv;
-    int64_t want = (p.decode ? 1024 : 512) / (tiles > 0 ? tiles : 1);
+    p.rows = p.decode ? 16 : bf16 && total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
+    const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
+    int64_t want = (p.decode ? 1024 : 256 * (256 / p.rows)) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;
     int64_t keys = (max_kv + want - 1) / want;
     const int64_t least = p.decode ? 128 : 1024;
@@ -456,7 +601,6 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     p.split_keys = (int32_t)((keys + 127) / 128 * 128);
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
     (void)d;
-    (void)bf16;
     return p;
 }
 
