@@ -25,17 +25,19 @@ GDN_HD bool kv_ok(int32_t kv, int32_t max_kv, int32_t page_size, int32_t max_pag
     return kv >= 0 && kv <= max_kv && ((int64_t)kv + page_size - 1) / page_size <= max_pages;
 }
 
-// Element offset of cached token j in the caches (head 0), or -1 with `bad` set where the block
-// table names no page.  j is in [0, kv) of a kv that passed kv_ok, so the table is read in bounds.
-GDN_HD int64_t cache_offset(const int32_t *table, int32_t j, int32_t page_size, int32_t n_pages, int64_t page_stride,
-                            int64_t token_stride, bool &bad) {
-    const int32_t p = j / page_size;
-    const int32_t page = table[p];
+// Element offset of a page's token in the caches (head 0), or -1 with `bad` set for no page.
+GDN_HD int64_t page_offset(int32_t page, int32_t token, int32_t n_pages, int64_t page_stride, int64_t token_stride, bool &bad) {
     if (page < 0 || page >= n_pages) {
         bad = true;
         return -1;
     }
-    return (int64_t)page * page_stride + (int64_t)(j - p * page_size) * token_stride;
+    return (int64_t)page * page_stride + (int64_t)token * token_stride;
+}
+// The same for cached token j of a sequence.  j is in [0, kv) of a kv that passed kv_ok, so the
+// block table is read in bounds.
+GDN_HD int64_t cache_offset(const int32_t *table, int32_t j, int32_t page_size, int32_t n_pages, int64_t page_stride,
+                            int64_t token_stride, bool &bad) {
+    return page_offset(table[j / page_size], j % page_size, n_pages, page_stride, token_stride, bad);
 }
 
 }  // namespace gdn

@@ -19,8 +19,8 @@
 // the matrix products; the waves take different rows and share the keys' tiles in LDS.
 //
 // Precision: scores, maximum, sum, O are fp32.  With bf16 elements the products take q, k and v as
-// they are, and P (0 <= P <= 1) is rounded to bf16 once, half a bf16 step as the output is; the sum
-// l takes the unrounded P.  Keys behind kv_len are never read: whatever a page holds there (or an
+// they are; P is rounded to bf16 once where the products are the bound (half a bf16 step, as the
+// output is), and taken in two bf16 terms where memory is.  The sum l takes the unrounded P.  Keys behind kv_len are never read: whatever a page holds there (or an
 // unused page) does not matter.
 #include "gdn_mfma.h"
 
@@ -59,14 +59,26 @@ __device__ __forceinline__ bool find_rows(const AttnArgs &a, int64_t tile, int r
 // Keys that row m sees: its position + 1 (0 or less: none).
 __device__ __forceinline__ int32_t row_limit(const Rows &r, int32_t m) { return r.pos0 + m / r.G + 1; }
 
-// Element offset of key j's row in the caches (head 0), or -1 behind `end` or for a bad page.
-__device__ __forceinline__ int64_t key_offset(const AttnArgs &a, const int32_t *table, int32_t j, int32_t end)
+// Where key j of a sequence is, in two steps, so that the block table's entry can be on its way while
+// other work goes on: the entry, and the byte offset of the key's row in the caches (head 0).  A key
+// behind the end stands for the last one (its score is masked), one of a bad page for the first
+// page's first (recorded): every address is one of the cache's, and P = 0 meets numbers.
+struct Key {
+    int32_t j, page;
+};
+__device__ __forceinline__ Key find_key(const AttnArgs &a, const int32_t *table, int32_t j, int32_t end)
 {
-    if (j >= end) return -1;
+    Key k;
+    k.j = j < end ? j : end - 1;
+    k.page = table[k.j / a.page_size];
+    return k;
+}
+__device__ __forceinline__ int64_t key_row(const AttnArgs &a, const Key &k, int elem_bytes)
+{
     bool bad = false;
-    const int64_t at = cache_offset(table, j, a.page_size, a.n_pages, a.page_stride, a.token_stride, bad);
+    const int64_t at = page_offset(k.page, k.j % a.page_size, a.n_pages, a.page_stride, a.token_stride, bad);
     if (bad) set_status(a.status);
-    return at;
+    return bad ? 0 : at * elem_bytes;
 }
 
 // Q^T operands of 16 NB rows: row l % 16 of tile b, entries in the nat map; negated for a negative
@@ -82,17 +94,19 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, const Rows &r, int hk,
         const typename M::T *p = static_cast<const typename M::T *>(a.q) + (int64_t)(r.beg + mm / r.G) * a.qs +
                                  (int64_t)(hk * r.G + mm % r.G) * D;
 #pragma unroll
-        for (int kb = 0; kb < D / 32; ++kb) {
-            q[b][kb] = M::row_nat(p + 32 * kb, 0, lane);
-            if (a.scale < 0.0f) {
+        for (int kb = 0; kb < D / 32; ++kb) q[b][kb] = M::row_nat(p + 32 * kb, 0, lane);
+    }
+    if (a.scale < 0.0f)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int kb = 0; kb < D / 32; ++kb) {
                 float f[8];
                 M::to_floats(q[b][kb], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = -f[i];
                 q[b][kb] = M::from_floats(f);
             }
-        }
-    }
 }
 
 // The running softmax of NB tiles of 16 rows, a step being 32 keys (two accumulator tiles of 16):
@@ -116,9 +130,10 @@ struct Soft {
         m = sum > 0.0f ? -neg[b] : -INFINITY;
     }
     // scale > 0; the lane's keys are key0 + i and key0 + 16 + i, i = 0..3
-    template <class M, int D>
+    // TERMS: P in that many terms of the element type (two bf16 terms hold 16 bits)
+    template <class M, int D, int TERMS>
     __device__ __forceinline__ void step(f32x4 (&st)[NB][2], float scale, int32_t key0, const int32_t (&limit)[NB],
-                                         bool masked, f32x4 (&o)[NB][D / 16], typename M::Frag (&p)[NB]) {
+                                         bool masked, f32x4 (&o)[NB][D / 16], typename M::Frag (&p)[NB][TERMS]) {
         float top[NB], over = -INFINITY;
         if (masked) {
 #pragma unroll
@@ -155,7 +170,16 @@ struct Soft {
                 s[i] = __builtin_amdgcn_exp2f(fmaf(st[b][i >> 2][i & 3], scale, neg[b]));
                 l[b] += s[i];
             }
-            p[b] = M::from_floats(s);
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) {
+                p[b][t] = M::from_floats(s);
+                if (t + 1 < TERMS) {
+                    float got[8];
+                    M::to_floats(p[b][t], got);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[i] -= got[i];
+                }
+            }
         }
     }
 };
@@ -181,120 +205,7 @@ __device__ __forceinline__ void store_share(const AttnArgs &a, const Rows &r, in
     if (d4 == 0) *reinterpret_cast<f32x2 *>(a.part_ml + at * 2) = f32x2{mx, l};
 }
 
-// ------------------------------------------------------------- few rows: waves over the keys
-template <class M, int D, int NB>
-__global__ void __launch_bounds__(NT) decode_kernel(AttnArgs a)
-{
-    typedef typename M::T T;
-    typedef typename M::Frag Frag;
-    constexpr int ROWS = 16 * NB, SD = D + M::PAD, KT = 32;
-    constexpr int VW = KT * SD * sizeof(T), OW = ROWS * (D + 4) * 4;
-    constexpr int WB = VW > OW ? VW : OW;                // a wave's LDS: its V tile, later its O
-    extern __shared__ __align__(16) char smem[];
-    __shared__ float sm[4][ROWS], sl[4][ROWS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
-    if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
-    const int hk = blockIdx.x % a.h_kv;
-    const int split = (blockIdx.x / a.h_kv) % a.splits;
-    const int64_t tile = blockIdx.x / a.h_kv / a.splits;
-    Rows r;
-    if (!find_rows(a, tile, ROWS, r)) return;
-    const int32_t most = row_limit(r, r.m0 + r.count - 1);        // keys that the tile's last row sees
-    const int32_t k_beg = split * a.split_keys;
-    if (split > 0 && k_beg >= most) return;                       // nothing here for any row
-    const int32_t k_end = most < k_beg + a.split_keys ? most : k_beg + a.split_keys;
-    const int32_t *table = a.table + (int64_t)r.n * a.max_pages;
-    const T *kc = static_cast<const T *>(a.kc) + hk * a.head_stride;
-    const T *vc = static_cast<const T *>(a.vc) + hk * a.head_stride;
-    T *Vs = reinterpret_cast<T *>(smem + wave * WB);
-
-    Frag q[NB][D / 32];
-    load_q<M, D, NB>(a, r, hk, 0, lane, q);
-    int32_t limit[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) limit[b] = row_limit(r, r.m0 + 16 * b + col);
-    const int32_t least = row_limit(r, r.m0);
-    const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // 0: every score is as good as 0
-    Soft<NB> sf;
-    f32x4 o[NB][D / 16];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[b][d] = f32x4{0, 0, 0, 0};
-    constexpr int NV = KT * D / M::V / 64;
-    for (int32_t k0 = k_beg + wave * KT; k0 < k_end; k0 += 4 * KT) {
-        // V: rows to LDS, 16 bytes a lane
-        u32x4 rv[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (lane + i * 64) * M::V;
-            const int64_t at = key_offset(a, table, k0 + e / D, k_end);
-            rv[i] = at >= 0 ? load16(vc + at + e % D) : u32x4{0, 0, 0, 0};
-        }
-        f32x4 st[NB][2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int64_t at = key_offset(a, table, k0 + 16 * t + col, k_end);
-            Frag kf[D / 32];
-#pragma unroll
-            for (int kb = 0; kb < D / 32; ++kb) {
-                if (at >= 0) kf[kb] = M::row_nat(kc + at + 32 * kb, 0, lane);
-                else kf[kb] = Frag{};
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                st[b][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int kb = 0; kb < D / 32; ++kb) st[b][t] = M::mma(st[b][t], kf[kb], q[b][kb]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (lane + i * 64) * M::V;
-            store16(Vs + e / D * SD + e % D, rv[i]);
-        }
-        wave_sync();
-        Frag p[NB];
-        sf.template step<M, D>(st, scale, k0 + 4 * g, limit, k0 + KT > least, o, p);
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-            const Frag vf = M::col_acc(Vs + 16 * d, SD, lane);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], vf, p[b]);
-        }
-        wave_sync();
-    }
-    // join the waves: every wave's (m, l, O) to LDS, then one thread per four entries of a row
-    float *Os = reinterpret_cast<float *>(smem + wave * WB);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        float mx, l;
-        sf.whole(b, mx, l);
-        if (g == 0) { sm[wave][16 * b + col] = mx; sl[wave][16 * b + col] = l; }
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-            *reinterpret_cast<f32x4 *>(Os + (16 * b + col) * (D + 4) + 16 * d + 4 * g) = o[b][d];
-    }
-    __syncthreads();
-    for (int e = threadIdx.x * 4; e < r.count * D; e += NT * 4) {
-        const int row = e / D, d4 = e % D;
-        float mx = sm[0][row];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) mx = fmaxf(mx, sm[w][row]);
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        f32x4 sum = {0, 0, 0, 0};
-        float ll = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float f = exp2f(sm[w][row] - base);
-            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(smem + w * WB) + row * (D + 4) + d4) * f;
-            ll += sl[w][row] * f;
-        }
-        store_share<M, D>(a, r, hk, split, row, d4, sum, mx, ll);
-    }
-}
-
-// ------------------------------------------------------------- many rows: waves over the rows
+// ------------------------------------------------------------- tiles of keys and values in LDS
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void global_void;
 
@@ -356,6 +267,179 @@ __device__ __forceinline__ uint32_t here(uint32_t v) {
     return v;
 }
 
+// Waits until at most N of the wave's last loads are on their way (they return in order), and until
+// all its LDS reads are done.  The compiler counts with these builtins, and no access moves over them.
+__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    fence();
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+    fence();
+}
+__device__ __forceinline__ void wait_reads() {
+    fence();
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+    fence();
+}
+
+// ------------------------------------------------------------- few rows: waves over the keys
+// Waves of a workgroup: two workgroups' tiles fit the LDS of a CU, so that one's first loads and
+// last sums overlap with the other's keys.
+template <class M, int D>
+constexpr int decode_waves() { return Tile<M, D>::RB >= 1024 ? 1 : Tile<M, D>::RB >= 512 ? 2 : 4; }
+
+// A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
+// from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
+template <class M, int D, int NB, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) decode_kernel(AttnArgs a)
+{
+    typedef typename M::T T;
+    typedef typename M::Frag Frag;
+    typedef Tile<M, D> Tl;
+    constexpr int ROWS = 16 * NB, KT = 32, RB = Tl::RB, CPR = Tl::CPR;
+    constexpr int NI = KT * RB / 1024;                   // 1 KB loads of one tile
+    static_assert(ROWS * D * 4 <= KT * RB, "the join's O fits where the keys were");
+    __shared__ __align__(1024) char Ks[WAVES][KT * RB], Vs[WAVES][KT * RB];
+    __shared__ int64_t off[WAVES][2][KT];
+    __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS];
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
+    const int hk = blockIdx.x % a.h_kv;
+    const int split = (blockIdx.x / a.h_kv) % a.splits;
+    const int64_t tile = blockIdx.x / a.h_kv / a.splits;
+    Rows r;
+    if (!find_rows(a, tile, ROWS, r)) return;
+    const int32_t most = row_limit(r, r.m0 + r.count - 1);        // keys that the tile's last row sees
+    const int32_t k_beg = split * a.split_keys;
+    if (split > 0 && k_beg >= most) return;                       // nothing here for any row
+    const int32_t k_end = most < k_beg + a.split_keys ? most : k_beg + a.split_keys;
+    const int32_t *table = a.table + (int64_t)r.n * a.max_pages;
+    const char *kc = reinterpret_cast<const char *>(static_cast<const T *>(a.kc) + hk * a.head_stride);
+    const char *vc = reinterpret_cast<const char *>(static_cast<const T *>(a.vc) + hk * a.head_stride);
+    if (most > 0 && a.n_pages == 0) {
+        if (threadIdx.x == 0) set_status(a.status);
+        return;
+    }
+    char *Kw = Ks[wave], *Vw = Vs[wave];
+    const uint32_t key_at = Tl::key_lane(lane), value_at = Tl::value_lane(lane);
+    const int nt = k_end > k_beg ? (k_end - k_beg + KT - 1) / KT : 0;
+
+    auto key_of = [&](int t) { return find_key(a, table, k_beg + t * KT + (lane & 31), k_end); };
+    // (the fences keep the loads in this order: the counts that are waited for below rely on it)
+    auto fetch_k = [&](int slot) {
+        fence();
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int at = i * 64 + lane, row = at / CPR, pc = at % CPR;
+            __builtin_amdgcn_global_load_lds((global_void *)(kc + off[wave][slot][row] + 16 * (pc ^ Tl::sw_k(row))),
+                                             (lds_void *)(Kw + i * 1024), 16, 0, 0);
+        }
+    };
+    auto fetch_v = [&](int slot) {
+        fence();
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int at = i * 64 + lane, row = at / CPR, pc = at % CPR;
+            __builtin_amdgcn_global_load_lds((global_void *)(vc + off[wave][slot][row] + 16 * (pc ^ Tl::sw_v(row))),
+                                             (lds_void *)(Vw + i * 1024), 16, 0, 0);
+        }
+    };
+    Key now = {0, 0}, next = {0, 0};
+    if (nt > 0) {
+        now = key_of(wave);
+        next = key_of(wave + WAVES);
+    }
+    Frag q[NB][D / 32];
+    load_q<M, D, NB>(a, r, hk, 0, lane, q);
+    if (wave < nt) {
+        if (lane < KT) off[wave][0][lane] = key_row(a, now, sizeof(T));
+        wave_sync();
+        fetch_k(0);
+        fetch_v(0);
+        wait_loads<(2 * NI < 63 ? 2 * NI : 63)>();       // what is in registers is here
+    }
+    int32_t limit[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) limit[b] = row_limit(r, r.m0 + 16 * b + col);
+    const int32_t least = row_limit(r, r.m0);
+    const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // 0: every score is as good as 0
+    Soft<NB> sf;
+    f32x4 o[NB][D / 16];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[b][d] = f32x4{0, 0, 0, 0};
+
+    for (int t = wave, slot = 1; t < nt; t += WAVES, slot ^= 1) {
+        const bool more = t + WAVES < nt;
+        if (lane < KT) off[wave][slot][lane] = key_row(a, next, sizeof(T));
+        wave_sync();
+        wait_loads<NI>();                                // K is here; V, the last NI loads, may not be
+        next = key_of(t + 2 * WAVES);
+        f32x4 st[NB][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) st[b][h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < D / 32; ++kb) {
+                const Frag kf = Tl::key(Kw, h, kb, key_at);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) st[b][h] = M::mma(st[b][h], kf, q[b][kb]);
+            }
+        }
+        wait_reads();                                    // K is read: its place may be filled
+        if (more) fetch_k(slot);
+        constexpr int TERMS = M::V == 8 ? 2 : 1;         // the products wait for memory: P costs nothing more
+        Frag p[NB][TERMS];
+        sf.template step<M, D, TERMS>(st, scale, k_beg + t * KT + 4 * g, limit, k_beg + t * KT + KT > least, o, p);
+        if (more) wait_loads<NI + 1>();                  // V is here; `next` and the new K may not be
+        else wait_loads<0>();
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const Frag vf = Tl::value(Vw, 0, d, value_at);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int term = TERMS - 1; term >= 0; --term) o[b][d] = M::mma(o[b][d], vf, p[b][term]);
+        }
+        wait_reads();
+        if (more) fetch_v(slot);
+    }
+    // join the waves: every wave's (m, l, O) to LDS, then one thread per four entries of a row
+    // (16-byte piece c of a row sits at c ^ row: the sixteen rows that a wave writes at once are
+    // then in different banks)
+    float *Os = reinterpret_cast<float *>(Kw);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float mx, l;
+        sf.whole(b, mx, l);
+        if (g == 0) { sm[wave][16 * b + col] = mx; sl[wave][16 * b + col] = l; }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+            *reinterpret_cast<f32x4 *>(Os + (16 * b + col) * D + 4 * ((4 * d + g) ^ col)) = o[b][d];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < r.count * D; e += 64 * WAVES * 4) {
+        const int row = e / D, d4 = e % D;
+        float mx = sm[0][row];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, sm[w][row]);
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        f32x4 sum = {0, 0, 0, 0};
+        float ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float f = exp2f(sm[w][row] - base);
+            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(Ks[w]) + row * D + 4 * ((d4 / 4) ^ (row & 15))) * f;
+            ll += sl[w][row] * f;
+        }
+        store_share<M, D>(a, r, hk, split, row, d4, sum, mx, ll);
+    }
+}
+
+// ------------------------------------------------------------- many rows: waves over the rows
 // KT: keys of a tile.  Two tiles of K and V each: the next one comes in while this one is used, one
 // barrier a tile.
 template <class M, int D, int NB, int WAVES, int KT>
@@ -403,16 +487,7 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
         for (int d = 0; d < D / 16; ++d) o[b][d] = f32x4{0, 0, 0, 0};
 
     const int nt = k_end > k_beg ? (k_end - k_beg + KT - 1) / KT : 0;
-    // The row of a key behind the end is the last key's (its score is masked), that of a bad page the
-    // first page's (recorded): every address is one of the cache's, and P = 0 meets numbers.
-    auto row_of = [&](int t) -> int64_t {
-        int32_t j = k_beg + t * KT + (int)threadIdx.x;
-        j = j < k_end ? j : k_end - 1;
-        bool bad = false;
-        const int64_t at = cache_offset(table, j, a.page_size, a.n_pages, a.page_stride, a.token_stride, bad);
-        if (bad) set_status(a.status);
-        return bad ? 0 : at * (int64_t)sizeof(T);
-    };
+    auto key_of = [&](int t) { return find_key(a, table, k_beg + t * KT + (int)threadIdx.x, k_end); };
     auto stage = [&](int t, char *Kb, char *Vb) {
         const int ln = (int)here(lane);
 #pragma unroll
@@ -443,14 +518,14 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
                     if (FENCE && kb % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            Frag p[NB];
-            sf.template step<M, D>(st, scale, k0 + k + 4 * g, limit, k0 + k + 32 > least, o, p);
+            Frag p[NB][1];
+            sf.template step<M, D, 1>(st, scale, k0 + k + 4 * g, limit, k0 + k + 32 > least, o, p);
             if (FENCE) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 const Frag vf = Tl::value(Vb, k, d, va);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], vf, p[b]);
+                for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], vf, p[b][0]);
                 if (FENCE && d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -458,12 +533,13 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
     auto turn = [&](int t, char *Kb, char *Vb, char *Kn, char *Vn) {
         __syncthreads();                                 // this tile is here, the other buffer is free
         const bool ahead = t + 2 < nt && threadIdx.x < KT;
-        int64_t row = 0;
-        if (ahead) row = row_of(t + 2);
+        Key key = {0, 0};
+        if (ahead) key = key_of(t + 2);
+        fence();
         if (t + 1 < nt) stage(t + 1, Kn, Vn);
         if (FENCE) __builtin_amdgcn_sched_barrier(0);
         compute(t, Kb, Vb);
-        if (ahead) off[t & 1][threadIdx.x] = row;
+        if (ahead) off[t & 1][threadIdx.x] = key_row(a, key, sizeof(T));
     };
     if (nt > 0) {
         if (a.n_pages == 0) {                            // no page at all: nothing can be read
@@ -471,8 +547,8 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
             return;
         }
         if (threadIdx.x < KT) {
-            off[0][threadIdx.x] = row_of(0);
-            if (nt > 1) off[1][threadIdx.x] = row_of(1);
+            off[0][threadIdx.x] = key_row(a, key_of(0), sizeof(T));
+            if (nt > 1) off[1][threadIdx.x] = key_row(a, key_of(1), sizeof(T));
         }
         __syncthreads();
         stage(0, K0, V0);
@@ -493,16 +569,17 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 }
 
 // ------------------------------------------------------------- the splits of a row, joined
-// One wave per row: the splits that hold keys of the row, in order.
+// One workgroup per row: 256 / (D / 4) slices of the row's splits, four entries a thread; the slices
+// meet in LDS, in order.
 template <class M, int D>
 __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
 {
     typedef typename M::T T;
-    constexpr int E = D / 64;                            // entries of a lane
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
-    if (row >= a.total * a.h_q) return;
-    const int64_t t = row / a.h_q;
+    constexpr int C = D / 4, SL = NT / C, MOST = 256;    // MOST: weights held in LDS at a time
+    __shared__ float w[MOST];
+    __shared__ __align__(16) f32x4 part[SL][C];
+    __shared__ float lpart[NT / 64];
+    const int64_t row = blockIdx.x, t = row / a.h_q;
     const int n = token_sequence(a.cu, a.n_seqs, t);
     const int32_t b = a.cu[n], e = a.cu[n + 1];
     if (!range_ok(b, e, a.total) || t < b || t >= e) return;
@@ -511,66 +588,76 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
     const int32_t limit = kv - (e - (int32_t)t) + 1;
     const int act = limit > 0 ? (limit + a.split_keys - 1) / a.split_keys : 1;
     const int64_t step = a.total * a.h_q;
-    float mx = -INFINITY;
+    const int lane = threadIdx.x & 63, c = threadIdx.x % C, slice = threadIdx.x / C;
+    float mx = -INFINITY;                                // every wave for itself
     for (int s = lane; s < act; s += 64) mx = fmaxf(mx, a.part_ml[(s * step + row) * 2]);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
     const float base = mx == -INFINITY ? 0.0f : mx;
-    float l = 0.0f, acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-    for (int s = 0; s < act; ++s) {
-        const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.part_ml + (s * step + row) * 2);
-        const float f = exp2f(ml.x - base);
-        l += ml.y * f;
-        const float *p = a.part_o + (s * step + row) * D + lane * E;
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = fmaf(p[i], f, acc[i]);
+    float l = 0.0f;
+    f32x4 acc = {0, 0, 0, 0};
+    for (int s0 = 0; s0 < act; s0 += MOST) {
+        const int some = act - s0 < MOST ? act - s0 : MOST;
+        if (s0 > 0) __syncthreads();
+        if ((int)threadIdx.x < some) {
+            const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.part_ml + ((s0 + threadIdx.x) * step + row) * 2);
+            const float f = exp2f(ml.x - base);
+            w[threadIdx.x] = f;
+            l += ml.y * f;
+        }
+        __syncthreads();
+        const float *p = a.part_o + (s0 * step + row) * D + 4 * c;
+#pragma unroll 4
+        for (int s = slice; s < some; s += SL) acc += *reinterpret_cast<const f32x4 *>(p + s * step * D) * w[s];
     }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off);
+    if (lane == 0) lpart[threadIdx.x >> 6] = l;
+    part[slice][c] = acc;
+    __syncthreads();
+    if (slice > 0) return;
+#pragma unroll
+    for (int s = 1; s < SL; ++s) acc += part[s][c];
+    l = lpart[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) l += lpart[i];
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    T *o = static_cast<T *>(a.o) + t * a.os + (row % a.h_q) * D + lane * E;
+    float x[4];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        if constexpr (M::V == 8) o[i] = (uint16_t)pack_bf16(acc[i] * inv, 0.0f);
-        else o[i] = acc[i] * inv;
-    }
-    if (a.lse && lane == 0) a.lse[row] = l > 0.0f ? mx * kLn2 + logf(l) : -INFINITY;
+    for (int i = 0; i < 4; ++i) x[i] = acc[i] * inv;
+    M::store4(static_cast<T *>(a.o) + t * a.os + (row % a.h_q) * D + 4 * c, x);
+    if (a.lse && c == 0) a.lse[row] = l > 0.0f ? mx * kLn2 + logf(l) : -INFINITY;
 }
 
 template <class K>
-hipError_t start(K k, int64_t blocks, int lds, const AttnArgs &a, hipStream_t stream, int threads = NT)
+hipError_t start(K k, int64_t blocks, const AttnArgs &a, hipStream_t stream, int threads)
 {
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     if (blocks <= 0) return hipSuccess;
-    if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(threads), lds, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
 }
 
 template <class M, int D>
 hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
-    constexpr int SD = D + M::PAD;
     const int G = a.h_q / a.h_kv;
     hipError_t e;
     if (p.decode) {
-        constexpr int VW = 32 * SD * sizeof(typename M::T), OW = 16 * (D + 4) * 4;
         const int64_t blocks = (a.total * G / 16 + a.n_seqs) * a.splits * a.h_kv;
-        e = start(decode_kernel<M, D, 1>, blocks, 4 * (VW > OW ? VW : OW), a, stream);
+        constexpr int WAVES = decode_waves<M, D>();
+        e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
     } else {
         // fp32 rows of 256 entries: the operands and sums of 16 rows fill a wave's registers
         constexpr bool WIDE = D * sizeof(typename M::T) > 512;
         constexpr int NB = WIDE ? 1 : 2, KT = WIDE ? 32 : 64;
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
-        if constexpr (WIDE) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, 0, a, stream, 512);
-        else if (p.rows == 256) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, 0, a, stream, 512);
-        else e = start(prefill_kernel<M, D, NB, 4, KT>, blocks, 0, a, stream, 256);
+        if constexpr (WIDE) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, a, stream, 512);
+        else if (p.rows == 256) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, a, stream, 512);
+        else e = start(prefill_kernel<M, D, NB, 4, KT>, blocks, a, stream, 256);
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    return start(join_kernel<M, D>, (a.total * a.h_q + 3) / 4, 0, a, stream);
+    return start(join_kernel<M, D>, a.total * a.h_q, a, stream, NT);
 }
 
 template <class M>
