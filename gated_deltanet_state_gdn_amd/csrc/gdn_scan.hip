@@ -11,9 +11,9 @@
 // stretch of tokens, formed as differences of a 64-bit running sum kept as two floats: strong
 // decays in front of weak ones cost the weak ones nothing.
 //
-// Work decomposition: a workgroup of four waves takes HB heads of one group over one segment of
-// one sequence, chunk by chunk.  The columns of S (d_v of every head) do not mix, so a wave owns
-// some 16-column tiles of S whole, in its accumulators; M is the only product the waves share, and
+// Work decomposition: a workgroup takes HB heads of one group over one segment of one sequence,
+// chunk by chunk.  The columns of S (d_v of every head) do not mix, so every wave owns a 16-column
+// tile of S whole, in its accumulators; M is the only product the waves share, and
 // goes through LDS.  Y is formed transposed (Y^T = S^T C^T + X^T M^T): accumulators of S become
 // operands where they are, and a lane ends with four consecutive entries of one token's y.
 //
@@ -69,6 +69,37 @@ __device__ __forceinline__ int chunks_per_segment(int64_t len, int segs) {
     return (int)((c + segs - 1) / segs);
 }
 
+// Inclusive sum over the lanes of a wave, by lane-shift operands (no LDS): within rows of 16 lanes,
+// then the rows' last lanes into the rows behind.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);    // 0.0 where there is no such lane
+}
+__device__ __forceinline__ double wave_scan(double v) {
+    v += shifted<0x111, 0xf>(v);         // row_shr 1, 2, 4, 8
+    v += shifted<0x112, 0xf>(v);
+    v += shifted<0x114, 0xf>(v);
+    v += shifted<0x118, 0xf>(v);
+    v += shifted<0x142, 0xa>(v);         // lane 15 of rows 0, 2 into rows 1, 3
+    v += shifted<0x143, 0xc>(v);         // lane 31 into rows 2, 3
+    return v;
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// What a chunk's gates are to the products, per head and token.
+struct Gates {
+    float hi[CH], lo[CH];                // G log2 e in two floats
+    float dt[CH], w[CH];                 // dt_j and exp(G_last - G_j) dt_j
+    float e[CH];                         // exp(G_i)
+    float last;                          // exp(G_last)
+};
 template <class M, int DK, int DV, int HB>
 struct Lds {
     typedef typename M::T T;
@@ -77,26 +108,22 @@ struct Lds {
     alignas(16) T C[CH * SK];
     alignas(16) T X[CH * SV];
     alignas(16) T Mx[HB][CH * SM];       // M, row i
-    float hi[HB][CH], lo[HB][CH];        // G log2 e in two floats
-    float dt[HB][CH], w[HB][CH];         // dt_j and exp(G_last - G_j) dt_j
-    float e[HB][CH];                     // exp(G_i)
-    float last[HB];                      // exp(G_last)
-    double total[HB];                    // log2 of the decay since the segment's start
+    alignas(16) Gates gate[2][HB];       // this chunk's and the next one's
 };
 
 template <class M, int DK, int DV, int HB, int MODE>
-__global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
+__global__ void __launch_bounds__(HB * DV * 4) scan_kernel(ScanArgs a)
 {
     typedef typename M::T T;
     typedef typename M::Frag Frag;
     typedef Lds<M, DK, DV, HB> L;
     constexpr int V = M::V;
-    constexpr int TILES = HB * DV / 16 / 4;          // 16-column tiles of a wave
+    constexpr int WAVES = HB * DV / 16, NTH = 64 * WAVES;    // a wave for every 16 columns
     constexpr bool Y = MODE != MODE_STATE;
     extern __shared__ __align__(16) char smem[];
     L &s = *reinterpret_cast<L *>(smem);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int g = lane >> 4, col = lane & 15;
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
     const int hblocks = a.h_v / HB;
@@ -124,104 +151,108 @@ __global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
     if (a.segs > 1 && sbeg >= end) return;           // an empty segment: nothing reads its state
     const int nch = sbeg < send ? (int)((send - sbeg + CH - 1) / CH) : 0;
 
-    // this wave's column tiles all belong to one head
-    const int hl = wave * TILES * 16 / DV;           // head within the block
-    const int h = h0 + hl;
-    const int c0 = wave * TILES * 16;                // first column within the block's HB * DV
+    const int hl = wave * 16 / DV, h = h0 + hl;      // this wave's head
+    const int c0 = wave * 16;                        // its columns within the block's HB * DV
     const int p0 = c0 - hl * DV;                     // and within the head
     const int64_t state = (((int64_t)n * a.segs + seg) * a.h_v + h) * DK * DV;
     const float *Sin = nullptr;
     if (MODE == MODE_OUT) Sin = a.seg_state + state;
     else if (a.segs == 1 && a.S0) Sin = a.S0 + state;
 
-    f32x4 S[DK / 16][TILES];
+    f32x4 S[DK / 16];
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt)
 #pragma unroll
-        for (int pt = 0; pt < TILES; ++pt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[kt][pt][i] = Sin ? Sin[(int64_t)(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col] : 0.0f;
+        for (int i = 0; i < 4; ++i)
+            S[kt][i] = Sin ? Sin[(16 * kt + 4 * g + i) * DV + p0 + col] : 0.0f;
 
     if (Y) {   // the tiles right of the diagonal that share a 32-deep step with it stay zero
-        for (int i = threadIdx.x; i < HB * CH * L::SM; i += NT) (&s.Mx[0][0])[i] = 0;
+        for (int i = threadIdx.x; i < HB * CH * L::SM; i += NTH) (&s.Mx[0][0])[i] = 0;
     }
-    if (threadIdx.x < HB) s.total[threadIdx.x] = 0.0;
 
     const int gq = h0 / (a.h_v / a.h_qk);            // the group's B and C
     const T *Bp = static_cast<const T *>(a.B) + (int64_t)gq * DK;
     const T *Cp = static_cast<const T *>(a.C) + (int64_t)gq * DK;
     const T *Xp = static_cast<const T *>(a.x) + (int64_t)h0 * DV;
-    const T *dtp = static_cast<const T *>(a.dt) + h0;
-    constexpr int NBK = CH * DK / V / NT, NX = CH * HB * DV / V / NT;
+    constexpr int NBK = CH * DK / V / NTH, NX = CH * HB * DV / V / NTH;
+    static_assert(NBK >= 1 && NX >= 1, "every thread has vectors of a chunk to bring in");
     u32x4 rb[NBK], rc[NBK], rx[NX];
-    float rdt = 0.0f;
-
+    // Rows behind the segment's end repeat its last one: their dt is 0, so they add nothing.
     auto fetch = [&](int64_t t0) {
+        const uint32_t lastrow = send - t0 < CH ? (uint32_t)(send - t0 - 1) : CH - 1;
+        const T *b = Bp + t0 * a.bs, *c = Cp + t0 * a.cs, *x = Xp + t0 * a.xs;
 #pragma unroll
         for (int i = 0; i < NBK; ++i) {
-            const int e = (threadIdx.x + i * NT) * V, row = e / DK;
-            const bool in = t0 + row < send;
-            rb[i] = in ? load16(Bp + (t0 + row) * a.bs + e % DK) : u32x4{0, 0, 0, 0};
-            if (Y) rc[i] = in ? load16(Cp + (t0 + row) * a.cs + e % DK) : u32x4{0, 0, 0, 0};
+            const uint32_t e = (threadIdx.x + i * NTH) * V, row = min(e / DK, lastrow);
+            rb[i] = load16(b + (uint64_t)row * (uint32_t)a.bs + e % DK);
+            if (Y) rc[i] = load16(c + (uint64_t)row * (uint32_t)a.cs + e % DK);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const int e = (threadIdx.x + i * NT) * V, row = e / (HB * DV);
-            rx[i] = t0 + row < send ? load16(Xp + (t0 + row) * a.xs + e % (HB * DV)) : u32x4{0, 0, 0, 0};
+            const uint32_t e = (threadIdx.x + i * NTH) * V, row = min(e / (HB * DV), lastrow);
+            rx[i] = load16(x + (uint64_t)row * (uint32_t)a.xs + e % (HB * DV));
         }
-        if (wave < HB) rdt = t0 + lane < send ? M::one(dtp + (t0 + lane) * a.dts + wave) : 0.0f;
     };
-    if (nch > 0) fetch(sbeg);
+    // The gates of one head, by one of the last waves (the first ones have more of M): a chunk ahead,
+    // from a dt that was loaded a chunk before that.
+    const int gw = WAVES - 1 - wave;
+    const bool gates = gw < HB;
+    const int gh = gates ? h0 + gw : h0;
+    const float gA = a.A[gh], gbias = a.dt_bias ? a.dt_bias[gh] : 0.0f;
+    const T *dtp = static_cast<const T *>(a.dt) + gh;
+    auto fetch_dt = [&](int64_t t0) {
+        const int64_t t = t0 + lane < send ? t0 + lane : send - 1;
+        return M::one(dtp + t * a.dts);
+    };
+    double total = 0.0;                              // log2 of the decay since the segment's start
+    auto form_gates = [&](int64_t t0, float raw, Gates &o) {
+        const bool in = t0 + lane < send;
+        float dt = raw + gbias;
+        if (a.softplus) dt = softplus(dt);
+        dt = in ? dt : 0.0f;
+        // log2 a; below -1000 it is 0 in fp32 whatever follows, and stays finite here
+        const double ga = in ? fmax((double)dt * (double)gA * 1.4426950408889634, -1000.0) : 0.0;
+        const double G = wave_scan(ga), all = last_lane(G);
+        const float hi = (float)G;
+        o.hi[lane] = hi;
+        o.lo[lane] = (float)(G - (double)hi);
+        o.dt[lane] = dt;
+        o.w[lane] = __builtin_amdgcn_exp2f((float)(all - G)) * dt;
+        o.e[lane] = __builtin_amdgcn_exp2f(hi);
+        if (lane == 0) o.last = __builtin_amdgcn_exp2f((float)all);
+        total += all;
+    };
+    float rdt = 0.0f;
+    if (nch > 0) {
+        fetch(sbeg);
+        if (gates) {
+            form_gates(sbeg, fetch_dt(sbeg), s.gate[0][gw]);
+            if (nch > 1) rdt = fetch_dt(sbeg + CH);
+        }
+    }
 
     for (int ch = 0; ch < nch; ++ch) {
         const int64_t t0 = sbeg + (int64_t)ch * CH;
         __syncthreads();                             // the last chunk's readers are done
 #pragma unroll
         for (int i = 0; i < NBK; ++i) {
-            const int e = (threadIdx.x + i * NT) * V, row = e / DK;
-            store16(&s.B[row * L::SK + e % DK], rb[i]);
-            if (Y) store16(&s.C[row * L::SK + e % DK], rc[i]);
+            const int e = (threadIdx.x + i * NTH) * V;
+            store16(&s.B[e / DK * L::SK + e % DK], rb[i]);
+            if (Y) store16(&s.C[e / DK * L::SK + e % DK], rc[i]);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const int e = (threadIdx.x + i * NT) * V, row = e / (HB * DV);
-            store16(&s.X[row * L::SV + e % (HB * DV)], rx[i]);
-        }
-        if (wave < HB) {                             // the gates of head h0 + wave
-            const bool in = t0 + lane < send;
-            float dt = rdt + (a.dt_bias ? a.dt_bias[h0 + wave] : 0.0f);
-            if (a.softplus) dt = softplus(dt);
-            dt = in ? dt : 0.0f;
-            // log2 a; below -1000 it is 0 in fp32 whatever follows, and stays finite here
-            double G = in ? fmax((double)dt * (double)a.A[h0 + wave] * 1.4426950408889634, -1000.0) : 0.0;
-#pragma unroll
-            for (int off = 1; off < 64; off *= 2) {
-                const double up = __shfl_up(G, off);
-                if (lane >= off) G += up;
-            }
-            const double all = __shfl(G, 63);
-            const float hi = (float)G;
-            s.hi[wave][lane] = hi;
-            s.lo[wave][lane] = (float)(G - (double)hi);
-            s.dt[wave][lane] = dt;
-            s.w[wave][lane] = exp2f((float)(all - G)) * dt;
-            s.e[wave][lane] = exp2f((float)G);
-            if (lane == 0) {
-                s.last[wave] = exp2f((float)all);
-                s.total[wave] += all;
-            }
+            const int e = (threadIdx.x + i * NTH) * V;
+            store16(&s.X[e / (HB * DV) * L::SV + e % (HB * DV)], rx[i]);
         }
         __syncthreads();
         if (ch + 1 < nch) fetch(t0 + CH);
+        const Gates &gt = s.gate[ch & 1][hl];
 
         if (Y) {
             // M: the ten 16 x 16 tiles on and below the diagonal, shared out among the waves;
             // C B^T is the same for the block's heads.  Rows j in the accumulator, column i.
-#pragma unroll
-            for (int tt = 0; tt < 3; ++tt) {
-                const int t = wave + 4 * tt;
-                if (t >= 10) break;
+            for (int t = wave; t < 10; t += WAVES) {
                 const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
                 const int jt = t - it * (it + 1) / 2;
                 f32x4 cb = {0, 0, 0, 0};
@@ -232,120 +263,96 @@ __global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
                 const int i = 16 * it + col, j0 = 16 * jt + 4 * g;
 #pragma unroll
                 for (int q = 0; q < HB; ++q) {
-                    const float hi = s.hi[q][i], lo = s.lo[q][i];
+                    const Gates &z = s.gate[ch & 1][q];
+                    const float hi = z.hi[i], lo = z.lo[i];
+                    const f32x4 hj = *reinterpret_cast<const f32x4 *>(&z.hi[j0]), lj = *reinterpret_cast<const f32x4 *>(&z.lo[j0]);
+                    const f32x4 dj = *reinterpret_cast<const f32x4 *>(&z.dt[j0]);
                     float m[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int j = j0 + k;
-                        const float d = (hi - s.hi[q][j]) + (lo - s.lo[q][j]);
-                        m[k] = j <= i ? cb[k] * (exp2f(d) * s.dt[q][j]) : 0.0f;
+                        const float d = (hi - hj[k]) + (lo - lj[k]);
+                        m[k] = j0 + k <= i ? cb[k] * (__builtin_amdgcn_exp2f(d) * dj[k]) : 0.0f;
                     }
                     M::store4(&s.Mx[q][i * L::SM + j0], m);
                 }
             }
         }
-        f32x4 yt[4][TILES];
+        if (gates && ch + 1 < nch) {
+            form_gates(t0 + CH, rdt, s.gate[(ch + 1) & 1][gw]);
+            if (ch + 2 < nch) rdt = fetch_dt(t0 + 2 * CH);
+        }
+        f32x4 yt[4];
         if (Y) {
             // exp(G_i) (S^T C^T)
 #pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int pt = 0; pt < TILES; ++pt) yt[it][pt] = f32x4{0, 0, 0, 0};
+            for (int it = 0; it < 4; ++it) yt[it] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < DK / 32; ++kb) {
-                Frag St[TILES];
+                float f[8];
 #pragma unroll
-                for (int pt = 0; pt < TILES; ++pt) {
-                    float f[8];
+                for (int i = 0; i < 8; ++i) f[i] = S[2 * kb + (i >> 2)][i & 3];
+                const Frag St = M::from_floats(f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = S[2 * kb + (i >> 2)][pt][i & 3];
-                    St[pt] = M::from_floats(f);
-                }
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const Frag cf = M::row_acc(&s.C[16 * it * L::SK + 32 * kb], L::SK, lane);
-#pragma unroll
-                    for (int pt = 0; pt < TILES; ++pt) yt[it][pt] = M::mma(yt[it][pt], St[pt], cf);
-                }
+                for (int it = 0; it < 4; ++it)
+                    yt[it] = M::mma(yt[it], St, M::row_acc(&s.C[16 * it * L::SK + 32 * kb], L::SK, lane));
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const float e = s.e[hl][16 * it + col];
-#pragma unroll
-                for (int pt = 0; pt < TILES; ++pt) yt[it][pt] *= e;
-            }
+            for (int it = 0; it < 4; ++it) yt[it] *= gt.e[16 * it + col];
             __syncthreads();                         // M is whole
         }
         // X^T: rows p for Y^T, and (the same registers) columns p for the state
-        Frag xf[2][TILES];
+        Frag xf[2];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int pt = 0; pt < TILES; ++pt)
-                xf[kb][pt] = M::col_acc(&s.X[32 * kb * L::SV + c0 + 16 * pt], L::SV, lane);
+        for (int kb = 0; kb < 2; ++kb) xf[kb] = M::col_acc(&s.X[32 * kb * L::SV + c0], L::SV, lane);
         if (Y) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
-                for (int kb = 0; kb <= it / 2; ++kb) {
-                    const Frag mf = M::row_acc(&s.Mx[hl][16 * it * L::SM + 32 * kb], L::SM, lane);
-#pragma unroll
-                    for (int pt = 0; pt < TILES; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
-                }
+                for (int kb = 0; kb <= it / 2; ++kb)
+                    yt[it] = M::mma(yt[it], xf[kb], M::row_acc(&s.Mx[hl][16 * it * L::SM + 32 * kb], L::SM, lane));
             const float D = a.D ? a.D[h] : 0.0f;
-            T *yp = static_cast<T *>(a.y);
+            const int left = send - t0 < CH ? (int)(send - t0) : CH;
+            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0 + 4 * g;
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const int i = 16 * it + col;
-                if (t0 + i >= send) continue;
+                float x[4], o[4];
+                M::load4(&s.X[i * L::SV + c0 + 4 * g], x);
 #pragma unroll
-                for (int pt = 0; pt < TILES; ++pt) {
-                    float x[4], o[4];
-                    M::load4(&s.X[i * L::SV + c0 + 16 * pt + 4 * g], x);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
-                    M::store4(yp + (row0 + (t0 - beg) + i) * a.ys + (int64_t)h * DV + p0 + 16 * pt + 4 * g, o);
-                }
+                for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][k]);
+                if (i < left) M::store4(yp + (uint64_t)(uint32_t)i * (uint32_t)a.ys, o);
             }
         }
         // the state; the outputs alone (MODE_OUT) only need it to the precision of C S
-        if (MODE == MODE_OUT && ch + 1 == nch) continue;
-        const float last = s.last[hl];
+        if (MODE == MODE_OUT && ch + 1 == nch) break;
+        const float last = gt.last;
 #pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt)
-#pragma unroll
-            for (int pt = 0; pt < TILES; ++pt) S[kt][pt] *= last;
+        for (int kt = 0; kt < DK / 16; ++kt) S[kt] *= last;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             constexpr int TERMS = V == 4 || MODE == MODE_OUT ? 1 : 3;
-            Frag wx[TILES][TERMS];
-            float w[8];
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + 4 * g]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + 16 + 4 * g]);
+            Frag wx[TERMS];
+            float x[8];
+            M::to_floats(xf[kb], x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = s.w[hl][32 * kb + 4 * g + (j & 3) + 16 * (j >> 2)];
+            for (int j = 0; j < 4; ++j) { x[j] *= w0[j]; x[4 + j] *= w1[j]; }
 #pragma unroll
-            for (int pt = 0; pt < TILES; ++pt) {
-                float x[8];
-                M::to_floats(xf[kb][pt], x);
+            for (int term = 0; term < TERMS; ++term) {
+                wx[term] = M::from_floats(x);
+                if (term + 1 < TERMS) {
+                    float got[8];
+                    M::to_floats(wx[term], got);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= w[j];
-#pragma unroll
-                for (int term = 0; term < TERMS; ++term) {
-                    wx[pt][term] = M::from_floats(x);
-                    if (term + 1 < TERMS) {
-                        float got[8];
-                        M::to_floats(wx[pt][term], got);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] -= got[j];
-                    }
+                    for (int j = 0; j < 8; ++j) x[j] -= got[j];
                 }
             }
 #pragma unroll
             for (int kt = 0; kt < DK / 16; ++kt) {
                 const Frag bf = M::col_acc(&s.B[32 * kb * L::SK + 16 * kt], L::SK, lane);
 #pragma unroll
-                for (int pt = 0; pt < TILES; ++pt)
-#pragma unroll
-                    for (int term = TERMS - 1; term >= 0; --term) S[kt][pt] = M::mma(S[kt][pt], bf, wx[pt][term]);
+                for (int term = TERMS - 1; term >= 0; --term) S[kt] = M::mma(S[kt], bf, wx[term]);
             }
         }
     }
@@ -354,12 +361,9 @@ __global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt)
 #pragma unroll
-        for (int pt = 0; pt < TILES; ++pt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                So[(int64_t)(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col] = S[kt][pt][i];
-    if (a.segs > 1 && threadIdx.x < HB)
-        a.seg_decay[((int64_t)n * a.segs + seg) * a.h_v + h0 + threadIdx.x] = (float)exp2(s.total[threadIdx.x]);
+        for (int i = 0; i < 4; ++i) So[(16 * kt + 4 * g + i) * DV + p0 + col] = S[kt][i];
+    if (a.segs > 1 && gates && lane == 0)
+        a.seg_decay[((int64_t)n * a.segs + seg) * a.h_v + gh] = (float)exp2(total);
 }
 
 // Chains the segments of a state: every segment's local state is replaced by the state in front
@@ -435,7 +439,7 @@ hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(NT), bytes, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(HB * DV * 4), bytes, stream, a);
     return hipGetLastError();
 }
 
@@ -470,15 +474,16 @@ hipError_t scan_v(const ScanArgs &a, int d_v, hipStream_t stream)
 
 }  // namespace
 
-// Enough segments that a launch has about 1024 workgroups, of eight chunks or more each.
+// Enough segments that a launch has about 1024 workgroups.  The longest sequence is not known on the
+// host: a short one's surplus segments are empty and end at once.
 int32_t scan_segments(int32_t n_seqs, int32_t h_qk, int32_t h_v, int32_t d_v, int bf16, int64_t tokens)
 {
     if (n_seqs <= 0) return 1;
     const int hb = bf16 && d_v == 64 && (h_v / h_qk) % 2 == 0 ? 2 : 1;
     const int64_t chains = (int64_t)n_seqs * (h_v / hb);
-    const int64_t chunks = (tokens / n_seqs + CH - 1) / CH;
+    const int64_t chunks = (tokens + CH - 1) / CH;
     int64_t s = 1024 / chains;
-    if (chunks / 8 < s) s = chunks / 8;
+    if (chunks / 2 < s) s = chunks / 2;
     return (int32_t)(s < 1 ? 1 : s);
 }
 
