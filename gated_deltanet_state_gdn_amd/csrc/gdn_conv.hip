@@ -16,8 +16,10 @@ namespace {
 
 constexpr int NT = 256;
 
+// y / (1 + e^-y) with the hardware's exponential and reciprocal (one unit in the last place each):
+// the division's and exp's exact forms cost more instructions than the whole filter.
 __device__ __forceinline__ float act(float y, int silu) {
-    return silu ? y / (1.0f + expf(-y)) : y;
+    return silu ? y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.4426950408889634f)) : y;
 }
 
 // W taps of V channels, [channels, W] row-major
@@ -77,22 +79,22 @@ __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a, int cols, uint32_t
     float tap[W][V], b[V];
     load_taps<W, V>(a.w, a.bias, c, tap, b);
     T *y = static_cast<T *>(a.y) + c;
+    float win[W][V];                                          // the window, each input unpacked once
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) E::unpack(in[i], win[i]);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         const int64_t t = t0 + i;
         if (t >= end) break;
+        E::unpack(in[i + W - 1], win[(i + W - 1) % W]);
         float acc[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = b[v];
+        for (int v = 0; v < V; ++v) {
+            acc[v] = b[v];
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            float f[V];
-            E::unpack(in[i + j], f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(tap[j][v], f[v], acc[v]);
+            for (int j = 0; j < W; ++j) acc[v] = fmaf(tap[j][v], win[(i + j) % W][v], acc[v]);
+            acc[v] = act(acc[v], a.silu);
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = act(acc[v], a.silu);
         store16(y + t * a.ys, E::pack(acc));
     }
 }

@@ -55,6 +55,12 @@ __device__ __forceinline__ void store16(void *p, u32x4 v) { *reinterpret_cast<u3
 // ln(1 + e^x): e^-|x| never overflows, and log1p keeps the small values of very negative x.
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
+// The value, in a register of its own: what is computed from it in a loop stays in the loop instead
+// of being kept in registers over it.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 // Orders the LDS accesses of one wave's lanes: what any lane wrote before is read after.
 __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

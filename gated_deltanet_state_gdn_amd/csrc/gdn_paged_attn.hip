@@ -260,13 +260,6 @@ struct Tile {
         }
     }
 };
-// The value, in a register of its own: what is computed from it in a loop stays in the loop instead
-// of being kept in registers over it.
-__device__ __forceinline__ uint32_t here(uint32_t v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-
 // Waits until at most N of the wave's last loads are on their way (they return in order), and until
 // all its LDS reads are done.  The compiler counts with these builtins, and no access moves over them.
 __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
@@ -569,17 +562,19 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 }
 
 // ------------------------------------------------------------- the splits of a row, joined
-// One workgroup per row: 256 / (D / 4) slices of the row's splits, four entries a thread; the slices
-// meet in LDS, in order.
-template <class M, int D>
+// A workgroup takes 256 / (D / 4) / SL rows of one token, four entries a thread, and SL slices of a
+// row's splits, which meet in LDS in order.  Few splits: one slice, and every thread for itself.
+template <class M, int D, int SL>
 __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
 {
     typedef typename M::T T;
-    constexpr int C = D / 4, SL = NT / C, MOST = 256;    // MOST: weights held in LDS at a time
-    __shared__ float w[MOST];
-    __shared__ __align__(16) f32x4 part[SL][C];
-    __shared__ float lpart[NT / 64];
-    const int64_t row = blockIdx.x, t = row / a.h_q;
+    constexpr int C = D / 4, RW = NT / C / SL;
+    __shared__ __align__(16) f32x4 part[SL][RW][C];
+    __shared__ float lpart[SL][RW];
+    const int blocks = (a.h_q + RW - 1) / RW;            // of one token
+    const int64_t t = blockIdx.x / blocks;
+    const int c = threadIdx.x % C, rw = threadIdx.x / C % RW, slice = threadIdx.x / C / RW;
+    const int h = (int)(blockIdx.x % blocks) * RW + rw;
     const int n = token_sequence(a.cu, a.n_seqs, t);
     const int32_t b = a.cu[n], e = a.cu[n + 1];
     if (!range_ok(b, e, a.total) || t < b || t >= e) return;
@@ -587,45 +582,44 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
     if (!kv_ok(kv, a.max_kv, a.page_size, a.max_pages)) return;
     const int32_t limit = kv - (e - (int32_t)t) + 1;
     const int act = limit > 0 ? (limit + a.split_keys - 1) / a.split_keys : 1;
-    const int64_t step = a.total * a.h_q;
-    const int lane = threadIdx.x & 63, c = threadIdx.x % C, slice = threadIdx.x / C;
-    float mx = -INFINITY;                                // every wave for itself
-    for (int s = lane; s < act; s += 64) mx = fmaxf(mx, a.part_ml[(s * step + row) * 2]);
+    const int64_t step = a.total * a.h_q, row = t * a.h_q + (h < a.h_q ? h : a.h_q - 1);
+    const f32x2 *ml = reinterpret_cast<const f32x2 *>(a.part_ml) + row;
+    float mx = -INFINITY;
+    if (SL > 1) {                                        // a wave is one row's: its lanes share the splits
+        for (int s = threadIdx.x & 63; s < act; s += 64) mx = fmaxf(mx, ml[s * step].x);
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+        for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+    } else {
+        for (int s = 0; s < act; ++s) mx = fmaxf(mx, ml[s * step].x);
+    }
     const float base = mx == -INFINITY ? 0.0f : mx;
     float l = 0.0f;
     f32x4 acc = {0, 0, 0, 0};
-    for (int s0 = 0; s0 < act; s0 += MOST) {
-        const int some = act - s0 < MOST ? act - s0 : MOST;
-        if (s0 > 0) __syncthreads();
-        if ((int)threadIdx.x < some) {
-            const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.part_ml + ((s0 + threadIdx.x) * step + row) * 2);
-            const float f = exp2f(ml.x - base);
-            w[threadIdx.x] = f;
-            l += ml.y * f;
-        }
-        __syncthreads();
-        const float *p = a.part_o + (s0 * step + row) * D + 4 * c;
+    const float *p = a.part_o + row * D + 4 * c;
 #pragma unroll 4
-        for (int s = slice; s < some; s += SL) acc += *reinterpret_cast<const f32x4 *>(p + s * step * D) * w[s];
+    for (int s = slice; s < act; s += SL) {
+        const f32x2 v = ml[s * step];
+        const float f = exp2f(v.x - base);
+        l += v.y * f;
+        acc += *reinterpret_cast<const f32x4 *>(p + s * step * D) * f;
     }
+    if (SL > 1) {
+        part[slice][rw][c] = acc;
+        if (c == 0) lpart[slice][rw] = l;
+        __syncthreads();
+        if (slice > 0) return;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off);
-    if (lane == 0) lpart[threadIdx.x >> 6] = l;
-    part[slice][c] = acc;
-    __syncthreads();
-    if (slice > 0) return;
-#pragma unroll
-    for (int s = 1; s < SL; ++s) acc += part[s][c];
-    l = lpart[0];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) l += lpart[i];
+        for (int s = 1; s < SL; ++s) {
+            acc += part[s][rw][c];
+            l += lpart[s][rw];
+        }
+    }
+    if (h >= a.h_q) return;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     float x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = acc[i] * inv;
-    M::store4(static_cast<T *>(a.o) + t * a.os + (row % a.h_q) * D + 4 * c, x);
+    M::store4(static_cast<T *>(a.o) + t * a.os + (int64_t)h * D + 4 * c, x);
     if (a.lse && c == 0) a.lse[row] = l > 0.0f ? mx * kLn2 + logf(l) : -INFINITY;
 }
 
@@ -657,7 +651,9 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
         else e = start(prefill_kernel<M, D, NB, 4, KT>, blocks, a, stream, 256);
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    return start(join_kernel<M, D>, a.total * a.h_q, a, stream, NT);
+    constexpr int R = NT / (D / 4);                      // rows of a workgroup without slices
+    if (a.splits <= 8) return start(join_kernel<M, D, 1>, a.total * ((a.h_q + R - 1) / R), a, stream, NT);
+    return start(join_kernel<M, D, R>, a.total * a.h_q, a, stream, NT);
 }
 
 template <class M>
@@ -680,10 +676,11 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     p.decode = total * G <= 32 * (int64_t)n_seqs;
     p.rows = p.decode ? 16 : bf16 && total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
-    int64_t want = (p.decode ? 1024 : 256 * (256 / p.rows)) / (tiles > 0 ? tiles : 1);
+    // fp32 products take long beside a split's share: many splits, for their even spread
+    int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 4096) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;
     int64_t keys = (max_kv + want - 1) / want;
-    const int64_t least = p.decode ? 128 : 1024;
+    const int64_t least = p.decode ? 128 : bf16 ? 1024 : 256;
     if (keys < least) keys = least;
     p.split_keys = (int32_t)((keys + 127) / 128 * 128);
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;

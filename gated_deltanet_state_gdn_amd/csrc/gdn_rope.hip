@@ -15,11 +15,12 @@ namespace {
 
 constexpr int NT = 256;
 
-template <class E>
-__device__ __forceinline__ void load8(const typename E::T *p, float *f) {
-    E::unpack(load16(p), f);
-    if (E::V == 4) E::unpack(load16(p + 4), f + 4);
+__device__ __forceinline__ void load8f(const float *p, float *f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = p[i];
 }
+// Where the last round of heads ends, for groups of `per` heads taken `per` at a time from any start
+__device__ __forceinline__ int first_end(int heads, int per) { return (heads + per - 1) / per * per; }
 template <class E>
 __device__ __forceinline__ void store8(typename E::T *p, const float *f) {
     store16(p, E::pack(f));
@@ -31,8 +32,26 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a)
 {
     typedef typename E::T T;
     constexpr int L = D / 8;                       // lanes of one head
+    constexpr int MOST = 4;                        // heads that a group of lanes has on their way
     const int64_t t = blockIdx.x;
     if (t == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
+    // the first heads' vectors are asked for before the token's place is looked up
+    const int l = threadIdx.x & (L - 1), e0 = 8 * l;
+    const int heads = a.h_q + 2 * a.h_kv;
+    u32x4 raw[MOST][8 / E::V];
+    auto fetch = [&](int h0) {
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            const int h = h0 + k * (NT / L);
+            const int hh = h < heads ? h : heads - 1;
+            const T *src = hh < a.h_q ? static_cast<const T *>(a.q) + t * a.qs + (int64_t)hh * D
+                         : hh < a.h_q + a.h_kv ? static_cast<const T *>(a.k) + t * a.ks + (int64_t)(hh - a.h_q) * D
+                                               : static_cast<const T *>(a.v) + t * a.vs + (int64_t)(hh - a.h_q - a.h_kv) * D;
+#pragma unroll
+            for (int i = 0; i < 8 / E::V; ++i) raw[k][i] = load16(src + e0 + i * E::V);
+        }
+    };
+    fetch(threadIdx.x / L);
     const int n = token_sequence(a.cu, a.n_seqs, t);
     const int32_t beg = a.cu[n], end = a.cu[n + 1];
     if (!range_ok(beg, end, a.total) || t < beg || t >= end) return;   // bad, or behind the last sequence
@@ -47,7 +66,6 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a)
     if (threadIdx.x == 0 && !(stores && turns)) set_status(a.status);
     if (!turns) return;
 
-    const int l = threadIdx.x & (L - 1), e0 = 8 * l;
     // the angles of this lane's entries, and the weight of the pair's other half
     const int half = a.rot / 2;
     float c[8], s[8];
@@ -67,41 +85,43 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a)
     const int lane = threadIdx.x & 63;
     const int from = (lane & ~(L - 1)) + other;
 
-    const int heads = a.h_q + 2 * a.h_kv;
     cell += e0;
+    float wq[8], wk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { wq[i] = 1.0f; wk[i] = 1.0f; }
+    if (a.qw) load8f(a.qw + e0, wq);
+    if (a.kw) load8f(a.kw + e0, wk);
     // every group of lanes goes round equally often: the exchanges are between all lanes
-    for (int h0 = 0; h0 < heads; h0 += NT / L) {
-        const int h = h0 + threadIdx.x / L;
-        const bool is_q = h < a.h_q, is_k = !is_q && h < a.h_q + a.h_kv;
-        const int hk = is_q ? h : is_k ? h - a.h_q : h - a.h_q - a.h_kv;
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (h < heads) {
-            const T *src = is_q ? static_cast<const T *>(a.q) + t * a.qs
-                         : is_k ? static_cast<const T *>(a.k) + t * a.ks : static_cast<const T *>(a.v) + t * a.vs;
-            load8<E>(src + (int64_t)hk * D + e0, x);
+    for (int h0 = threadIdx.x / L; h0 < first_end(heads, NT / L); h0 += MOST * (NT / L)) {
+        if (h0 >= MOST * (NT / L)) fetch(h0);
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            const int h = h0 + k * (NT / L);
+            const bool is_q = h < a.h_q, is_k = !is_q && h < a.h_q + a.h_kv;
+            const int hk = is_q ? h : is_k ? h - a.h_q : h - a.h_q - a.h_kv;
+            float x[8], y[8], z[8];
+            E::unpack(raw[k][0], x);
+            if (E::V == 4) E::unpack(raw[k][E::V == 4], x + 4);
+            float inv = 1.0f;
+            if (a.norm) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+                for (int off = 1; off < L; off *= 2) ss += __shfl_xor(ss, off);
+                inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i] * inv * (is_q ? wq[i] : wk[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = INTER ? y[i ^ 1] : __shfl(y[i], from);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = e0 < a.rot ? fmaf(y[i], c[i], z[i] * s[i]) : y[i];
+            if (h >= heads) continue;
+            if (is_q) store8<E>(static_cast<T *>(a.qo) + t * a.qos + (int64_t)hk * D + e0, z);
+            else if (stores && is_k) store8<E>(static_cast<T *>(a.kc) + cell + hk * a.head_stride, z);
+            else if (stores) store8<E>(static_cast<T *>(a.vc) + cell + hk * a.head_stride, x);
         }
-        float y[8];
-        float inv = 1.0f;
-        if (a.norm) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int off = 1; off < L; off *= 2) ss += __shfl_xor(ss, off);
-            inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        }
-        const float *w = is_q ? a.qw : a.kw;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] * inv * (w ? w[e0 + i] : 1.0f);
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = INTER ? y[i ^ 1] : __shfl(y[i], from);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = e0 < a.rot ? fmaf(y[i], c[i], z[i] * s[i]) : y[i];
-        if (h >= heads) continue;
-        if (is_q) store8<E>(static_cast<T *>(a.qo) + t * a.qos + (int64_t)hk * D + e0, z);
-        else if (stores && is_k) store8<E>(static_cast<T *>(a.kc) + cell + hk * a.head_stride, z);
-        else if (stores) store8<E>(static_cast<T *>(a.vc) + cell + hk * a.head_stride, x);
     }
 }
 

@@ -112,7 +112,7 @@ struct Lds {
 };
 
 template <class M, int DK, int DV, int HB, int MODE>
-__global__ void __launch_bounds__(HB * DV * 4) scan_kernel(ScanArgs a)
+__global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 : 2) scan_kernel(ScanArgs a)
 {
     typedef typename M::T T;
     typedef typename M::Frag Frag;
@@ -181,15 +181,16 @@ __global__ void __launch_bounds__(HB * DV * 4) scan_kernel(ScanArgs a)
     auto fetch = [&](int64_t t0) {
         const uint32_t lastrow = send - t0 < CH ? (uint32_t)(send - t0 - 1) : CH - 1;
         const T *b = Bp + t0 * a.bs, *c = Cp + t0 * a.cs, *x = Xp + t0 * a.xs;
+        const uint32_t tid = here(threadIdx.x);
 #pragma unroll
         for (int i = 0; i < NBK; ++i) {
-            const uint32_t e = (threadIdx.x + i * NTH) * V, row = min(e / DK, lastrow);
+            const uint32_t e = (tid + i * NTH) * V, row = min(e / DK, lastrow);
             rb[i] = load16(b + (uint64_t)row * (uint32_t)a.bs + e % DK);
             if (Y) rc[i] = load16(c + (uint64_t)row * (uint32_t)a.cs + e % DK);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const uint32_t e = (threadIdx.x + i * NTH) * V, row = min(e / (HB * DV), lastrow);
+            const uint32_t e = (tid + i * NTH) * V, row = min(e / (HB * DV), lastrow);
             rx[i] = load16(x + (uint64_t)row * (uint32_t)a.xs + e % (HB * DV));
         }
     };
@@ -234,20 +235,22 @@ __global__ void __launch_bounds__(HB * DV * 4) scan_kernel(ScanArgs a)
     for (int ch = 0; ch < nch; ++ch) {
         const int64_t t0 = sbeg + (int64_t)ch * CH;
         __syncthreads();                             // the last chunk's readers are done
+        const uint32_t tid = here(threadIdx.x);
 #pragma unroll
         for (int i = 0; i < NBK; ++i) {
-            const int e = (threadIdx.x + i * NTH) * V;
+            const uint32_t e = (tid + i * NTH) * V;
             store16(&s.B[e / DK * L::SK + e % DK], rb[i]);
             if (Y) store16(&s.C[e / DK * L::SK + e % DK], rc[i]);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const int e = (threadIdx.x + i * NTH) * V;
+            const uint32_t e = (tid + i * NTH) * V;
             store16(&s.X[e / (HB * DV) * L::SV + e % (HB * DV)], rx[i]);
         }
         __syncthreads();
         if (ch + 1 < nch) fetch(t0 + CH);
         const Gates &gt = s.gate[ch & 1][hl];
+        const int lane = (int)here(threadIdx.x & 63), g = lane >> 4, col = lane & 15;
 
         if (Y) {
             // M: the ten 16 x 16 tiles on and below the diagonal, shared out among the waves;
