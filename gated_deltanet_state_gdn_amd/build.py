@@ -1,4 +1,4 @@
-"""Build the gfx950 HIP library ``libgdn.so`` in-tree (hipcc, no JIT cache).
+"""Build the gfx950 HIP library ``libgdn.so`` (hipcc) and the binding ``_gdn_torch.so`` in-tree, no JIT cache.
 
     python -m gated_deltanet_state_gdn_amd.build [--jobs N]
 """
@@ -16,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING = os.path.join(PKG, "_gdn_torch.so")
 SOURCES = ["gdn_api.hip", "gdn_chunk_ws.hip", "gdn_relerr.hip", "gdn_adaptive.hip", "gdn_segment.hip",
            "gdn_ops_api.hip", "gdn_conv.hip", "gdn_scan.hip", "gdn_step.hip", "gdn_rope.hip", "gdn_paged_attn.hip"]
 # host-only sources: argument validation and launches
@@ -48,16 +49,36 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_binding() -> str:
+    """The native half of the Python binding: host code against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    root = os.path.dirname(torch.__file__)
+    inc = [p for p in cpp_extension.include_paths() if os.path.isdir(p)] + [sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.check_call([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+                           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
+                          + [a for p in inc for a in ("-isystem", p)]
+                          + [os.path.join(CSRC, "gdn_torch.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
+                             "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + os.path.join(root, "lib")])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(jobs: int = 4, verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, jobs) + 1) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
     if verbose:
-        print("built", LIB)
+        print("built", LIB, "and", BINDING)
     return LIB
 
 
