@@ -98,4 +98,60 @@ struct MfmaF32 : ElemF32 {
     static __device__ __forceinline__ void load4(const T *p, float *x) { unpack(load16(p), x); }
 };
 
+// A tile of ROWS x COLS elements in LDS for products whose contraction runs along the rows or down
+// them, both in the acc map.
+//
+// bf16: no padding; 16-byte chunk c of row r sits at chunk c ^ swz(r).  Logical chunk 4 kb + g holds
+// columns 32 kb + {4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3}: a whole fragment of lane group g, one
+// 16-byte read; an aligned group of four columns is always 8 contiguous bytes.  The swizzles are the
+// ones that measured free of bank conflicts for these reads and keep the 8-byte transposing reads
+// at full rate (256-byte rows: the three low row bits, reversed, on chunk bits 3..1).
+template <class M, int ROWS, int COLS>
+struct Tile2;
+
+template <int ROWS, int COLS>
+struct Tile2<MfmaBF16, ROWS, COLS> {
+    typedef MfmaBF16::Frag Frag;
+    static constexpr int RB = COLS * 2;
+    static_assert(RB == 256 || RB == 128, "rows of 128 or 64 elements");
+    alignas(16) char d[ROWS * RB];
+
+    static __device__ __forceinline__ int swz(int r) {
+        return RB == 256 ? (((r & 1) << 3) | ((r & 2) << 1) | ((r & 4) >> 1)) : ((((r >> 1) & 1) << 2) | ((r >> 2) & 3));
+    }
+    __device__ __forceinline__ char *four(int r, int c) {           // columns c .. c + 3, c a multiple of 4
+        return d + r * RB + 16 * ((4 * (c >> 5) + ((c >> 2) & 3)) ^ swz(r)) + 8 * ((c >> 4) & 1);
+    }
+    __device__ __forceinline__ const char *four(int r, int c) const { return const_cast<Tile2 *>(this)->four(r, c); }
+    __device__ __forceinline__ void put16(int r, int c, u32x4 v) {  // columns c .. c + 7
+        *reinterpret_cast<u32x2 *>(four(r, c)) = u32x2{v.x, v.y};
+        *reinterpret_cast<u32x2 *>(four(r, c + 4)) = u32x2{v.z, v.w};
+    }
+    __device__ __forceinline__ void put4(int r, int c, const float *x) { MfmaBF16::store4(reinterpret_cast<uint16_t *>(four(r, c)), x); }
+    __device__ __forceinline__ void get4(int r, int c, float *x) const { MfmaBF16::load4(reinterpret_cast<const uint16_t *>(four(r, c)), x); }
+    // row r0 + l % 16 (r0 a multiple of 16), columns from 32 kb
+    __device__ __forceinline__ Frag row(int r0, int kb, int lane) const {
+        const int r = lane & 15;
+        return __builtin_bit_cast(Frag, load16(d + r0 * RB + ((r * RB + 16 * ((lane >> 4) ^ swz(r))) ^ (64 * kb))));
+    }
+    // column 16 ct + l % 16, rows from 32 kb
+    __device__ __forceinline__ Frag col(int kb, int ct, int lane) const {
+        const int m = lane & 15, r = 4 * (lane >> 4) + (m >> 2);
+        const char *p = d + 32 * kb * RB + ((r * RB + 16 * ((m & 3) ^ swz(r))) ^ (64 * (ct >> 1))) + 8 * (ct & 1);
+        return frag_of(read_tr(reinterpret_cast<const uint16_t *>(p)), read_tr(reinterpret_cast<const uint16_t *>(p + 16 * RB)));
+    }
+};
+
+template <int ROWS, int COLS>
+struct Tile2<MfmaF32, ROWS, COLS> {
+    typedef MfmaF32::Frag Frag;
+    static constexpr int ST = COLS + MfmaF32::PAD;
+    alignas(16) float d[ROWS * ST];
+    __device__ __forceinline__ void put16(int r, int c, u32x4 v) { store16(d + r * ST + c, v); }
+    __device__ __forceinline__ void put4(int r, int c, const float *x) { MfmaF32::store4(d + r * ST + c, x); }
+    __device__ __forceinline__ void get4(int r, int c, float *x) const { MfmaF32::load4(d + r * ST + c, x); }
+    __device__ __forceinline__ Frag row(int r0, int kb, int lane) const { return MfmaF32::row_acc(d + r0 * ST + 32 * kb, ST, lane); }
+    __device__ __forceinline__ Frag col(int kb, int ct, int lane) const { return MfmaF32::col_acc(d + 32 * kb * ST + 16 * ct, ST, lane); }
+};
+
 }  // namespace gdn

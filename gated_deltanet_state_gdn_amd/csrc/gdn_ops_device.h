@@ -52,6 +52,15 @@ struct ElemF32 {
 __device__ __forceinline__ u32x4 load16(const void *p) { return *reinterpret_cast<const u32x4 *>(p); }
 __device__ __forceinline__ void store16(void *p, u32x4 v) { *reinterpret_cast<u32x4 *>(p) = v; }
 
+// Workgroups go to the eight XCDs in turn.  This numbers them so that each run of `unit` consecutive
+// ones, which read the same memory, is on one XCD and shares its L2, and runs take the XCDs in turn.
+__device__ __forceinline__ uint32_t xcd_block(uint32_t unit) {
+    const uint32_t b = blockIdx.x, whole = gridDim.x / (8 * unit) * (8 * unit);
+    if (b >= whole) return b;
+    const uint32_t x = b % 8, i = b / 8;
+    return ((i / unit) * 8 + x) * unit + i % unit;
+}
+
 // ln(1 + e^x): e^-|x| never overflows, and log1p keeps the small values of very negative x.
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 

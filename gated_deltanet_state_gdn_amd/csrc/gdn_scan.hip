@@ -12,8 +12,8 @@
 // decays in front of weak ones cost the weak ones nothing.
 //
 // Work decomposition: a workgroup takes HB heads of one group over one segment of one sequence,
-// chunk by chunk.  The columns of S (d_v of every head) do not mix, so every wave owns a 16-column
-// tile of S whole, in its accumulators; M is the only product the waves share, and
+// chunk by chunk.  The columns of S (d_v of every head) do not mix, so every wave owns one or two
+// 16-column tiles of S whole, in its accumulators; M is the only product the waves share, and
 // goes through LDS.  Y is formed transposed (Y^T = S^T C^T + X^T M^T): accumulators of S become
 // operands where they are, and a lane ends with four consecutive entries of one token's y.
 //
@@ -102,23 +102,24 @@ struct Gates {
 };
 template <class M, int DK, int DV, int HB>
 struct Lds {
-    typedef typename M::T T;
-    static constexpr int SK = DK + M::PAD, SV = HB * DV + M::PAD, SM = CH + M::PAD;
-    alignas(16) T B[CH * SK];
-    alignas(16) T C[CH * SK];
-    alignas(16) T X[CH * SV];
-    alignas(16) T Mx[HB][CH * SM];       // M, row i
+    Tile2<M, CH, DK> B, C;
+    Tile2<M, CH, HB * DV> X;
+    Tile2<M, CH, CH> Mx[HB];             // M, row i
     alignas(16) Gates gate[2][HB];       // this chunk's and the next one's
 };
+// 16-column tiles of S that a wave owns: with two, the operands that every wave reads (C, B^T) serve
+// twice; bf16 workgroups of 128 columns then have four waves.
+template <class M, int DV, int HB>
+constexpr int wave_tiles() { return M::V == 8 && HB * DV == 128 ? 2 : 1; }
 
-template <class M, int DK, int DV, int HB, int MODE>
-__global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 : 2) scan_kernel(ScanArgs a)
+template <class M, int DK, int DV, int HB, int MODE, int WT>
+__global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
 {
     typedef typename M::T T;
     typedef typename M::Frag Frag;
     typedef Lds<M, DK, DV, HB> L;
     constexpr int V = M::V;
-    constexpr int WAVES = HB * DV / 16, NTH = 64 * WAVES;    // a wave for every 16 columns
+    constexpr int WAVES = HB * DV / 16 / WT, NTH = 64 * WAVES;
     constexpr bool Y = MODE != MODE_STATE;
     extern __shared__ __align__(16) char smem[];
     L &s = *reinterpret_cast<L *>(smem);
@@ -126,10 +127,12 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
+    // the heads of a segment next to each other: those of a group read the same B and C
     const int hblocks = a.h_v / HB;
-    const int hb = blockIdx.x % hblocks;
-    const int seg = (blockIdx.x / hblocks) % a.segs;
-    const int n = blockIdx.x / hblocks / a.segs;
+    const uint32_t block = xcd_block(a.h_v / a.h_qk / HB);
+    const int hb = block % hblocks;
+    const int seg = (block / hblocks) % a.segs;
+    const int n = block / hblocks / a.segs;
     const int h0 = hb * HB;
     int64_t beg, end;
     if (!window(a, n, beg, end)) {
@@ -151,23 +154,31 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
     if (a.segs > 1 && sbeg >= end) return;           // an empty segment: nothing reads its state
     const int nch = sbeg < send ? (int)((send - sbeg + CH - 1) / CH) : 0;
 
-    const int hl = wave * 16 / DV, h = h0 + hl;      // this wave's head
-    const int c0 = wave * 16;                        // its columns within the block's HB * DV
+    const int c0 = wave * 16 * WT;                   // this wave's columns within the block's HB * DV
+    const int hl = c0 / DV, h = h0 + hl;             // their head
     const int p0 = c0 - hl * DV;                     // and within the head
     const int64_t state = (((int64_t)n * a.segs + seg) * a.h_v + h) * DK * DV;
     const float *Sin = nullptr;
     if (MODE == MODE_OUT) Sin = a.seg_state + state;
     else if (a.segs == 1 && a.S0) Sin = a.S0 + state;
 
-    f32x4 S[DK / 16];
+    f32x4 S[DK / 16][WT];
+    if (Sin) {
 #pragma unroll
-    for (int kt = 0; kt < DK / 16; ++kt)
+        for (int kt = 0; kt < DK / 16; ++kt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            S[kt][i] = Sin ? Sin[(16 * kt + 4 * g + i) * DV + p0 + col] : 0.0f;
+            for (int pt = 0; pt < WT; ++pt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[kt][pt][i] = Sin[(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col];
+    } else {
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt)
+#pragma unroll
+            for (int pt = 0; pt < WT; ++pt) S[kt][pt] = f32x4{0, 0, 0, 0};
+    }
 
     if (Y) {   // the tiles right of the diagonal that share a 32-deep step with it stay zero
-        for (int i = threadIdx.x; i < HB * CH * L::SM; i += NTH) (&s.Mx[0][0])[i] = 0;
+        for (uint32_t i = threadIdx.x; i < sizeof(s.Mx) / 16; i += NTH) reinterpret_cast<u32x4 *>(s.Mx)[i] = u32x4{0, 0, 0, 0};
     }
 
     const int gq = h0 / (a.h_v / a.h_qk);            // the group's B and C
@@ -239,13 +250,13 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
 #pragma unroll
         for (int i = 0; i < NBK; ++i) {
             const uint32_t e = (tid + i * NTH) * V;
-            store16(&s.B[e / DK * L::SK + e % DK], rb[i]);
-            if (Y) store16(&s.C[e / DK * L::SK + e % DK], rc[i]);
+            s.B.put16(e / DK, e % DK, rb[i]);
+            if (Y) s.C.put16(e / DK, e % DK, rc[i]);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             const uint32_t e = (tid + i * NTH) * V;
-            store16(&s.X[e / (HB * DV) * L::SV + e % (HB * DV)], rx[i]);
+            s.X.put16(e / (HB * DV), e % (HB * DV), rx[i]);
         }
         __syncthreads();
         if (ch + 1 < nch) fetch(t0 + CH);
@@ -261,8 +272,7 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
                 f32x4 cb = {0, 0, 0, 0};
 #pragma unroll
                 for (int kb = 0; kb < DK / 32; ++kb)
-                    cb = M::mma(cb, M::row_nat(&s.B[16 * jt * L::SK + 32 * kb], L::SK, lane),
-                                M::row_nat(&s.C[16 * it * L::SK + 32 * kb], L::SK, lane));
+                    cb = M::mma(cb, s.B.row(16 * jt, kb, lane), s.C.row(16 * it, kb, lane));
                 const int i = 16 * it + col, j0 = 16 * jt + 4 * g;
 #pragma unroll
                 for (int q = 0; q < HB; ++q) {
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
                         const float d = (hi - hj[k]) + (lo - lj[k]);
                         m[k] = j0 + k <= i ? cb[k] * (__builtin_amdgcn_exp2f(d) * dj[k]) : 0.0f;
                     }
-                    M::store4(&s.Mx[q][i * L::SM + j0], m);
+                    s.Mx[q].put4(i, j0, m);
                 }
             }
         }
@@ -284,78 +294,107 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
             form_gates(t0 + CH, rdt, s.gate[(ch + 1) & 1][gw]);
             if (ch + 2 < nch) rdt = fetch_dt(t0 + 2 * CH);
         }
-        f32x4 yt[4];
+        f32x4 yt[4][WT];
         if (Y) {
             // exp(G_i) (S^T C^T)
 #pragma unroll
-            for (int it = 0; it < 4; ++it) yt[it] = f32x4{0, 0, 0, 0};
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int pt = 0; pt < WT; ++pt) yt[it][pt] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < DK / 32; ++kb) {
-                float f[8];
+                Frag St[WT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = S[2 * kb + (i >> 2)][i & 3];
-                const Frag St = M::from_floats(f);
+                for (int pt = 0; pt < WT; ++pt) {
+                    float f[8];
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
-                    yt[it] = M::mma(yt[it], St, M::row_acc(&s.C[16 * it * L::SK + 32 * kb], L::SK, lane));
+                    for (int i = 0; i < 8; ++i) f[i] = S[2 * kb + (i >> 2)][pt][i & 3];
+                    St[pt] = M::from_floats(f);
+                }
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const Frag cf = s.C.row(16 * it, kb, lane);
+#pragma unroll
+                    for (int pt = 0; pt < WT; ++pt) yt[it][pt] = M::mma(yt[it][pt], St[pt], cf);
+                }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) yt[it] *= gt.e[16 * it + col];
+            for (int it = 0; it < 4; ++it) {
+                const float e = gt.e[16 * it + col];
+#pragma unroll
+                for (int pt = 0; pt < WT; ++pt) yt[it][pt] *= e;
+            }
             __syncthreads();                         // M is whole
         }
         // X^T: rows p for Y^T, and (the same registers) columns p for the state
-        Frag xf[2];
+        Frag xf[2][WT];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) xf[kb] = M::col_acc(&s.X[32 * kb * L::SV + c0], L::SV, lane);
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int pt = 0; pt < WT; ++pt) xf[kb][pt] = s.X.col(kb, c0 / 16 + pt, lane);
         if (Y) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
-                for (int kb = 0; kb <= it / 2; ++kb)
-                    yt[it] = M::mma(yt[it], xf[kb], M::row_acc(&s.Mx[hl][16 * it * L::SM + 32 * kb], L::SM, lane));
+                for (int kb = 0; kb <= it / 2; ++kb) {
+                    const Frag mf = s.Mx[hl].row(16 * it, kb, lane);
+#pragma unroll
+                    for (int pt = 0; pt < WT; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
+                }
             const float D = a.D ? a.D[h] : 0.0f;
             const int left = send - t0 < CH ? (int)(send - t0) : CH;
             T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0 + 4 * g;
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const int i = 16 * it + col;
-                float x[4], o[4];
-                M::load4(&s.X[i * L::SV + c0 + 4 * g], x);
+                T *yi = yp + (uint64_t)(uint32_t)i * (uint32_t)a.ys;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][k]);
-                if (i < left) M::store4(yp + (uint64_t)(uint32_t)i * (uint32_t)a.ys, o);
+                for (int pt = 0; pt < WT; ++pt) {
+                    float x[4], o[4];
+                    s.X.get4(i, c0 + 16 * pt + 4 * g, x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
+                    if (i < left) M::store4(yi + 16 * pt, o);
+                }
             }
         }
         // the state; the outputs alone (MODE_OUT) only need it to the precision of C S
         if (MODE == MODE_OUT && ch + 1 == nch) break;
         const float last = gt.last;
 #pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt) S[kt] *= last;
+        for (int kt = 0; kt < DK / 16; ++kt)
+#pragma unroll
+            for (int pt = 0; pt < WT; ++pt) S[kt][pt] *= last;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             constexpr int TERMS = V == 4 || MODE == MODE_OUT ? 1 : 3;
             const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + 4 * g]);
             const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + 16 + 4 * g]);
-            Frag wx[TERMS];
-            float x[8];
-            M::to_floats(xf[kb], x);
+            Frag wx[WT][TERMS];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) { x[j] *= w0[j]; x[4 + j] *= w1[j]; }
+            for (int pt = 0; pt < WT; ++pt) {
+                float x[8];
+                M::to_floats(xf[kb][pt], x);
 #pragma unroll
-            for (int term = 0; term < TERMS; ++term) {
-                wx[term] = M::from_floats(x);
-                if (term + 1 < TERMS) {
-                    float got[8];
-                    M::to_floats(wx[term], got);
+                for (int j = 0; j < 4; ++j) { x[j] *= w0[j]; x[4 + j] *= w1[j]; }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] -= got[j];
+                for (int term = 0; term < TERMS; ++term) {
+                    wx[pt][term] = M::from_floats(x);
+                    if (term + 1 < TERMS) {
+                        float got[8];
+                        M::to_floats(wx[pt][term], got);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] -= got[j];
+                    }
                 }
             }
 #pragma unroll
             for (int kt = 0; kt < DK / 16; ++kt) {
-                const Frag bf = M::col_acc(&s.B[32 * kb * L::SK + 16 * kt], L::SK, lane);
+                const Frag bf = s.B.col(kb, kt, lane);
 #pragma unroll
-                for (int term = TERMS - 1; term >= 0; --term) S[kt] = M::mma(S[kt], bf, wx[term]);
+                for (int pt = 0; pt < WT; ++pt)
+#pragma unroll
+                    for (int term = TERMS - 1; term >= 0; --term) S[kt][pt] = M::mma(S[kt][pt], bf, wx[pt][term]);
             }
         }
     }
@@ -364,7 +403,9 @@ __global__ void __launch_bounds__(HB * DV * 4, M::V == 8 && HB * DV == 128 ? 4 :
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) So[(16 * kt + 4 * g + i) * DV + p0 + col] = S[kt][i];
+        for (int pt = 0; pt < WT; ++pt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) So[(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col] = S[kt][pt][i];
     if (a.segs > 1 && gates && lane == 0)
         a.seg_decay[((int64_t)n * a.segs + seg) * a.h_v + gh] = (float)exp2(total);
 }
@@ -437,12 +478,13 @@ hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
     static_assert(bytes <= 160 * 1024, "one workgroup's LDS");
     const int64_t blocks = (int64_t)a.n_seqs * a.segs * (a.h_v / HB);
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-    auto k = scan_kernel<M, DK, DV, HB, MODE>;
+    constexpr int WT = wave_tiles<M, DV, HB>();
+    auto k = scan_kernel<M, DK, DV, HB, MODE, WT>;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(HB * DV * 4), bytes, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(HB * DV * 4 / WT), bytes, stream, a);
     return hipGetLastError();
 }
 
@@ -477,15 +519,17 @@ hipError_t scan_v(const ScanArgs &a, int d_v, hipStream_t stream)
 
 }  // namespace
 
-// Enough segments that a launch has about 1024 workgroups.  The longest sequence is not known on the
-// host: a short one's surplus segments are empty and end at once.
+// bf16: segments for 512 workgroups, the two of every CU that run at once (one sequence of 32768
+// tokens, 32 heads: 207 us; 256: 284, 768: 238, 1024: 225, 2048: 266 us).  fp32: 2048, whose products
+// take long beside the chain of the segments (24 ragged prompts: 41 us; 512: 48, 1024: 46 us).  The
+// longest sequence is not known on the host: a short one's surplus segments are empty and end at once.
 int32_t scan_segments(int32_t n_seqs, int32_t h_qk, int32_t h_v, int32_t d_v, int bf16, int64_t tokens)
 {
     if (n_seqs <= 0) return 1;
     const int hb = bf16 && d_v == 64 && (h_v / h_qk) % 2 == 0 ? 2 : 1;
     const int64_t chains = (int64_t)n_seqs * (h_v / hb);
     const int64_t chunks = (tokens + CH - 1) / CH;
-    int64_t s = 1024 / chains;
+    int64_t s = (bf16 ? 512 : 2048) / chains;
     if (chunks / 2 < s) s = chunks / 2;
     return (int32_t)(s < 1 ? 1 : s);
 }
