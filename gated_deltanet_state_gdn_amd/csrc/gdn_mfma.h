@@ -99,13 +99,15 @@ struct MfmaF32 : ElemF32 {
 };
 
 // A tile of ROWS x COLS elements in LDS for products whose contraction runs along the rows or down
-// them, both in the acc map.
+// them.
 //
-// bf16: no padding; 16-byte chunk c of row r sits at chunk c ^ swz(r).  Logical chunk 4 kb + g holds
-// columns 32 kb + {4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3}: a whole fragment of lane group g, one
-// 16-byte read; an aligned group of four columns is always 8 contiguous bytes.  The swizzles are the
-// ones that measured free of bank conflicts for these reads and keep the 8-byte transposing reads
-// at full rate (256-byte rows: the three low row bits, reversed, on chunk bits 3..1).
+// bf16: the nat map, rows without padding; 16-byte chunk c of row r sits at chunk c ^ swz(r).  The
+// swizzles are ones that measured free of bank conflicts for 16-byte reads of 16 rows at one chunk
+// and that leave the 8-byte transposing reads at their full rate (256-byte rows: the three low row
+// bits, reversed, on chunk bits 3..1).
+// An accumulator tile kt whose rows are the contraction index of a later product along COLS holds
+// the entries state_row(kt, g, i) in element i of lane group g, so that it is that product's operand
+// where it is; spread(kb, kt) reads this tile's columns in that order.
 template <class M, int ROWS, int COLS>
 struct Tile2;
 
@@ -113,20 +115,20 @@ template <int ROWS, int COLS>
 struct Tile2<MfmaBF16, ROWS, COLS> {
     typedef MfmaBF16::Frag Frag;
     static constexpr int RB = COLS * 2;
+    static constexpr int LANE = 8, HALF = 4;        // contraction slots j of lane group g: 8 g + j
     static_assert(RB == 256 || RB == 128, "rows of 128 or 64 elements");
     alignas(16) char d[ROWS * RB];
 
     static __device__ __forceinline__ int swz(int r) {
         return RB == 256 ? (((r & 1) << 3) | ((r & 2) << 1) | ((r & 4) >> 1)) : ((((r >> 1) & 1) << 2) | ((r >> 2) & 3));
     }
+    static constexpr int NEXT4 = RB == 256 ? 32 : 16;               // what r -> r + 4 (r & 4 = 0) does to a chunk's place
+    static __device__ __forceinline__ int state_row(int kt, int g, int i) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1) + i; }
     __device__ __forceinline__ char *four(int r, int c) {           // columns c .. c + 3, c a multiple of 4
-        return d + r * RB + 16 * ((4 * (c >> 5) + ((c >> 2) & 3)) ^ swz(r)) + 8 * ((c >> 4) & 1);
+        return d + r * RB + 16 * ((c >> 3) ^ swz(r)) + 8 * ((c >> 2) & 1);
     }
     __device__ __forceinline__ const char *four(int r, int c) const { return const_cast<Tile2 *>(this)->four(r, c); }
-    __device__ __forceinline__ void put16(int r, int c, u32x4 v) {  // columns c .. c + 7
-        *reinterpret_cast<u32x2 *>(four(r, c)) = u32x2{v.x, v.y};
-        *reinterpret_cast<u32x2 *>(four(r, c + 4)) = u32x2{v.z, v.w};
-    }
+    __device__ __forceinline__ void put16(int r, int c, u32x4 v) { store16(d + r * RB + 16 * ((c >> 3) ^ swz(r)), v); }
     __device__ __forceinline__ void put4(int r, int c, const float *x) { MfmaBF16::store4(reinterpret_cast<uint16_t *>(four(r, c)), x); }
     __device__ __forceinline__ void get4(int r, int c, float *x) const { MfmaBF16::load4(reinterpret_cast<const uint16_t *>(four(r, c)), x); }
     // row r0 + l % 16 (r0 a multiple of 16), columns from 32 kb
@@ -134,11 +136,19 @@ struct Tile2<MfmaBF16, ROWS, COLS> {
         const int r = lane & 15;
         return __builtin_bit_cast(Frag, load16(d + r0 * RB + ((r * RB + 16 * ((lane >> 4) ^ swz(r))) ^ (64 * kb))));
     }
-    // column 16 ct + l % 16, rows from 32 kb
+    // rows from 32 kb; column 16 ct + l % 16
     __device__ __forceinline__ Frag col(int kb, int ct, int lane) const {
-        const int m = lane & 15, r = 4 * (lane >> 4) + (m >> 2);
-        const char *p = d + 32 * kb * RB + ((r * RB + 16 * ((m & 3) ^ swz(r))) ^ (64 * (ct >> 1))) + 8 * (ct & 1);
-        return frag_of(read_tr(reinterpret_cast<const uint16_t *>(p)), read_tr(reinterpret_cast<const uint16_t *>(p + 16 * RB)));
+        const int x = lane & 3, r = 8 * (lane >> 4) + ((lane & 15) >> 2);
+        return pair(kb, (r * RB + 16 * ((x >> 1) ^ swz(r)) + 8 * (x & 1)) ^ (32 * ct));
+    }
+    // rows from 32 kb; column state_row(kt, l / 4 % 4, l % 4)
+    __device__ __forceinline__ Frag spread(int kb, int kt, int lane) const {
+        const int x = lane & 3, r = 8 * (lane >> 4) + ((lane & 15) >> 2);
+        return pair(kb, ((r * RB + 16 * (x ^ swz(r))) ^ (64 * (kt >> 1))) + 8 * (kt & 1));
+    }
+    __device__ __forceinline__ Frag pair(int kb, uint32_t at) const {
+        return frag_of(read_tr(reinterpret_cast<const uint16_t *>(d + 32 * kb * RB + at)),
+                       read_tr(reinterpret_cast<const uint16_t *>(d + (32 * kb + 4) * RB + (at ^ NEXT4))));
     }
 };
 
@@ -146,12 +156,15 @@ template <int ROWS, int COLS>
 struct Tile2<MfmaF32, ROWS, COLS> {
     typedef MfmaF32::Frag Frag;
     static constexpr int ST = COLS + MfmaF32::PAD;
+    static constexpr int LANE = 4, HALF = 16;       // the acc map
     alignas(16) float d[ROWS * ST];
+    static __device__ __forceinline__ int state_row(int kt, int g, int i) { return 16 * kt + 4 * g + i; }
     __device__ __forceinline__ void put16(int r, int c, u32x4 v) { store16(d + r * ST + c, v); }
     __device__ __forceinline__ void put4(int r, int c, const float *x) { MfmaF32::store4(d + r * ST + c, x); }
     __device__ __forceinline__ void get4(int r, int c, float *x) const { MfmaF32::load4(d + r * ST + c, x); }
     __device__ __forceinline__ Frag row(int r0, int kb, int lane) const { return MfmaF32::row_acc(d + r0 * ST + 32 * kb, ST, lane); }
     __device__ __forceinline__ Frag col(int kb, int ct, int lane) const { return MfmaF32::col_acc(d + 32 * kb * ST + 16 * ct, ST, lane); }
+    __device__ __forceinline__ Frag spread(int kb, int kt, int lane) const { return col(kb, kt, lane); }
 };
 
 }  // namespace gdn

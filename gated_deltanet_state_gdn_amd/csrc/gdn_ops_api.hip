@@ -81,6 +81,9 @@ int32_t check_ssm(const gdn_ssm_desc *d, bool step)
     if (!stride_ok(d->x_stride, x, d->dtype) || !stride_ok(d->b_stride, k, d->dtype) ||
         !stride_ok(d->c_stride, k, d->dtype) || !stride_ok(d->y_stride, x, d->dtype))
         return refuse(GDN_ERR_ALIGN, "x, B, C, y strides: at least a token's row, a multiple of 16 bytes");
+    const int64_t widest = d->x_stride > d->y_stride ? d->x_stride : d->y_stride, groups = d->b_stride > d->c_stride ? d->b_stride : d->c_stride;
+    if (!step && (widest > groups ? widest : groups) * 64 * elem_bytes(d->dtype) >= 0x7fffffffLL)
+        return refuse(GDN_ERR_SHAPE, "state space: a 64-token chunk must span less than 2 GiB");
     if (d->dt_stride < d->h_v || d->dt_stride >= (1LL << 40)) return refuse(GDN_ERR_SHAPE, "dt_stride below h_v");
     return GDN_OK;
 }

@@ -87,9 +87,9 @@ __device__ __forceinline__ double wave_scan(double v) {
     v += shifted<0x143, 0xc>(v);         // lane 31 into rows 2, 3
     return v;
 }
-__device__ __forceinline__ double last_lane(double v) {
+__device__ __forceinline__ double lane_value(double v, int lane) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
@@ -98,6 +98,9 @@ struct Gates {
     float hi[CH], lo[CH];                // G log2 e in two floats
     float dt[CH], w[CH];                 // dt_j and exp(G_last - G_j) dt_j
     float e[CH];                         // exp(G_i)
+    // Tiles of M left of the diagonal one in tile row t: exp(G_i - G_j) dt_j = row[i] col[t - 1][j],
+    // split at token 16 t - 1 (both exponents <= 0, so neither factor overflows)
+    float row[CH], col[3][CH];
     float last;                          // exp(G_last)
 };
 template <class M, int DK, int DV, int HB>
@@ -118,6 +121,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
     typedef typename M::T T;
     typedef typename M::Frag Frag;
     typedef Lds<M, DK, DV, HB> L;
+    typedef Tile2<M, CH, DK> Bt;
     constexpr int V = M::V;
     constexpr int WAVES = HB * DV / 16 / WT, NTH = 64 * WAVES;
     constexpr bool Y = MODE != MODE_STATE;
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
 #pragma unroll
             for (int pt = 0; pt < WT; ++pt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[kt][pt][i] = Sin[(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col];
+                for (int i = 0; i < 4; ++i) S[kt][pt][i] = Sin[Bt::state_row(kt, g, i) * DV + p0 + 16 * pt + col];
     } else {
 #pragma unroll
         for (int kt = 0; kt < DK / 16; ++kt)
@@ -188,21 +192,35 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
     constexpr int NBK = CH * DK / V / NTH, NX = CH * HB * DV / V / NTH;
     static_assert(NBK >= 1 && NX >= 1, "every thread has vectors of a chunk to bring in");
     u32x4 rb[NBK], rc[NBK], rx[NX];
-    // Rows behind the segment's end repeat its last one: their dt is 0, so they add nothing.
+    // A thread's vectors of a chunk are NTH V elements apart: whole rows, one column.  Their places are
+    // 32-bit offsets (the host has checked that a chunk spans less than 2 GiB) from scalar addresses.
+    constexpr int RBK = NTH * V / DK, RX = NTH * V / (HB * DV);         // rows from one vector to the next
+    static_assert(RBK * DK == NTH * V && RX * HB * DV == NTH * V, "whole rows");
+    const uint32_t bk_row = threadIdx.x * V / DK, bk_col = threadIdx.x * V % DK;
+    const uint32_t x_row = threadIdx.x * V / (HB * DV), x_col = threadIdx.x * V % (HB * DV);
+    const uint32_t b_at = bk_row * (uint32_t)a.bs + bk_col, c_at = bk_row * (uint32_t)a.cs + bk_col;
+    const uint32_t x_at = x_row * (uint32_t)a.xs + x_col;
     auto fetch = [&](int64_t t0) {
-        const uint32_t lastrow = send - t0 < CH ? (uint32_t)(send - t0 - 1) : CH - 1;
         const T *b = Bp + t0 * a.bs, *c = Cp + t0 * a.cs, *x = Xp + t0 * a.xs;
-        const uint32_t tid = here(threadIdx.x);
+        if (send - t0 >= CH) {
 #pragma unroll
-        for (int i = 0; i < NBK; ++i) {
-            const uint32_t e = (tid + i * NTH) * V, row = min(e / DK, lastrow);
-            rb[i] = load16(b + (uint64_t)row * (uint32_t)a.bs + e % DK);
-            if (Y) rc[i] = load16(c + (uint64_t)row * (uint32_t)a.cs + e % DK);
-        }
+            for (int i = 0; i < NBK; ++i) {
+                rb[i] = load16(b + i * RBK * a.bs + b_at);
+                if (Y) rc[i] = load16(c + i * RBK * a.cs + c_at);
+            }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const uint32_t e = (tid + i * NTH) * V, row = min(e / (HB * DV), lastrow);
-            rx[i] = load16(x + (uint64_t)row * (uint32_t)a.xs + e % (HB * DV));
+            for (int i = 0; i < NX; ++i) rx[i] = load16(x + i * RX * a.xs + x_at);
+        } else {
+            // rows behind the segment's end repeat its last one: their dt is 0, so they add nothing
+            const uint32_t lastrow = (uint32_t)(send - t0 - 1);
+#pragma unroll
+            for (int i = 0; i < NBK; ++i) {
+                const uint32_t row = min(bk_row + i * RBK, lastrow);
+                rb[i] = load16(b + row * (uint32_t)a.bs + bk_col);
+                if (Y) rc[i] = load16(c + row * (uint32_t)a.cs + bk_col);
+            }
+#pragma unroll
+            for (int i = 0; i < NX; ++i) rx[i] = load16(x + min(x_row + i * RX, lastrow) * (uint32_t)a.xs + x_col);
         }
     };
     // The gates of one head, by one of the last waves (the first ones have more of M): a chunk ahead,
@@ -224,13 +242,23 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
         dt = in ? dt : 0.0f;
         // log2 a; below -1000 it is 0 in fp32 whatever follows, and stays finite here
         const double ga = in ? fmax((double)dt * (double)gA * 1.4426950408889634, -1000.0) : 0.0;
-        const double G = wave_scan(ga), all = last_lane(G);
+        const double G = wave_scan(ga), all = lane_value(G, 63);
         const float hi = (float)G;
         o.hi[lane] = hi;
         o.lo[lane] = (float)(G - (double)hi);
         o.dt[lane] = dt;
         o.w[lane] = __builtin_amdgcn_exp2f((float)(all - G)) * dt;
         o.e[lane] = __builtin_amdgcn_exp2f(hi);
+        if (Y) {
+            double at = 0.0;                         // G at the token in front of this lane's tile
+#pragma unroll
+            for (int t = 1; t < 4; ++t) {
+                const double b = lane_value(G, 16 * t - 1);
+                if (lane >= 16 * t) at = b;
+                o.col[t - 1][lane] = __builtin_amdgcn_exp2f((float)(b - G)) * dt;   // read for lane < 16 t
+            }
+            o.row[lane] = __builtin_amdgcn_exp2f((float)(G - at));
+        }
         if (lane == 0) o.last = __builtin_amdgcn_exp2f((float)all);
         total += all;
     };
@@ -246,18 +274,13 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
     for (int ch = 0; ch < nch; ++ch) {
         const int64_t t0 = sbeg + (int64_t)ch * CH;
         __syncthreads();                             // the last chunk's readers are done
-        const uint32_t tid = here(threadIdx.x);
 #pragma unroll
         for (int i = 0; i < NBK; ++i) {
-            const uint32_t e = (tid + i * NTH) * V;
-            s.B.put16(e / DK, e % DK, rb[i]);
-            if (Y) s.C.put16(e / DK, e % DK, rc[i]);
+            s.B.put16(bk_row + i * RBK, bk_col, rb[i]);
+            if (Y) s.C.put16(bk_row + i * RBK, bk_col, rc[i]);
         }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const uint32_t e = (tid + i * NTH) * V;
-            s.X.put16(e / (HB * DV), e % (HB * DV), rx[i]);
-        }
+        for (int i = 0; i < NX; ++i) s.X.put16(x_row + i * RX, x_col, rx[i]);
         __syncthreads();
         if (ch + 1 < nch) fetch(t0 + CH);
         const Gates &gt = s.gate[ch & 1][hl];
@@ -277,14 +300,21 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
 #pragma unroll
                 for (int q = 0; q < HB; ++q) {
                     const Gates &z = s.gate[ch & 1][q];
-                    const float hi = z.hi[i], lo = z.lo[i];
-                    const f32x4 hj = *reinterpret_cast<const f32x4 *>(&z.hi[j0]), lj = *reinterpret_cast<const f32x4 *>(&z.lo[j0]);
-                    const f32x4 dj = *reinterpret_cast<const f32x4 *>(&z.dt[j0]);
                     float m[4];
+                    if (jt < it) {
+                        const float f = z.row[i];
+                        const f32x4 cj = *reinterpret_cast<const f32x4 *>(&z.col[it - 1][j0]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float d = (hi - hj[k]) + (lo - lj[k]);
-                        m[k] = j0 + k <= i ? cb[k] * (__builtin_amdgcn_exp2f(d) * dj[k]) : 0.0f;
+                        for (int k = 0; k < 4; ++k) m[k] = cb[k] * (f * cj[k]);
+                    } else {
+                        const float hi = z.hi[i], lo = z.lo[i];
+                        const f32x4 hj = *reinterpret_cast<const f32x4 *>(&z.hi[j0]), lj = *reinterpret_cast<const f32x4 *>(&z.lo[j0]);
+                        const f32x4 dj = *reinterpret_cast<const f32x4 *>(&z.dt[j0]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float d = (hi - hj[k]) + (lo - lj[k]);
+                            m[k] = j0 + k <= i ? cb[k] * (__builtin_amdgcn_exp2f(d) * dj[k]) : 0.0f;
+                        }
                     }
                     s.Mx[q].put4(i, j0, m);
                 }
@@ -343,11 +373,12 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
                 }
             const float D = a.D ? a.D[h] : 0.0f;
             const int left = send - t0 < CH ? (int)(send - t0) : CH;
-            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0 + 4 * g;
+            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0;
+            const uint32_t y_at = col * (uint32_t)a.ys + 4 * g;
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const int i = 16 * it + col;
-                T *yi = yp + (uint64_t)(uint32_t)i * (uint32_t)a.ys;
+                T *yi = yp + 16 * it * a.ys + y_at;
 #pragma unroll
                 for (int pt = 0; pt < WT; ++pt) {
                     float x[4], o[4];
@@ -368,8 +399,8 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             constexpr int TERMS = V == 4 || MODE == MODE_OUT ? 1 : 3;
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + 4 * g]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + 16 + 4 * g]);
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + Bt::LANE * g]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + Bt::LANE * g + Bt::HALF]);
             Frag wx[WT][TERMS];
 #pragma unroll
             for (int pt = 0; pt < WT; ++pt) {
@@ -390,7 +421,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
             }
 #pragma unroll
             for (int kt = 0; kt < DK / 16; ++kt) {
-                const Frag bf = s.B.col(kb, kt, lane);
+                const Frag bf = s.B.spread(kb, kt, lane);
 #pragma unroll
                 for (int pt = 0; pt < WT; ++pt)
 #pragma unroll
@@ -405,7 +436,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
 #pragma unroll
         for (int pt = 0; pt < WT; ++pt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) So[(16 * kt + 4 * g + i) * DV + p0 + 16 * pt + col] = S[kt][pt][i];
+            for (int i = 0; i < 4; ++i) So[Bt::state_row(kt, g, i) * DV + p0 + 16 * pt + col] = S[kt][pt][i];
     if (a.segs > 1 && gates && lane == 0)
         a.seg_decay[((int64_t)n * a.segs + seg) * a.h_v + gh] = (float)exp2(total);
 }

@@ -293,7 +293,8 @@ typedef struct {
     int32_t softplus;          /* 1: softplus over dt + dt_bias, 0: the sum itself */
     int64_t total_tokens;      /* rows of x, B, C, dt; gdn_ssm_step: n_seqs */
     int64_t total_out_tokens;  /* rows of y: total_tokens, or sum r[n] with replay lengths */
-    int64_t x_stride, b_stride, c_stride, dt_stride, y_stride;   /* dt_stride: any >= h_v */
+    int64_t x_stride, b_stride, c_stride, dt_stride, y_stride;   /* dt_stride: any >= h_v;
+                                  gdn_ssm_scan: 64 rows span less than 2 GiB */
 } gdn_ssm_desc;
 
 /* Bytes of gdn_ssm_scan's workspace: 256, and for few long sequences the states of the segments
