@@ -61,8 +61,27 @@ __device__ __forceinline__ uint32_t xcd_block(uint32_t unit) {
     return ((i / unit) * 8 + x) * unit + i % unit;
 }
 
-// ln(1 + e^x): e^-|x| never overflows, and log1p keeps the small values of very negative x.
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
+// ln(1 + e^x) = max(x, 0) + ln(1 + z), z = e^-|x| in (0, 1].  The exponential's argument is kept in two
+// floats; ln(1 + z) = 2 atanh(s), s = z / (2 + z) <= 1/3, by its series up to s^15 (the next term is
+// below 3e-9 of the sum), which also keeps the small values of very negative x.
+__device__ __forceinline__ float softplus(float x) {
+    const float a = -fabsf(x);
+    const float p = a * 1.4426950408889634f;
+    const float r = fmaf(a, 1.4426950408889634f, -p) + a * 1.925963033500e-8f;     // log2 e in two floats
+    const float z = __builtin_amdgcn_exp2f(p) * fmaf(r, 0.6931471805599453f, 1.0f);
+    const float d = 2.0f + z;
+    float q = __builtin_amdgcn_rcpf(d);
+    q = fmaf(fmaf(-d, q, 1.0f), q, q);
+    const float s = z * q, t = s * s;
+    float u = 1.0f / 15.0f;
+    u = fmaf(u, t, 1.0f / 13.0f);
+    u = fmaf(u, t, 1.0f / 11.0f);
+    u = fmaf(u, t, 1.0f / 9.0f);
+    u = fmaf(u, t, 1.0f / 7.0f);
+    u = fmaf(u, t, 1.0f / 5.0f);
+    u = fmaf(u, t, 1.0f / 3.0f);
+    return fmaxf(x, 0.0f) + 2.0f * fmaf(s * t, u, s);
+}
 
 // The value, in a register of its own: what is computed from it in a loop stays in the loop instead
 // of being kept in registers over it.

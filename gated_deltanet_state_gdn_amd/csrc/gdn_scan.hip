@@ -12,8 +12,8 @@
 // decays in front of weak ones cost the weak ones nothing.
 //
 // Work decomposition: a workgroup takes HB heads of one group over one segment of one sequence,
-// chunk by chunk.  The columns of S (d_v of every head) do not mix, so every wave owns one or two
-// 16-column tiles of S whole, in its accumulators; M is the only product the waves share, and
+// chunk by chunk.  The columns of S (d_v of every head) do not mix, so every wave owns a
+// 16-column tile of S whole, in its accumulators; M is the only product the waves share, and
 // goes through LDS.  Y is formed transposed (Y^T = S^T C^T + X^T M^T): accumulators of S become
 // operands where they are, and a lane ends with four consecutive entries of one token's y.
 //
@@ -93,6 +93,10 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
 // What a chunk's gates are to the products, per head and token.
 struct Gates {
     float hi[CH], lo[CH];                // G log2 e in two floats
@@ -110,13 +114,13 @@ struct Lds {
     Tile2<M, CH, CH> Mx[HB];             // M, row i
     alignas(16) Gates gate[2][HB];       // this chunk's and the next one's
 };
-// 16-column tiles of S that a wave owns: with two, the operands that every wave reads (C, B^T) serve
-// twice; bf16 workgroups of 128 columns then have four waves.
-template <class M, int DV, int HB>
-constexpr int wave_tiles() { return M::V == 8 && HB * DV == 128 ? 2 : 1; }
+// 16-column tiles of S that a wave owns.  Two would halve the reads of C and B^T (which every wave
+// reads whole) and leave two waves a SIMD instead of four: one sequence of 32768 tokens, 32 heads took
+// 82 + 143 us with two and 75 + 133 us with one (states, outputs).
+constexpr int WT = 1;
 
-template <class M, int DK, int DV, int HB, int MODE, int WT>
-__global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
+template <class M, int DK, int DV, int HB, int MODE>
+__global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 ? 4 : 2) scan_kernel(ScanArgs a)
 {
     typedef typename M::T T;
     typedef typename M::Frag Frag;
@@ -234,6 +238,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
         const int64_t t = t0 + lane < send ? t0 + lane : send - 1;
         return M::one(dtp + t * a.dts);
     };
+    const double gL = (double)gA * 1.4426950408889634;
     double total = 0.0;                              // log2 of the decay since the segment's start
     auto form_gates = [&](int64_t t0, float raw, Gates &o) {
         const bool in = t0 + lane < send;
@@ -241,25 +246,26 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
         if (a.softplus) dt = softplus(dt);
         dt = in ? dt : 0.0f;
         // log2 a; below -1000 it is 0 in fp32 whatever follows, and stays finite here
-        const double ga = in ? fmax((double)dt * (double)gA * 1.4426950408889634, -1000.0) : 0.0;
-        const double G = wave_scan(ga), all = lane_value(G, 63);
-        const float hi = (float)G;
+        const double G = wave_scan(in ? fmax((double)dt * gL, -1000.0) : 0.0), all = lane_value(G, 63);
+        const float hi = (float)G, lo = (float)(G - (double)hi);
+        // 2^(G at lane l - G), and the reverse
+        auto from = [&](int l) { return (lane_value(hi, l) - hi) + (lane_value(lo, l) - lo); };
         o.hi[lane] = hi;
-        o.lo[lane] = (float)(G - (double)hi);
+        o.lo[lane] = lo;
         o.dt[lane] = dt;
-        o.w[lane] = __builtin_amdgcn_exp2f((float)(all - G)) * dt;
-        o.e[lane] = __builtin_amdgcn_exp2f(hi);
+        o.w[lane] = __builtin_amdgcn_exp2f(from(63)) * dt;
+        if (lane == 0) o.last = __builtin_amdgcn_exp2f((float)all);
         if (Y) {
-            double at = 0.0;                         // G at the token in front of this lane's tile
+            o.e[lane] = __builtin_amdgcn_exp2f(hi);
+            float at = 0.0f;                         // G - G at the token in front of this lane's tile
 #pragma unroll
             for (int t = 1; t < 4; ++t) {
-                const double b = lane_value(G, 16 * t - 1);
+                const float b = from(16 * t - 1);
                 if (lane >= 16 * t) at = b;
-                o.col[t - 1][lane] = __builtin_amdgcn_exp2f((float)(b - G)) * dt;   // read for lane < 16 t
+                o.col[t - 1][lane] = __builtin_amdgcn_exp2f(b) * dt;   // read for lane < 16 t
             }
-            o.row[lane] = __builtin_amdgcn_exp2f((float)(G - at));
+            o.row[lane] = __builtin_amdgcn_exp2f(-at);
         }
-        if (lane == 0) o.last = __builtin_amdgcn_exp2f((float)all);
         total += all;
     };
     float rdt = 0.0f;
@@ -354,7 +360,6 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
 #pragma unroll
                 for (int pt = 0; pt < WT; ++pt) yt[it][pt] *= e;
             }
-            __syncthreads();                         // M is whole
         }
         // X^T: rows p for Y^T, and (the same registers) columns p for the state
         Frag xf[2][WT];
@@ -362,35 +367,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int pt = 0; pt < WT; ++pt) xf[kb][pt] = s.X.col(kb, c0 / 16 + pt, lane);
-        if (Y) {
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int kb = 0; kb <= it / 2; ++kb) {
-                    const Frag mf = s.Mx[hl].row(16 * it, kb, lane);
-#pragma unroll
-                    for (int pt = 0; pt < WT; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
-                }
-            const float D = a.D ? a.D[h] : 0.0f;
-            const int left = send - t0 < CH ? (int)(send - t0) : CH;
-            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0;
-            const uint32_t y_at = col * (uint32_t)a.ys + 4 * g;
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int i = 16 * it + col;
-                T *yi = yp + 16 * it * a.ys + y_at;
-#pragma unroll
-                for (int pt = 0; pt < WT; ++pt) {
-                    float x[4], o[4];
-                    s.X.get4(i, c0 + 16 * pt + 4 * g, x);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
-                    if (i < left) M::store4(yi + 16 * pt, o);
-                }
-            }
-        }
         // the state; the outputs alone (MODE_OUT) only need it to the precision of C S
-        if (MODE == MODE_OUT && ch + 1 == nch) break;
         const float last = gt.last;
 #pragma unroll
         for (int kt = 0; kt < DK / 16; ++kt)
@@ -426,6 +403,34 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, 2) scan_kernel(ScanArgs a)
                 for (int pt = 0; pt < WT; ++pt)
 #pragma unroll
                     for (int term = TERMS - 1; term >= 0; --term) S[kt][pt] = M::mma(S[kt][pt], bf, wx[pt][term]);
+            }
+        }
+        if (Y) {
+            __syncthreads();                         // M is whole
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int kb = 0; kb <= it / 2; ++kb) {
+                    const Frag mf = s.Mx[hl].row(16 * it, kb, lane);
+#pragma unroll
+                    for (int pt = 0; pt < WT; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
+                }
+            const float D = a.D ? a.D[h] : 0.0f;
+            const int left = send - t0 < CH ? (int)(send - t0) : CH;
+            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0;
+            const uint32_t y_at = col * (uint32_t)a.ys + 4 * g;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int i = 16 * it + col;
+                T *yi = yp + 16 * it * a.ys + y_at;
+#pragma unroll
+                for (int pt = 0; pt < WT; ++pt) {
+                    float x[4], o[4];
+                    s.X.get4(i, c0 + 16 * pt + 4 * g, x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
+                    if (i < left) M::store4(yi + 16 * pt, o);
+                }
             }
         }
     }
@@ -509,8 +514,7 @@ hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
     static_assert(bytes <= 160 * 1024, "one workgroup's LDS");
     const int64_t blocks = (int64_t)a.n_seqs * a.segs * (a.h_v / HB);
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-    constexpr int WT = wave_tiles<M, DV, HB>();
-    auto k = scan_kernel<M, DK, DV, HB, MODE, WT>;
+    auto k = scan_kernel<M, DK, DV, HB, MODE>;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
