@@ -129,19 +129,21 @@ struct Soft {
         sum += __shfl_xor(sum, 32);
         m = sum > 0.0f ? -neg[b] : -INFINITY;
     }
-    // scale > 0; the lane's keys are key0 + i and key0 + 16 + i, i = 0..3
+    // scale > 0; the lane's keys are key0 + i and key0 + 16 + i, i = 0..3; limit(b): keys that its row sees
     // TERMS: P in that many terms of the element type (two bf16 terms hold 16 bits)
-    template <class M, int D, int TERMS>
-    __device__ __forceinline__ void step(f32x4 (&st)[NB][2], float scale, int32_t key0, const int32_t (&limit)[NB],
-                                         bool masked, f32x4 (&o)[NB][D / 16], typename M::Frag (&p)[NB][TERMS]) {
+    template <class M, int D, int TERMS, class Limit>
+    __device__ __forceinline__ void step(f32x4 (&st)[NB][2], float scale, int32_t key0, Limit limit, bool masked,
+                                         f32x4 (&o)[NB][D / 16], typename M::Frag (&p)[NB][TERMS]) {
         float top[NB], over = -INFINITY;
         if (masked) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) {
+                const int32_t end = limit(b) - key0;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) st[b][t][i] = key0 + 16 * t + i >= limit[b] ? -INFINITY : st[b][t][i];
+                    for (int i = 0; i < 4; ++i) st[b][t][i] = 16 * t + i >= end ? -INFINITY : st[b][t][i];
+            }
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -155,7 +157,7 @@ struct Soft {
                 float t = fmaxf(top[b], __shfl_xor(top[b], 16));
                 t = fmaxf(t, __shfl_xor(t, 32)) * scale;
                 const float base = fmaxf(t, -neg[b]);
-                const float f = exp2f(-neg[b] - base);   // 0 at the first key
+                const float f = __builtin_amdgcn_exp2f(-neg[b] - base);   // 0 at the first key
                 neg[b] = -base;
                 l[b] *= f;
 #pragma unroll
@@ -180,6 +182,7 @@ struct Soft {
                     for (int i = 0; i < 8; ++i) s[i] -= got[i];
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);           // one row tile's temporaries at a time
         }
     }
 };
@@ -260,6 +263,13 @@ struct Tile {
         }
     }
 };
+// The factor of the scores, in a scalar register: log2 units, positive (0 becomes a number so small
+// that every score is as good as 0).
+__device__ __forceinline__ float score_scale(const AttnArgs &a) {
+    const float s = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+    return __uint_as_float(__builtin_amdgcn_readfirstlane((int)__float_as_uint(s)));
+}
+
 // Waits until at most N of the wave's last loads are on their way (they return in order), and until
 // all its LDS reads are done.  The compiler counts with these builtins, and no access moves over them.
 __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
@@ -352,11 +362,9 @@ __global__ void __launch_bounds__(64 * WAVES) decode_kernel(AttnArgs a)
         fetch_v(0);
         wait_loads<(2 * NI < 63 ? 2 * NI : 63)>();       // what is in registers is here
     }
-    int32_t limit[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) limit[b] = row_limit(r, r.m0 + 16 * b + col);
+    auto limit = [&](int b) { return row_limit(r, r.m0 + 16 * b + col); };
     const int32_t least = row_limit(r, r.m0);
-    const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // 0: every score is as good as 0
+    const float scale = score_scale(a);
     Soft<NB> sf;
     f32x4 o[NB][D / 16];
 #pragma unroll
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
     typedef typename M::T T;
     typedef typename M::Frag Frag;
     typedef Tile<M, D> Tl;
-    constexpr bool FENCE = D == 256;
+    constexpr int PRE = 6 < D / 16 ? 6 : D / 16;
     constexpr int ROWS = 16 * NB * WAVES, RB = Tl::RB, CPR = Tl::CPR;
     constexpr int NI = KT * RB / 1024 / WAVES;           // 1 KB loads of a wave for one tile of K or V
     static_assert(NI >= 1, "a tile has work for every wave");
@@ -467,11 +475,9 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 
     Frag q[NB][D / 32];
     load_q<M, D, NB>(a, r, hk, first, lane, q);
-    int32_t limit[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) limit[b] = row_limit(r, r.m0 + first + 16 * b + col);
+    auto limit = [&](int b) { return row_limit(r, r.m0 + first + 16 * b + (int)here(col)); };
     const int32_t least = row_limit(r, r.m0 + first);
-    const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // 0: every score is as good as 0
+    const float scale = score_scale(a);
     Soft<NB> sf;
     f32x4 o[NB][D / 16];
 #pragma unroll
@@ -480,7 +486,12 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
         for (int d = 0; d < D / 16; ++d) o[b][d] = f32x4{0, 0, 0, 0};
 
     const int nt = k_end > k_beg ? (k_end - k_beg + KT - 1) / KT : 0;
-    auto key_of = [&](int t) { return find_key(a, table, k_beg + t * KT + (int)threadIdx.x, k_end); };
+    auto key_at_tile = [&](int t) {
+        const int32_t j = k_beg + t * KT + (int)threadIdx.x;
+        return j < k_end ? j : k_end - 1;
+    };
+    auto page_of = [&](int t) { return table[key_at_tile(t) / a.page_size]; };
+    auto place = [&](int t, int32_t page) { off[t & 1][threadIdx.x] = key_row(a, Key{key_at_tile(t), page}, sizeof(T)); };
     auto stage = [&](int t, char *Kb, char *Vb) {
         const int ln = (int)here(lane);
 #pragma unroll
@@ -495,44 +506,54 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
     };
     auto compute = [&](int t, const char *Kb, const char *Vb) {
         const int32_t k0 = k_beg + t * KT;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < KT; k += 32) {
             const uint32_t ka = here(key_at), va = here(value_at);
+            // The wave whose products are next goes first: two waves of a SIMD then take turns, one's
+            // products beside the other's softmax.
+            __builtin_amdgcn_s_setprio(2);
+            // Operands are read PRE steps ahead of their products.  The scheduling barriers hold the
+            // order: short of registers (D = 256) the compiler would wait for each read where it is
+            // used, an LDS latency for every two products.
             f32x4 st[NB][2];
+            Frag ring[PRE];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int i = 0; i < PRE; ++i) ring[i] = Tl::key(Kb, k / 16 + (i & 1), i >> 1, ka);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) st[b][h] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < D / 16; ++i) {           // entries 32 (i / 2) .. of the keys 16 (i % 2) ..
+                const int h = i & 1, kb = i >> 1;
 #pragma unroll
-                for (int kb = 0; kb < D / 32; ++kb) {
-                    const Frag kf = Tl::key(Kb, k / 16 + h, kb, ka);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) st[b][h] = M::mma(st[b][h], kf, q[b][kb]);
-                    if (FENCE && kb % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-                }
+                for (int b = 0; b < NB; ++b) st[b][h] = M::mma(kb == 0 ? f32x4{0, 0, 0, 0} : st[b][h], ring[i % PRE], q[b][kb]);
+                const int n = i + PRE;
+                if (n < D / 16) ring[i % PRE] = Tl::key(Kb, k / 16 + (n & 1), n >> 1, ka);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            __builtin_amdgcn_s_setprio(0);
             Frag p[NB][1];
             sf.template step<M, D, 1>(st, scale, k0 + k + 4 * g, limit, k0 + k + 32 > least, o, p);
-            if (FENCE) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < PRE; ++i) ring[i] = Tl::value(Vb, k, i, va);
+            __builtin_amdgcn_s_setprio(2);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
-                const Frag vf = Tl::value(Vb, k, d, va);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], vf, p[b][0]);
-                if (FENCE && d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], ring[d % PRE], p[b][0]);
+                if (d + PRE < D / 16) ring[d % PRE] = Tl::value(Vb, k, d + PRE, va);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
     auto turn = [&](int t, char *Kb, char *Vb, char *Kn, char *Vn) {
         __syncthreads();                                 // this tile is here, the other buffer is free
         const bool ahead = t + 2 < nt && threadIdx.x < KT;
-        Key key = {0, 0};
-        if (ahead) key = key_of(t + 2);
+        int32_t page = 0;
+        if (ahead) page = page_of(t + 2);
         fence();
         if (t + 1 < nt) stage(t + 1, Kn, Vn);
-        if (FENCE) __builtin_amdgcn_sched_barrier(0);
         compute(t, Kb, Vb);
-        if (ahead) off[t & 1][threadIdx.x] = key_row(a, key, sizeof(T));
+        if (ahead) place(t + 2, page);
     };
     if (nt > 0) {
         if (a.n_pages == 0) {                            // no page at all: nothing can be read
@@ -540,8 +561,8 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
             return;
         }
         if (threadIdx.x < KT) {
-            off[0][threadIdx.x] = key_row(a, key_of(0), sizeof(T));
-            if (nt > 1) off[1][threadIdx.x] = key_row(a, key_of(1), sizeof(T));
+            place(0, page_of(0));
+            if (nt > 1) place(1, page_of(1));
         }
         __syncthreads();
         stage(0, K0, V0);
@@ -677,10 +698,10 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     p.rows = p.decode ? 16 : bf16 && total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
     // fp32 products take long beside a split's share: many splits, for their even spread
-    int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 4096) / (tiles > 0 ? tiles : 1);
+    int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;
     int64_t keys = (max_kv + want - 1) / want;
-    const int64_t least = p.decode ? 128 : bf16 ? 1024 : 256;
+    const int64_t least = p.decode ? 128 : bf16 ? 1024 : 512;
     if (keys < least) keys = least;
     p.split_keys = (int32_t)((keys + 127) / 128 * 128);
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
