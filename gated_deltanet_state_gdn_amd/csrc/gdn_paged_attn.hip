@@ -286,10 +286,10 @@ __device__ __forceinline__ void wait_reads() {
 }
 
 // ------------------------------------------------------------- few rows: waves over the keys
-// Waves of a workgroup: two workgroups' tiles fit the LDS of a CU, so that one's first loads and
-// last sums overlap with the other's keys.
+// Waves of a workgroup: two workgroups' tiles fit the LDS of a CU (rows of 1 KB aside), so that one's
+// first loads and last sums overlap with the other's keys.
 template <class M, int D>
-constexpr int decode_waves() { return Tile<M, D>::RB >= 1024 ? 1 : Tile<M, D>::RB >= 512 ? 2 : 4; }
+constexpr int decode_waves() { return Tile<M, D>::RB >= 512 ? 2 : 4; }
 
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
@@ -663,13 +663,10 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
         constexpr int WAVES = decode_waves<M, D>();
         e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
     } else {
-        // fp32 rows of 256 entries: the operands and sums of 16 rows fill a wave's registers
-        constexpr bool WIDE = D * sizeof(typename M::T) > 512;
-        constexpr int NB = WIDE ? 1 : 2, KT = WIDE ? 32 : 64;
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
-        if constexpr (WIDE) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, a, stream, 512);
-        else if (p.rows == 256) e = start(prefill_kernel<M, D, NB, 8, KT>, blocks, a, stream, 512);
-        else e = start(prefill_kernel<M, D, NB, 4, KT>, blocks, a, stream, 256);
+        if constexpr (M::V == 4) e = start(prefill_kernel<M, D, 1, 4, 32>, blocks, a, stream, 256);
+        else if (p.rows == 256) e = start(prefill_kernel<M, D, 2, 8, 64>, blocks, a, stream, 512);
+        else e = start(prefill_kernel<M, D, 2, 4, 64>, blocks, a, stream, 256);
     }
     if (e != hipSuccess || a.splits == 1) return e;
     constexpr int R = NT / (D / 4);                      // rows of a workgroup without slices
@@ -695,14 +692,15 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     const int64_t G = h_q / h_kv;
     AttnPlan p;
     p.decode = total * G <= 32 * (int64_t)n_seqs;
-    p.rows = p.decode ? 16 : bf16 && total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
+    // bf16: 256 rows share a tile of keys where sequences have them, for one workgroup a CU.  fp32
+    // products take sixteen times as long and the reads beside them do not count: 64 rows, and splits
+    // for several workgroups a CU, for their even spread.
+    p.rows = p.decode ? 16 : !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
-    // fp32 products take long beside a split's share: many splits, for their even spread
     int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;
     int64_t keys = (max_kv + want - 1) / want;
-    const int64_t least = p.decode ? 128 : bf16 ? 1024 : 512;
-    if (keys < least) keys = least;
+    if (keys < 128) keys = 128;
     p.split_keys = (int32_t)((keys + 127) / 128 * 128);
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
     (void)d;

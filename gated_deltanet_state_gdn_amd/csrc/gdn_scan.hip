@@ -34,6 +34,15 @@ constexpr int CH = 64;      // tokens of a chunk
 constexpr int NT = 256;
 constexpr int MODE_FULL = 0, MODE_STATE = 1, MODE_OUT = 2;
 
+// Columns of a workgroup, for a launch over so many in all.  128 (two heads of 64 of a group, or one
+// of 128) read B and C and form C B^T half as often; 64 spread over twice as many CUs, which counts
+// where there are few workgroups, and for fp32, whose products keep a CU busy alone.
+int scan_columns(int32_t h_qk, int32_t h_v, int32_t d_v, int bf16, int64_t columns)
+{
+    if (!bf16 || columns / 128 < 256) return 64;
+    return d_v == 128 || (h_v / h_qk) % 2 == 0 ? 128 : 64;
+}
+
 // The window of sequence n: its tokens [beg, end), false if cu or r is bad.
 __device__ __forceinline__ bool window(const ScanArgs &a, int n, int64_t &beg, int64_t &end) {
     const int32_t b = a.cu[n], e = a.cu[n + 1];
@@ -107,10 +116,11 @@ struct Gates {
     float row[CH], col[3][CH];
     float last;                          // exp(G_last)
 };
-template <class M, int DK, int DV, int HB>
+// COLS columns of a workgroup: HB = COLS / DV whole heads, or 64 of a head's 128.
+template <class M, int DK, int COLS, int HB>
 struct Lds {
     Tile2<M, CH, DK> B, C;
-    Tile2<M, CH, HB * DV> X;
+    Tile2<M, CH, COLS> X;
     Tile2<M, CH, CH> Mx[HB];             // M, row i
     alignas(16) Gates gate[2][HB];       // this chunk's and the next one's
 };
@@ -119,15 +129,16 @@ struct Lds {
 // 82 + 143 us with two and 75 + 133 us with one (states, outputs).
 constexpr int WT = 1;
 
-template <class M, int DK, int DV, int HB, int MODE>
-__global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 ? 4 : 2) scan_kernel(ScanArgs a)
+template <class M, int DK, int DV, int COLS, int MODE>
+__global__ void __launch_bounds__(COLS * 4 / WT, M::V == 8 && COLS == 128 ? 4 : 2) scan_kernel(ScanArgs a)
 {
+    constexpr int HB = COLS >= DV ? COLS / DV : 1, PARTS = COLS >= DV ? 1 : DV / COLS;
     typedef typename M::T T;
     typedef typename M::Frag Frag;
-    typedef Lds<M, DK, DV, HB> L;
+    typedef Lds<M, DK, COLS, HB> L;
     typedef Tile2<M, CH, DK> Bt;
     constexpr int V = M::V;
-    constexpr int WAVES = HB * DV / 16 / WT, NTH = 64 * WAVES;
+    constexpr int WAVES = COLS / 16 / WT, NTH = 64 * WAVES;
     constexpr bool Y = MODE != MODE_STATE;
     extern __shared__ __align__(16) char smem[];
     L &s = *reinterpret_cast<L *>(smem);
@@ -136,12 +147,12 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 
 
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
     // the heads of a segment next to each other: those of a group read the same B and C
-    const int hblocks = a.h_v / HB;
-    const uint32_t block = xcd_block(a.h_v / a.h_qk / HB);
+    const int hblocks = a.h_v / HB * PARTS;
+    const uint32_t block = xcd_block(a.h_v / a.h_qk / HB * PARTS);
     const int hb = block % hblocks;
     const int seg = (block / hblocks) % a.segs;
     const int n = block / hblocks / a.segs;
-    const int h0 = hb * HB;
+    const int h0 = hb / PARTS * HB, part = hb % PARTS * COLS;   // first head; first column of its part
     int64_t beg, end;
     if (!window(a, n, beg, end)) {
         if (threadIdx.x == 0) set_status(a.status);
@@ -162,9 +173,9 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 
     if (a.segs > 1 && sbeg >= end) return;           // an empty segment: nothing reads its state
     const int nch = sbeg < send ? (int)((send - sbeg + CH - 1) / CH) : 0;
 
-    const int c0 = wave * 16 * WT;                   // this wave's columns within the block's HB * DV
+    const int c0 = wave * 16 * WT;                   // this wave's columns within the block's
     const int hl = c0 / DV, h = h0 + hl;             // their head
-    const int p0 = c0 - hl * DV;                     // and within the head
+    const int p0 = part + c0 - hl * DV;              // and within the head
     const int64_t state = (((int64_t)n * a.segs + seg) * a.h_v + h) * DK * DV;
     const float *Sin = nullptr;
     if (MODE == MODE_OUT) Sin = a.seg_state + state;
@@ -192,16 +203,16 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 
     const int gq = h0 / (a.h_v / a.h_qk);            // the group's B and C
     const T *Bp = static_cast<const T *>(a.B) + (int64_t)gq * DK;
     const T *Cp = static_cast<const T *>(a.C) + (int64_t)gq * DK;
-    const T *Xp = static_cast<const T *>(a.x) + (int64_t)h0 * DV;
-    constexpr int NBK = CH * DK / V / NTH, NX = CH * HB * DV / V / NTH;
+    const T *Xp = static_cast<const T *>(a.x) + (int64_t)h0 * DV + part;
+    constexpr int NBK = CH * DK / V / NTH, NX = CH * COLS / V / NTH;
     static_assert(NBK >= 1 && NX >= 1, "every thread has vectors of a chunk to bring in");
     u32x4 rb[NBK], rc[NBK], rx[NX];
     // A thread's vectors of a chunk are NTH V elements apart: whole rows, one column.  Their places are
     // 32-bit offsets (the host has checked that a chunk spans less than 2 GiB) from scalar addresses.
-    constexpr int RBK = NTH * V / DK, RX = NTH * V / (HB * DV);         // rows from one vector to the next
-    static_assert(RBK * DK == NTH * V && RX * HB * DV == NTH * V, "whole rows");
+    constexpr int RBK = NTH * V / DK, RX = NTH * V / COLS;         // rows from one vector to the next
+    static_assert(RBK * DK == NTH * V && RX * COLS == NTH * V, "whole rows");
     const uint32_t bk_row = threadIdx.x * V / DK, bk_col = threadIdx.x * V % DK;
-    const uint32_t x_row = threadIdx.x * V / (HB * DV), x_col = threadIdx.x * V % (HB * DV);
+    const uint32_t x_row = threadIdx.x * V / COLS, x_col = threadIdx.x * V % COLS;
     const uint32_t b_at = bk_row * (uint32_t)a.bs + bk_col, c_at = bk_row * (uint32_t)a.cs + bk_col;
     const uint32_t x_at = x_row * (uint32_t)a.xs + x_col;
     auto fetch = [&](int64_t t0) {
@@ -361,13 +372,42 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 
                 for (int pt = 0; pt < WT; ++pt) yt[it][pt] *= e;
             }
         }
+        if (Y) __syncthreads();                      // M is whole
         // X^T: rows p for Y^T, and (the same registers) columns p for the state
         Frag xf[2][WT];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int pt = 0; pt < WT; ++pt) xf[kb][pt] = s.X.col(kb, c0 / 16 + pt, lane);
+        if (Y) {
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int kb = 0; kb <= it / 2; ++kb) {
+                    const Frag mf = s.Mx[hl].row(16 * it, kb, lane);
+#pragma unroll
+                    for (int pt = 0; pt < WT; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
+                }
+            const float D = a.D ? a.D[h] : 0.0f;
+            const int left = send - t0 < CH ? (int)(send - t0) : CH;
+            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0;
+            const uint32_t y_at = col * (uint32_t)a.ys + 4 * g;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int i = 16 * it + col;
+                T *yi = yp + 16 * it * a.ys + y_at;
+#pragma unroll
+                for (int pt = 0; pt < WT; ++pt) {
+                    float x[4], o[4];
+                    s.X.get4(i, c0 + 16 * pt + 4 * g, x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
+                    if (i < left) M::store4(yi + 16 * pt, o);
+                }
+            }
+        }
         // the state; the outputs alone (MODE_OUT) only need it to the precision of C S
+        if (MODE == MODE_OUT && ch + 1 == nch) break;
         const float last = gt.last;
 #pragma unroll
         for (int kt = 0; kt < DK / 16; ++kt)
@@ -405,34 +445,6 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 
                     for (int term = TERMS - 1; term >= 0; --term) S[kt][pt] = M::mma(S[kt][pt], bf, wx[pt][term]);
             }
         }
-        if (Y) {
-            __syncthreads();                         // M is whole
-#pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int kb = 0; kb <= it / 2; ++kb) {
-                    const Frag mf = s.Mx[hl].row(16 * it, kb, lane);
-#pragma unroll
-                    for (int pt = 0; pt < WT; ++pt) yt[it][pt] = M::mma(yt[it][pt], xf[kb][pt], mf);
-                }
-            const float D = a.D ? a.D[h] : 0.0f;
-            const int left = send - t0 < CH ? (int)(send - t0) : CH;
-            T *yp = static_cast<T *>(a.y) + (row0 + (t0 - beg)) * a.ys + (int64_t)h * DV + p0;
-            const uint32_t y_at = col * (uint32_t)a.ys + 4 * g;
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int i = 16 * it + col;
-                T *yi = yp + 16 * it * a.ys + y_at;
-#pragma unroll
-                for (int pt = 0; pt < WT; ++pt) {
-                    float x[4], o[4];
-                    s.X.get4(i, c0 + 16 * pt + 4 * g, x);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[k] = fmaf(D, x[k], yt[it][pt][k]);
-                    if (i < left) M::store4(yi + 16 * pt, o);
-                }
-            }
-        }
     }
     if (MODE == MODE_OUT) return;
     float *So = a.segs > 1 ? a.seg_state + state : a.S_out + state;
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(HB * DV * 4 / WT, M::V == 8 && HB * DV == 128 
         for (int pt = 0; pt < WT; ++pt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) So[Bt::state_row(kt, g, i) * DV + p0 + 16 * pt + col] = S[kt][pt][i];
-    if (a.segs > 1 && gates && lane == 0)
+    if (a.segs > 1 && gates && part == 0 && lane == 0)
         a.seg_decay[((int64_t)n * a.segs + seg) * a.h_v + gh] = (float)exp2(total);
 }
 
@@ -465,7 +477,7 @@ __global__ void __launch_bounds__(NT) chain_kernel(ScanArgs a, int elems)
     float *p = a.seg_state + ((int64_t)n * a.segs * a.h_v + h) * elems + at;
     const float *d = a.seg_decay + (int64_t)n * a.segs * a.h_v + h;
     const int64_t next = (int64_t)a.h_v * elems;
-    constexpr int U = 4;                              // loads in flight: the chain itself is short
+    constexpr int U = 8;                              // loads in flight: the chain itself is short
     for (int s0 = 0; s0 < act; s0 += U) {
         f32x4 l[U];
         float f[U];
@@ -507,49 +519,48 @@ __global__ void __launch_bounds__(64) offsets_kernel(ScanArgs a)
     }
 }
 
-template <class M, int DK, int DV, int HB, int MODE>
+template <class M, int DK, int DV, int COLS, int MODE>
 hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
 {
-    constexpr int bytes = sizeof(Lds<M, DK, DV, HB>);
+    constexpr int bytes = sizeof(Lds<M, DK, COLS, COLS >= DV ? COLS / DV : 1>);
     static_assert(bytes <= 160 * 1024, "one workgroup's LDS");
-    const int64_t blocks = (int64_t)a.n_seqs * a.segs * (a.h_v / HB);
+    const int64_t blocks = (int64_t)a.n_seqs * a.segs * ((int64_t)a.h_v * DV / COLS);
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-    auto k = scan_kernel<M, DK, DV, HB, MODE>;
+    auto k = scan_kernel<M, DK, DV, COLS, MODE>;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(HB * DV * 4 / WT), bytes, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(COLS * 4 / WT), bytes, stream, a);
     return hipGetLastError();
 }
 
-template <class M, int DK, int DV, int HB>
-hipError_t scan_h(const ScanArgs &a, hipStream_t stream)
+template <class M, int DK, int DV, int COLS>
+hipError_t scan_c(const ScanArgs &a, hipStream_t stream)
 {
     if (a.cu_out) {
         hipLaunchKernelGGL(offsets_kernel, dim3(1), dim3(64), 0, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.segs == 1) return a.y ? scan_m<M, DK, DV, HB, MODE_FULL>(a, stream) : scan_m<M, DK, DV, HB, MODE_STATE>(a, stream);
-    hipError_t e = scan_m<M, DK, DV, HB, MODE_STATE>(a, stream);
+    if (a.segs == 1) return a.y ? scan_m<M, DK, DV, COLS, MODE_FULL>(a, stream) : scan_m<M, DK, DV, COLS, MODE_STATE>(a, stream);
+    hipError_t e = scan_m<M, DK, DV, COLS, MODE_STATE>(a, stream);
     if (e != hipSuccess) return e;
     const int64_t blocks = ((int64_t)a.n_seqs * a.h_v * (DK * DV / 4) + NT - 1) / NT;
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(chain_kernel, dim3((unsigned)blocks), dim3(NT), 0, stream, a, DK * DV);
     e = hipGetLastError();
     if (e != hipSuccess || !a.y) return e;
-    return scan_m<M, DK, DV, HB, MODE_OUT>(a, stream);
+    return scan_m<M, DK, DV, COLS, MODE_OUT>(a, stream);
 }
 
 template <class M, int DK>
 hipError_t scan_v(const ScanArgs &a, int d_v, hipStream_t stream)
 {
-    if (d_v == 128) return scan_h<M, DK, 128, 1>(a, stream);
-    // two heads of a group side by side halve the reads of B and C; fp32 tiles fill the LDS alone
+    const int cols = scan_columns(a.h_qk, a.h_v, d_v, M::V == 8, (int64_t)a.n_seqs * a.segs * a.h_v * d_v);
     if constexpr (M::V == 8)
-        if ((a.h_v / a.h_qk) % 2 == 0) return scan_h<M, DK, 64, 2>(a, stream);
-    return scan_h<M, DK, 64, 1>(a, stream);
+        if (cols == 128) return d_v == 128 ? scan_c<M, DK, 128, 128>(a, stream) : scan_c<M, DK, 64, 128>(a, stream);
+    return d_v == 128 ? scan_c<M, DK, 128, 64>(a, stream) : scan_c<M, DK, 64, 64>(a, stream);
 }
 
 }  // namespace
@@ -557,14 +568,17 @@ hipError_t scan_v(const ScanArgs &a, int d_v, hipStream_t stream)
 // bf16: segments for 512 workgroups, the two of every CU that run at once (one sequence of 32768
 // tokens, 32 heads: 207 us; 256: 284, 768: 238, 1024: 225, 2048: 266 us).  fp32: 2048, whose products
 // take long beside the chain of the segments (24 ragged prompts: 41 us; 512: 48, 1024: 46 us).  The
-// longest sequence is not known on the host: a short one's surplus segments are empty and end at once.
+// longest sequence is not known on the host; it is taken as four times the mean.  Where that is a
+// few chunks, two more launches cost more than they save.  A short sequence's surplus segments are
+// empty and end at once.
 int32_t scan_segments(int32_t n_seqs, int32_t h_qk, int32_t h_v, int32_t d_v, int bf16, int64_t tokens)
 {
     if (n_seqs <= 0) return 1;
-    const int hb = bf16 && d_v == 64 && (h_v / h_qk) % 2 == 0 ? 2 : 1;
-    const int64_t chains = (int64_t)n_seqs * (h_v / hb);
+    const int64_t longest = tokens / n_seqs * 4 < tokens ? tokens / n_seqs * 4 : tokens;
+    if (longest <= (bf16 ? 8 : 4) * CH) return 1;
+    const int64_t chains = (int64_t)n_seqs * h_v * d_v / scan_columns(h_qk, h_v, d_v, bf16, 1LL << 40);
     const int64_t chunks = (tokens + CH - 1) / CH;
-    int64_t s = (bf16 ? 512 : 2048) / chains;
+    int64_t s = (bf16 ? 512 : 2048) / (chains > 0 ? chains : 1);
     if (chunks / 2 < s) s = chunks / 2;
     return (int32_t)(s < 1 ? 1 : s);
 }
