@@ -281,9 +281,9 @@ int32_t gdn_qk_norm_rope(const gdn_paged_desc *d, const void *q, const void *k, 
                                                     (d->rot_dim > 0 && !cos_sin))))
         return GDN_ERR_NULL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q_out) ||
-        !aligned4(q_weight) || !aligned4(k_weight) || !aligned4(cos_sin) || !aligned4(block_table) || !aligned4(cu) ||
+        !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin) || !aligned4(block_table) || !aligned4(cu) ||
         !aligned4(kv_len) || !aligned4(positions))
-        return refuse(GDN_ERR_ALIGN, "pointer alignment: 16 bytes required (4 for weights, tables and integer arrays)");
+        return refuse(GDN_ERR_ALIGN, "pointer alignment: 16 bytes required (4 for integer arrays)");
     st = check_ws(ws, ws_bytes, kWorkspaceBytes);
     if (st != GDN_OK || d->n_seqs == 0 || d->total_tokens == 0) return st;
     gdn::RopeArgs a = {};

@@ -15,9 +15,10 @@ namespace {
 
 constexpr int NT = 256;
 
-__device__ __forceinline__ void load8f(const float *p, float *f) {
+template <int N>
+__device__ __forceinline__ void loadf(const float *p, float *f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = p[i];
+    for (int i = 0; i < N; i += 4) ElemF32::unpack(load16(p + i), f + i);
 }
 // Where the last round of heads ends, for groups of `per` heads taken `per` at a time from any start
 __device__ __forceinline__ int first_end(int heads, int per) { return (heads + per - 1) / per * per; }
@@ -73,12 +74,21 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a)
     for (int i = 0; i < 8; ++i) { c[i] = 1.0f; s[i] = 0.0f; }
     if (e0 < a.rot) {
         const float *cs = a.cos_sin + (int64_t)pos * a.rot;
+        if (INTER) {                               // entry e is one of pair e / 2
+            float cp[4], sp[4];
+            loadf<4>(cs + e0 / 2, cp);
+            loadf<4>(cs + half + e0 / 2, sp);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int f = INTER ? (e0 + i) >> 1 : e0 + i < half ? e0 + i : e0 + i - half;
-            const bool first = INTER ? !(i & 1) : e0 + i < half;
-            c[i] = cs[f];
-            s[i] = first ? -cs[half + f] : cs[half + f];
+            for (int i = 0; i < 8; ++i) {
+                c[i] = cp[i / 2];
+                s[i] = i & 1 ? sp[i / 2] : -sp[i / 2];
+            }
+        } else {                                   // entries e and e + half are pair e
+            const int f = e0 < half ? e0 : e0 - half;
+            loadf<8>(cs + f, c);
+            loadf<8>(cs + half + f, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = e0 < half ? -s[i] : s[i];
         }
     }
     const int other = INTER ? l : e0 < half ? l + half / 8 : e0 < a.rot ? l - half / 8 : l;
@@ -89,8 +99,8 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a)
     float wq[8], wk[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) { wq[i] = 1.0f; wk[i] = 1.0f; }
-    if (a.qw) load8f(a.qw + e0, wq);
-    if (a.kw) load8f(a.kw + e0, wk);
+    if (a.qw) loadf<8>(a.qw + e0, wq);
+    if (a.kw) loadf<8>(a.kw + e0, wk);
     // every group of lanes goes round equally often: the exchanges are between all lanes
     for (int h0 = threadIdx.x / L; h0 < first_end(heads, NT / L); h0 += MOST * (NT / L)) {
         if (h0 >= MOST * (NT / L)) fetch(h0);

@@ -578,6 +578,7 @@ int32_t scan_segments(int32_t n_seqs, int32_t h_qk, int32_t h_v, int32_t d_v, in
     if (longest <= (bf16 ? 8 : 4) * CH) return 1;
     const int64_t chains = (int64_t)n_seqs * h_v * d_v / scan_columns(h_qk, h_v, d_v, bf16, 1LL << 40);
     const int64_t chunks = (tokens + CH - 1) / CH;
+    if (chains >= 512) return 1;
     int64_t s = (bf16 ? 512 : 2048) / (chains > 0 ? chains : 1);
     if (chunks / 2 < s) s = chunks / 2;
     return (int32_t)(s < 1 ? 1 : s);
