@@ -294,17 +294,17 @@ constexpr int decode_waves() { return Tile<M, D>::RB >= 512 ? 2 : 4; }
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
 template <class M, int D, int NB, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) decode_kernel(AttnArgs a)
+__global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(AttnArgs a)
 {
     typedef typename M::T T;
     typedef typename M::Frag Frag;
     typedef Tile<M, D> Tl;
     constexpr int ROWS = 16 * NB, KT = 32, RB = Tl::RB, CPR = Tl::CPR;
     constexpr int NI = KT * RB / 1024;                   // 1 KB loads of one tile
-    static_assert(ROWS * D * 4 <= KT * RB, "the join's O fits where the keys were");
+    static_assert(16 * D * 4 <= KT * RB, "the join's O, 16 rows at a time, fits where the keys were");
     __shared__ __align__(1024) char Ks[WAVES][KT * RB], Vs[WAVES][KT * RB];
     __shared__ int64_t off[WAVES][2][KT];
-    __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS];
+    __shared__ float sm[WAVES][16], sl[WAVES][16];
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
@@ -408,35 +408,37 @@ __global__ void __launch_bounds__(64 * WAVES) decode_kernel(AttnArgs a)
         wait_reads();
         if (more) fetch_v(slot);
     }
-    // join the waves: every wave's (m, l, O) to LDS, then one thread per four entries of a row
-    // (16-byte piece c of a row sits at c ^ row: the sixteen rows that a wave writes at once are
-    // then in different banks)
+    // join the waves, 16 rows at a time: every wave's (m, l, O) to LDS, then one thread per four
+    // entries of a row (16-byte piece c of a row sits at c ^ row: the sixteen rows that a wave writes
+    // at once are then in different banks)
     float *Os = reinterpret_cast<float *>(Kw);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        float mx, l;
-        sf.whole(b, mx, l);
-        if (g == 0) { sm[wave][16 * b + col] = mx; sl[wave][16 * b + col] = l; }
+        float m, sum;
+        sf.whole(b, m, sum);
+        if (b > 0) __syncthreads();                      // the last rows are read
+        if (g == 0) { sm[wave][col] = m; sl[wave][col] = sum; }
 #pragma unroll
         for (int d = 0; d < D / 16; ++d)
-            *reinterpret_cast<f32x4 *>(Os + (16 * b + col) * D + 4 * ((4 * d + g) ^ col)) = o[b][d];
-    }
-    __syncthreads();
-    for (int e = threadIdx.x * 4; e < r.count * D; e += 64 * WAVES * 4) {
-        const int row = e / D, d4 = e % D;
-        float mx = sm[0][row];
+            *reinterpret_cast<f32x4 *>(Os + col * D + 4 * ((4 * d + g) ^ col)) = o[b][d];
+        __syncthreads();
+        const int rows = r.count - 16 * b < 16 ? r.count - 16 * b : 16;
+        for (int e = threadIdx.x * 4; e < rows * D; e += 64 * WAVES * 4) {
+            const int row = e / D, d4 = e % D;
+            float mx = sm[0][row];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, sm[w][row]);
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        f32x4 sum = {0, 0, 0, 0};
-        float ll = 0.0f;
+            for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, sm[w][row]);
+            const float base = mx == -INFINITY ? 0.0f : mx;
+            f32x4 all = {0, 0, 0, 0};
+            float ll = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const float f = exp2f(sm[w][row] - base);
-            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(Ks[w]) + row * D + 4 * ((d4 / 4) ^ (row & 15))) * f;
-            ll += sl[w][row] * f;
+            for (int w = 0; w < WAVES; ++w) {
+                const float f = exp2f(sm[w][row] - base);
+                all += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(Ks[w]) + row * D + 4 * ((d4 / 4) ^ row)) * f;
+                ll += sl[w][row] * f;
+            }
+            store_share<M, D>(a, r, hk, split, 16 * b + row, d4, all, mx, ll);
         }
-        store_share<M, D>(a, r, hk, split, row, d4, sum, mx, ll);
     }
 }
 
@@ -659,9 +661,11 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
     const int G = a.h_q / a.h_kv;
     hipError_t e;
     if (p.decode) {
-        const int64_t blocks = (a.total * G / 16 + a.n_seqs) * a.splits * a.h_kv;
+        const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         constexpr int WAVES = decode_waves<M, D>();
-        e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
+        if (p.rows == 16) e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
+        else if constexpr (M::V == 8 || D < 256) e = start(decode_kernel<M, D, 2, WAVES>, blocks, a, stream, 64 * WAVES);
+        else e = hipErrorNotSupported;                   // 32 rows of 256 fp32 entries do not fit the registers
     } else {
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         if constexpr (M::V == 4) e = start(prefill_kernel<M, D, 1, 4, 32>, blocks, a, stream, 256);
@@ -695,15 +699,17 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     // bf16: 256 rows share a tile of keys where sequences have them, for one workgroup a CU.  fp32
     // products take sixteen times as long and the reads beside them do not count: 64 rows, and splits
     // for several workgroups a CU, for their even spread.
-    p.rows = p.decode ? 16 : !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
+    p.rows = p.decode ? (total * G <= 16 * (int64_t)n_seqs || (!bf16 && d == 256) ? 16 : 32) : !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
     int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;
     int64_t keys = (max_kv + want - 1) / want;
-    if (keys < 128) keys = 128;
-    p.split_keys = (int32_t)((keys + 127) / 128 * 128);
+    // at least a tile for each of two waves, two where the context is long enough for many splits all
+    // the same (one token over 8K keys: 14.9 us in splits of 128 keys, 16.3 of 64, 17.5 of 256)
+    const int64_t least = p.decode && max_kv < 4096 ? 64 : 128;
+    if (keys < least) keys = least;
+    p.split_keys = (int32_t)((keys + least - 1) / least * least);
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
-    (void)d;
     return p;
 }
 
