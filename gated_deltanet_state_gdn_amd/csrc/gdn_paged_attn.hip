@@ -20,8 +20,8 @@
 //
 // Precision: scores, maximum, sum, O are fp32.  With bf16 elements the products take q, k and v as
 // they are; P is rounded to bf16 once where the products are the bound (half a bf16 step, as the
-// output is), and taken in two bf16 terms where memory is.  The sum l takes the unrounded P.  Keys behind kv_len are never read: whatever a page holds there (or an
-// unused page) does not matter.
+// output is), and taken in two bf16 terms where memory is.  The sum l takes the unrounded P.
+// Keys behind kv_len are never read: whatever a page holds there (or an unused page) does not matter.
 #include "gdn_mfma.h"
 
 namespace gdn {
@@ -664,8 +664,8 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         constexpr int WAVES = decode_waves<M, D>();
         if (p.rows == 16) e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
-        else if constexpr (M::V == 8 || D < 256) e = start(decode_kernel<M, D, 2, WAVES>, blocks, a, stream, 64 * WAVES);
-        else e = hipErrorNotSupported;                   // 32 rows of 256 fp32 entries do not fit the registers
+        else if constexpr (M::V == 8 && D != 128) e = start(decode_kernel<M, D, 2, WAVES>, blocks, a, stream, 64 * WAVES);
+        else e = hipErrorNotSupported;                   // the plan has no such rows
     } else {
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         if constexpr (M::V == 4) e = start(prefill_kernel<M, D, 1, 4, 32>, blocks, a, stream, 256);
@@ -699,7 +699,12 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     // bf16: 256 rows share a tile of keys where sequences have them, for one workgroup a CU.  fp32
     // products take sixteen times as long and the reads beside them do not count: 64 rows, and splits
     // for several workgroups a CU, for their even spread.
-    p.rows = p.decode ? (total * G <= 16 * (int64_t)n_seqs || (!bf16 && d == 256) ? 16 : 32) : !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
+    // Few rows: 32 to a workgroup read the keys once where 16 would twice (32 ragged sequences of up to
+    // 8K keys, 32 query heads on each of 2 cache heads, d = 64: 32.3 us for 40.4; 16 sequences, 24 heads
+    // on one, d = 256: 31.3 for 42.2).  At d = 128 the first call takes 67.4 us for 59.2 with 16, and
+    // fp32 gains nothing (25.2 for 25.6).
+    if (p.decode) p.rows = bf16 && d != 128 && total * G > 16 * (int64_t)n_seqs ? 32 : 16;
+    else p.rows = !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
     int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;

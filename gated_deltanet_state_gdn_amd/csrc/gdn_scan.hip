@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(COLS * 4 / WT, M::V == 8 && COLS == 128 ? 4 : 
     constexpr int V = M::V;
     constexpr int WAVES = COLS / 16 / WT, NTH = 64 * WAVES;
     constexpr bool Y = MODE != MODE_STATE;
-    extern __shared__ __align__(16) char smem[];
-    L &s = *reinterpret_cast<L *>(smem);
+    __shared__ L s;
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -522,16 +521,10 @@ __global__ void __launch_bounds__(64) offsets_kernel(ScanArgs a)
 template <class M, int DK, int DV, int COLS, int MODE>
 hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
 {
-    constexpr int bytes = sizeof(Lds<M, DK, COLS, COLS >= DV ? COLS / DV : 1>);
-    static_assert(bytes <= 160 * 1024, "one workgroup's LDS");
     const int64_t blocks = (int64_t)a.n_seqs * a.segs * ((int64_t)a.h_v * DV / COLS);
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     auto k = scan_kernel<M, DK, DV, COLS, MODE>;
-    if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(COLS * 4 / WT), bytes, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(COLS * 4 / WT), 0, stream, a);
     return hipGetLastError();
 }
 

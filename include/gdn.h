@@ -279,7 +279,7 @@ int32_t gdn_conv_step(const gdn_conv_desc *desc, const void *x, const float *wei
                       size_t workspace_bytes, void *stream);
 
 /* Selective state space recurrence, per (sequence, head h), group q = floor(h h_qk / h_v):
- *     dt'_t = softplus(dt[t, h] + dt_bias[h])   (softplus = 0: the sum itself),
+ *     dt'_t = softplus(dt[t, h] + dt_bias[h])   (softplus = 0: the sum itself, not negative),
  *     S_t = exp(dt'_t A[h]) S_{t-1} + dt'_t B[t, q] x[t, h]^T,   y_t = S_t^T C[t, q] + D[h] x[t, h],
  * S [d_k, d_v] as in gdn_prefill.  x, y [T, h_v, d_v], B, C [T, h_qk, d_k], dt [T, h_v] have
  * `dtype`; A, dt_bias, D [h_v] are fp32 (the last two nullable); states are fp32.  A is finite
@@ -346,6 +346,7 @@ typedef struct {
 
 /* q_out = rot(q / rms(q) * q_weight), and k likewise and v as it is into the caches at the
  * tokens' positions; rms(x)^2 = mean of x^2 over the head + eps, weights [d] fp32 (NULL: ones).
+ * The weights and cos_sin are 16-byte aligned.
  * cos_sin [max_pos, rot_dim] fp32: the rot_dim / 2 cosines, then sines, of a position; pair i
  * turns (a, b) to (a cos - b sin, b cos + a sin).  positions (nullable) [T]: rotate by these
  * instead of the place in the cache.  q_out may be q.  A token without a place in the cache, or a
