@@ -245,7 +245,8 @@ int32_t gdn_device_status(const void *workspace, void *stream, int32_t *status_h
  * elements from one token's row to the next, the rows themselves are contiguous and start on
  * 16 bytes.  Outputs must not overlap inputs except where it is said.  Rows behind the last
  * sequence (tokens at or after cu_seqlens[n_seqs]) are left as they were.  Non-finite inputs
- * are not checked; what a cache holds behind a sequence's kv_len is never read.
+ * are not checked: a token's reach the outputs of its own sequence only, but may reach those of
+ * the same call's earlier tokens too.  What a cache holds behind a sequence's kv_len is never read.
  *
  * Single-token calls: row i uses state slots[i] of a pool of n_slots states, updated in place;
  * slots NULL: state i.  slots[i] = -1 marks a padded row: neither its state nor its output is

@@ -125,6 +125,11 @@ SCAN = [  # groups, heads, d_k, d_v, lengths, state0, softplus
     (1, 1, 64, 64, [1], True, True), (1, 2, 128, 64, [65, 0, 64, 1, 130], True, True),
     (2, 4, 64, 128, [63, 200], False, True), (2, 2, 128, 128, [129], True, False),
     (1, 4, 64, 64, [1100], True, True),                        # cut into segments
+    # workgroups of 128 columns (bf16): in one launch, and cut into segments with empty ones among them
+    (2, 8, 64, 64, [3, 65, 0, 17, 64, 1, 30, 128] * 8, True, True), (1, 16, 128, 128, [1, 66, 0, 5] * 4 + [9], False, True),
+    (2, 32, 64, 64, [2600, 0, 5, 1500], True, True), (4, 16, 64, 128, [2500, 1700], True, True),
+    (3, 9, 64, 64, [20] * 60, False, True),                    # many workgroups, but three heads to a group
+    (2, 2, 128, 128, [0, 0], True, True),                      # nothing to scan: the states pass through
 ]
 
 
@@ -160,6 +165,7 @@ def scan_check(got_y, got_S, i, inp, lo, hi, S0, dt, softplus, what):
     if got_y is not None:
         R.within(got_y, ref[0], yt, what + ": y")
     R.within(got_S, ref[2], st, what + ": S")
+    return ref, st
 
 
 @TYPES
@@ -178,13 +184,12 @@ def test_scan(dt, g, h, k, p, lens, start, softplus):
     assert G().gdn_device_status(ws) == 0
     assert (y[T:] == 7).all()
     zero = torch.zeros(h, k, p, dtype=torch.float64)
-    for i in range(n):
-        scan_check(y[cu[i]:cu[i + 1]], S[i], i, inp, cu[i], cu[i + 1], R.d(S0[i]) if start else zero, dt, softplus,
-                   "sequence %d" % i)
+    refs = [scan_check(y[cu[i]:cu[i + 1]], S[i], i, inp, cu[i], cu[i + 1], R.d(S0[i]) if start else zero, dt, softplus,
+                       "sequence %d" % i) for i in range(n)]
     S2, none, _ = G().gdn_ssm_scan(**inp, cu_seqlens=ints(cu), softplus=softplus, S0=S0, y_out=None, ws=ws)
     assert none is None
-    for i in range(n):
-        scan_check(None, S2[i], i, inp, cu[i], cu[i + 1], R.d(S0[i]) if start else zero, dt, softplus, "state alone %d" % i)
+    for i, (ref, st) in enumerate(refs):
+        R.within(S2[i], ref[2], st, "state alone %d" % i)
     if start:                                                  # the new state in place of the old one
         G().gdn_ssm_scan(**inp, cu_seqlens=ints(cu), softplus=softplus, S0=S0, S_out=S0, y_out=y, ws=ws)
         assert torch.equal(S0, S)
@@ -424,6 +429,13 @@ ATTN = [  # h_q, h_kv, d, page, lengths, context, heads first
     (4, 4, 128, 1, [2, 1], [40, 3], False), (32, 1, 64, 32, [1, 1], [90, 300], False),
     (8, 2, 128, 16, [70, 1, 0, 130], [0, 200, 5, 33], False), (16, 2, 256, 64, [65], [190], False),
     (3, 1, 64, 48, [129, 2], [0, 64], True), (5, 5, 128, 128, [33], [1], False),
+    # 17 to 32 rows a sequence
+    (24, 1, 64, 16, [1, 1, 0, 1], [300, 5, 9, 64], False), (20, 1, 256, 32, [1, 1], [130, 700], True),
+    (24, 1, 128, 16, [1, 1], [90, 257], False), (8, 2, 64, 16, [8, 3, 0, 9], [500, 0, 7, 31], False),
+    (4, 2, 256, 16, [16, 1, 12], [70, 300, 0], False),
+    # 192 rows a sequence and more: large tiles of rows, one split, a few splits, many
+    (8, 2, 128, 16, [70, 50, 130], [0, 90, 33], False), (4, 1, 256, 64, [300], [700], False),
+    (8, 1, 64, 16, [41, 30, 2], [2100, 0, 64], True),
 ]
 
 
@@ -483,6 +495,18 @@ def test_attention_splits_and_empty_rows(dt, lens, kv):
     attn_check(c, q, o, lse, lens, kv, 0.25, dt)
 
 
+@TYPES
+@pytest.mark.parametrize("lens,kv", [([1, 1], [700, 90]), ([40], [260])])
+def test_attention_scale_of_any_sign(dt, lens, kv):
+    hq, hk, dim = 4, 1, 64
+    r = Rand(21)
+    c = Cache(r, kv, 16, hk, dim, dt)
+    q = r.n(sum(lens), hq, dim, dt=dt)
+    for scale in (0.0, -0.3):
+        o, lse = G().gdn_paged_attn(q, c.k, c.v, c.table, ints(cu_of(lens)), ints(kv), scale=scale, lse=True)
+        attn_check(c, q, o, lse, lens, kv, scale, dt)
+
+
 def test_attention_large_scores():
     # scores of several hundred, rising and falling along the keys: the running maximum matters
     dt, hq, hk, dim, kv = F32, 2, 1, 64, 300
@@ -520,6 +544,138 @@ def test_attention_reports_bad_input():
         assert call(table=t)[0] == bad
         assert call(kv_len=[49, 33])[0] == bad and call(kv_len=[-1, 33])[0] == bad
         assert call(cu=[0, T + 1, T])[0] == bad
+
+
+# ------------------------------------------------------------------ apart
+def test_rows_far_apart():
+    """Rows, states' neighbours and pages more than 2^31 elements apart, against the same call on
+    compact tensors: the same arithmetic, so the same bits."""
+    g = G()
+    r = Rand(3)
+    T, h, hq, hk, dim, ps = 300, 2, 4, 2, 64, 16
+    far = torch.empty(T, 1 << 23, dtype=BF, device="cuda")        # row 299 is 2.5e9 elements in
+    at = [0]
+
+    def place(t):
+        n = t[0].numel()
+        v = far[:, at[0]:at[0] + n].unflatten(1, t.shape[1:])
+        at[0] += -(-n // 8) * 8                                   # the next one starts on 16 bytes
+        v.copy_(t)
+        return v
+
+    cu = ints([0, 290, 300])
+    x, w = r.n(T, 256, dt=BF), r.n(256, 4)
+    y, st = g.gdn_conv(x, w, cu)
+    y2, st2 = g.gdn_conv(place(x), w, cu, y=place(torch.zeros_like(y)))
+    assert torch.equal(y, y2) and torch.equal(st, st2)
+    inp = {n: (t.contiguous() if t is not None else t) for n, t in scan_inputs(r, T, 1, h, 64, 64, BF, True).items()}
+    S, y, _ = g.gdn_ssm_scan(**inp, cu_seqlens=cu)
+    apart = {n: place(t) if n in ("x", "B", "C") else t for n, t in inp.items()}
+    apart["dt"] = place(inp["dt"])
+    S2, y2, _ = g.gdn_ssm_scan(**apart, cu_seqlens=cu, y_out=place(torch.zeros_like(y)))
+    assert torch.equal(S, S2) and torch.equal(y, y2)
+    pool, pool2 = (torch.ones(T, 3, 256, dtype=BF, device="cuda") for _ in range(2))
+    y = g.gdn_conv_step(x, w, pool)
+    assert torch.equal(y, g.gdn_conv_step(place(x), w, pool2, y=place(torch.zeros_like(y)))) and torch.equal(pool, pool2)
+    S, S2 = (torch.ones(T, h, 64, 64, device="cuda") for _ in range(2))
+    a, b = ([d[n] for n in ("x", "B", "C", "dt", "A")] for d in (inp, apart))
+    y = g.gdn_ssm_step(*a, S)
+    assert torch.equal(y, g.gdn_ssm_step(*b, S2, y=place(torch.zeros_like(y)))) and torch.equal(S, S2)
+    q, k, v = r.n(T, hq, dim, dt=BF), r.n(T, hk, dim, dt=BF), r.n(T, hk, dim, dt=BF)
+    cs, kv = r.n(400, dim), ints([290, 60])
+    c = Cache(r, [290, 60], ps, hk, dim, BF)
+    qr = g.gdn_qk_norm_rope(q, k, v, cs, c.k, c.v, c.table, cu, kv)
+    k1, v1 = c.k.clone(), c.v.clone()
+    qr2 = g.gdn_qk_norm_rope(place(q), place(k), place(v), cs, c.k, c.v, c.table, cu, kv, q_out=place(torch.zeros_like(q)))
+    assert torch.equal(qr, qr2) and torch.equal(k1.nan_to_num(), c.k.nan_to_num()) and torch.equal(v1.nan_to_num(), c.v.nan_to_num())
+    # caches whose last pages are used: more than 2^31 elements, 4 GiB and more
+    pages = 1100000
+    base = pages - c.k.shape[0]
+    K, V = (torch.empty(pages, ps, hk, dim, dtype=BF, device="cuda") for _ in range(2))
+    K[base:], V[base:] = c.k, c.v
+    table = torch.where(c.table >= 0, c.table + base, c.table)
+    assert torch.equal(qr, g.gdn_qk_norm_rope(q, k, v, cs, K, V, table, cu, kv))
+    assert torch.equal(K[base:].nan_to_num(), c.k.nan_to_num()) and torch.equal(V[base:].nan_to_num(), c.v.nan_to_num())
+    one = ints([0, 1, 2])
+    for n, cus in ((T, cu), (2, one)):
+        o = g.gdn_paged_attn(qr[:n], c.k, c.v, c.table, cus, kv)
+        assert torch.equal(o, g.gdn_paged_attn(qr2[:n], K, V, table, cus, kv, o=place(torch.zeros_like(q))[:n]))
+    # a pool of states whose used slots are 2^31 elements in
+    pool = torch.empty(600000, h, 64, 64, device="cuda")
+    slots = torch.arange(T, dtype=torch.int32, device="cuda") + (600000 - T)
+    pool[600000 - T:] = 1.0
+    y2 = g.gdn_ssm_step(*a, pool, slots=slots)
+    assert torch.equal(y, y2) and torch.equal(pool[600000 - T:], S2)
+
+
+def test_a_sequence_does_not_reach_its_neighbours():
+    """A sequence of NaN, NaN behind the last one and in front of a window: the others' bits stay."""
+    g = G()
+    r = Rand(41)
+    lens, h, hq, hk, dim = [70, 33, 100], 2, 4, 2, 64
+    cu, T = cu_of(lens), sum(lens)
+    mine = torch.ones(T + 5, dtype=torch.bool, device="cuda")
+    mine[cu[1]:cu[2]] = False
+    mine[T:] = False
+
+    def both(x):
+        bad = x.clone()
+        bad[~mine] = math.nan
+        return x, bad
+
+    w, cut = r.n(128, 4), ints(cu)
+    for dt in (BF, F32):
+        xs = both(r.n(T + 5, 128, dt=dt))
+        (y, s), (y2, s2) = (g.gdn_conv(x, w, cut) for x in xs)
+        assert torch.equal(y[mine], y2[mine]) and torch.equal(s[::2], s2[::2])
+        inp = {n: (t.contiguous() if t is not None else t) for n, t in scan_inputs(r, T + 5, 1, h, 64, 64, dt, True).items()}
+        bad = dict(inp)
+        for n in ("x", "B", "C", "dt"):
+            bad[n] = both(inp[n])[1]
+        (S, y, _), (S2, y2, _) = (g.gdn_ssm_scan(**i, cu_seqlens=cut) for i in (inp, bad))
+        assert torch.equal(y[mine], y2[mine]) and torch.equal(S[::2], S2[::2])
+        rep = ints([20, 33, 100])
+        mine[:cu[1] - 20] = False
+        for n in ("x", "B", "C", "dt"):
+            bad[n] = both(inp[n])[1]
+        (S, y, _), (S2, y2, _) = (g.gdn_ssm_scan(**i, cu_seqlens=cut, r=rep, total_out_tokens=153) for i in (inp, bad))
+        assert torch.equal(y[:20], y2[:20]) and torch.equal(y[53:], y2[53:]) and torch.equal(S[::2], S2[::2])
+        mine[:cu[1]] = True
+        for L in (lens, [1, 1, 1]):
+            kv, cus = [90, 33, 100], ints(cu_of(L))
+            c = Cache(r, kv, 16, hk, dim, dt)
+            q = r.n(sum(L), hq, dim, dt=dt)
+            o = g.gdn_paged_attn(q, c.k, c.v, c.table, cus, ints(kv))
+            for p in c.pages[1]:
+                c.k[p], c.v[p] = math.nan, math.nan
+            o2 = g.gdn_paged_attn(q, c.k, c.v, c.table, cus, ints(kv))
+            a, b = L[0], L[0] + L[1]
+            assert torch.equal(o[:a], o2[:a]) and torch.equal(o[b:], o2[b:])
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams, each with workspaces of its own, against one after the other."""
+    g = G()
+    r = Rand(51)
+    inp = [scan_inputs(r, 1500, 1, 4, 64, 64, BF, True) for _ in range(2)]
+    cu, kv = ints([0, 1500]), [2500, 900]
+    c = Cache(r, kv, 16, 2, 64, BF)
+    q = [r.n(2, 4, 64, dt=BF) for _ in range(2)]
+    wss = [[new_ws(1 << 24), new_ws(1 << 24)] for _ in range(2)]
+    cut, kvt = ints([0, 1, 2]), ints(kv)
+
+    def calls(i, stream):
+        S, y, _ = g.gdn_ssm_scan(**inp[i], cu_seqlens=cu, ws=wss[i][0], stream=stream)
+        return S, y, g.gdn_paged_attn(q[i], c.k, c.v, c.table, cut, kvt, ws=wss[i][1], stream=stream)
+
+    want = [calls(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[calls(i, streams[i]) for i in range(2)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for a, b in zip(turn, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 # ------------------------------------------------------------------ together
