@@ -695,7 +695,10 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
 {
     const int64_t G = h_q / h_kv;
     AttnPlan p;
-    p.decode = total * G <= 32 * (int64_t)n_seqs;
+    // fp32 in few workgroups over short contexts too: 16 rows to a workgroup whose waves share the keys
+    // (5 prompts of 47 tokens on average, 2 heads of 256, 100 keys: 16.8 us for 21.5 with 64 rows; over
+    // 8K keys the reads count, 60 us with 64 rows for 94)
+    p.decode = total * G <= 32 * (int64_t)n_seqs || (!bf16 && max_kv <= 512 && (total * G / 64 + n_seqs) * h_kv < 128);
     // bf16: 256 rows share a tile of keys where sequences have them, for one workgroup a CU.  fp32
     // products take sixteen times as long and the reads beside them do not count: 64 rows, and splits
     // for several workgroups a CU, for their even spread.
@@ -709,9 +712,10 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
     if (want < 1) want = 1;
     int64_t keys = (max_kv + want - 1) / want;
-    // at least a tile for each of two waves, two where the context is long enough for many splits all
-    // the same (one token over 8K keys: 14.9 us in splits of 128 keys, 16.3 of 64, 17.5 of 256)
-    const int64_t least = p.decode && max_kv < 4096 ? 64 : 128;
+    // At least a tile for each of two waves, two where the context is long enough for many splits all
+    // the same (one token over 8K keys: 14.9 us in splits of 128 keys, 16.3 of 64, 17.5 of 256).  fp32
+    // likewise, whose tile takes 4 us (55 prompts of 11 tokens, 110 keys before them: 16.1 us, 20.3 of 128).
+    const int64_t least = (p.decode || !bf16) && max_kv < 4096 ? 64 : 128;
     if (keys < least) keys = least;
     p.split_keys = (int32_t)((keys + least - 1) / least * least);
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;

@@ -472,7 +472,7 @@ def test_attention(dt, hq, hk, dim, ps, lens, ctx, hf):
     c = Cache(r, kv, ps, hk, dim, dt, heads_first=hf)
     q = r.n(T + 2, hq * dim + 16, dt=dt)[:, :hq * dim].unflatten(1, (hq, dim))
     o = torch.full((T + 2, hq, dim), 7.0, dtype=dt, device="cuda")
-    lse, ws = torch.full((T + 2, hq), 7.0, device="cuda"), new_ws(1 << 24)
+    lse, ws = torch.full((T + 2, hq), 7.0, device="cuda"), new_ws(1 << 26)
     say("attention", dt, hq, hk, dim, ps, lens, ctx)
     G().gdn_paged_attn(q, c.k, c.v, c.table, ints(cu_of(lens)), ints(kv), max_kv_len=max(kv), o=o, lse=lse, ws=ws)
     assert G().gdn_device_status(ws) == 0
