@@ -288,8 +288,7 @@ __device__ __forceinline__ void wait_reads() {
 // ------------------------------------------------------------- few rows: waves over the keys
 // Waves of a workgroup: two workgroups' tiles fit the LDS of a CU (rows of 1 KB aside), so that one's
 // first loads and last sums overlap with the other's keys.
-template <class M, int D>
-constexpr int decode_waves() { return Tile<M, D>::RB >= 512 ? 2 : 4; }
+constexpr int decode_waves(int row_bytes) { return row_bytes >= 512 ? 2 : 4; }
 
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
@@ -309,8 +308,10 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
     const int hk = blockIdx.x % a.h_kv;
-    const int split = (blockIdx.x / a.h_kv) % a.splits;
     const int64_t tile = blockIdx.x / a.h_kv / a.splits;
+    // turned by the tile's number: a multiple of 8 blocks for each would give all the first splits, which
+    // no context is too short for, to the same XCD
+    const int split = (int)((blockIdx.x / a.h_kv + tile) % a.splits);
     Rows r;
     if (!find_rows(a, tile, ROWS, r)) return;
     const int32_t most = row_limit(r, r.m0 + r.count - 1);        // keys that the tile's last row sees
@@ -662,7 +663,7 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
     hipError_t e;
     if (p.decode) {
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
-        constexpr int WAVES = decode_waves<M, D>();
+        constexpr int WAVES = decode_waves(Tile<M, D>::RB);
         if (p.rows == 16) e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
         else if constexpr (M::V == 8 && D != 128) e = start(decode_kernel<M, D, 2, WAVES>, blocks, a, stream, 64 * WAVES);
         else e = hipErrorNotSupported;                   // the plan has no such rows
@@ -674,7 +675,8 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
     }
     if (e != hipSuccess || a.splits == 1) return e;
     constexpr int R = NT / (D / 4);                      // rows of a workgroup without slices
-    if (a.splits <= 8) return start(join_kernel<M, D, 1>, a.total * ((a.h_q + R - 1) / R), a, stream, NT);
+    // slices where splits are many, or rows few (48 rows of 8 splits: 9.1 us with the attention, 12.0 without)
+    if (a.splits <= 2 || (a.splits <= 8 && a.total * a.h_q > 4096)) return start(join_kernel<M, D, 1>, a.total * ((a.h_q + R - 1) / R), a, stream, NT);
     return start(join_kernel<M, D, R>, a.total * a.h_q, a, stream, NT);
 }
 
@@ -687,6 +689,32 @@ hipError_t attn_m(const AttnArgs &a, const AttnPlan &p, int d, hipStream_t strea
     case 256: return attn_d<M, 256>(a, p, stream);
     default: return hipErrorNotSupported;
     }
+}
+
+// Keys of a split where rows are few and contexts short: the least of what the workgroups' tiles take,
+// one after the other and in as many rounds as there are workgroups for three quarters of the places
+// (which is where uneven ones began to count), the reads, of half the longest context, and the join of
+// more than one split.  In microseconds, fitted to times of 6 to 300 sequences of 96 to 4000 keys, equal
+// and ragged; d = 128, bf16, 2 cache heads: 20 sequences of 256 keys 6.6 us in one split and 9.3 in two,
+// of 1000 keys 13.6 in one and 10.3 in eight; 160 of 500 keys 17.0 in one and 23.0 in three.
+int32_t short_splits(int64_t rows, int64_t tiles, int64_t heads, int d, int32_t max_kv, int bf16)
+{
+    const int row = d * (bf16 ? 2 : 4), waves = decode_waves(row);
+    const int64_t places = 192 * (waves * 64 * row <= 80 * 1024 ? 2 : 1);
+    const double tile = bf16 ? 0.3 + 0.006 * d : 0.6 + 0.018 * d, reads = (double)heads * max_kv * row / 5e6;
+    const int32_t all = max_kv > 0 ? (max_kv + 32 * waves - 1) / (32 * waves) : 1;    // tiles of a wave
+    int32_t best = all;
+    double least = 0.0;
+    for (int32_t splits = 1; splits <= all; ++splits) {
+        const int32_t k = (all + splits - 1) / splits;
+        const double products = (double)((tiles * splits + places - 1) / places) * (2.0 + k * tile);
+        const double join = splits > 1 ? 5.0 + (double)rows * splits * d * 8 / 4e6 : 0.0;
+        const double t = products + reads + join;
+        if (splits > 1 && t >= least) continue;
+        least = t;
+        best = k;
+    }
+    return best * 32 * waves;
 }
 
 }  // namespace
@@ -709,15 +737,21 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     if (p.decode) p.rows = bf16 && d != 128 && total * G > 16 * (int64_t)n_seqs ? 32 : 16;
     else p.rows = !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
-    int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
-    if (want < 1) want = 1;
-    int64_t keys = (max_kv + want - 1) / want;
-    // At least a tile for each of two waves, two where the context is long enough for many splits all
-    // the same (one token over 8K keys: 14.9 us in splits of 128 keys, 16.3 of 64, 17.5 of 256).  fp32
-    // likewise, whose tile takes 4 us (55 prompts of 11 tokens, 110 keys before them: 16.1 us, 20.3 of 128).
-    const int64_t least = (p.decode || !bf16) && max_kv < 4096 ? 64 : 128;
-    if (keys < least) keys = least;
-    p.split_keys = (int32_t)((keys + least - 1) / least * least);
+    if (p.decode && max_kv < 4096) {
+        const int64_t least = total * G / p.rows > n_seqs ? total * G / p.rows : n_seqs;
+        p.split_keys = short_splits(total * h_q, least * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16);
+    } else {
+        // Long contexts may be ragged, and the longest then runs alone: splits for several workgroups a CU.
+        int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
+        if (want < 1) want = 1;
+        const int64_t keys = (max_kv + want - 1) / want;
+        // No join for a few tiles (4 prompts of 100 tokens over 64 cached ones, 2 cache heads: 12.5 us, 17.1
+        // in two splits of d = 128; 20.7 and 28.5 of d = 256), else at least 128 keys (one token over 8K
+        // keys: 14.9 us, 16.3 in splits of 64, 17.5 of 256; 4 prompts over 450: 22.8, 23.6 and 25.1), in
+        // fp32, whose tile takes 4 us, 64 (55 prompts of 11 tokens over 110: 16.1 us, 20.3 of 128).
+        const int64_t least = max_kv <= 256 ? 256 : !bf16 && max_kv < 4096 ? 64 : 128;
+        p.split_keys = (int32_t)((keys > least ? keys + least - 1 : least) / least * least);
+    }
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
     return p;
 }
