@@ -54,7 +54,7 @@ struct ScanArgs {
     int32_t n_seqs, h_qk, h_v, softplus, segs;
 };
 // Segments that each window is cut into: the host's choice from sizes alone.
-int32_t scan_segments(int32_t n_seqs, int32_t h_qk, int32_t h_v, int32_t d_v, int bf16, int64_t tokens);
+int32_t scan_segments(int32_t n_seqs, int32_t h_v, int32_t d_k, int32_t d_v, int bf16, int64_t tokens);
 hipError_t launch_scan(const ScanArgs &a, int bf16, int d_k, int d_v, hipStream_t stream);
 
 struct RopeArgs {

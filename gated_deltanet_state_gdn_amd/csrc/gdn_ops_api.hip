@@ -94,7 +94,7 @@ struct ScanPlan {
 ScanPlan scan_plan(const gdn_ssm_desc *d)
 {
     ScanPlan p;
-    p.segs = gdn::scan_segments(d->n_seqs, d->h_qk, d->h_v, d->d_v, d->dtype == GDN_BF16, d->total_out_tokens);
+    p.segs = gdn::scan_segments(d->n_seqs, d->h_v, d->d_k, d->d_v, d->dtype == GDN_BF16, d->total_out_tokens);
     const size_t chains = (size_t)d->n_seqs * (size_t)p.segs * (size_t)d->h_v;
     p.state = kWorkspaceBytes;
     p.decay = p.state + chains * (size_t)d->d_k * (size_t)d->d_v * sizeof(float);
