@@ -697,6 +697,27 @@ hipError_t attn_m(const AttnArgs &a, const AttnPlan &p, int d, hipStream_t strea
     }
 }
 
+// Keys of a split for many bf16 rows: the least of the rounds of workgroups, each as long as its tiles of
+// 64 keys (3.7 us for 256 rows of d = 256 and by d) and 3 us of start and end, and the join.  The chip
+// holds one workgroup of 256 rows a CU, or two of 128 in as long: 1024 tokens of 8 heads on each of 2 cache
+// heads over 32K, 64 workgroups, take 480 us in four splits, 583 in three, 726 in five, 503 in eight.
+int32_t long_splits(int64_t rows, int64_t tiles, int64_t places, int d, int32_t max_kv)
+{
+    const int32_t all = max_kv > 0 ? (max_kv + 63) / 64 : 1;
+    const double tile = 3.7 * d / 256;
+    int32_t best = all;
+    double least = 0.0;
+    for (int32_t splits = 1; splits == 1 || (2 * splits <= all + 1 && splits <= 64); ++splits) {
+        const int32_t k = (all + splits - 1) / splits;
+        const double rounds = (double)((tiles * splits + places - 1) / places);
+        const double t = rounds * (k * tile + 3.0) + (splits > 1 ? 5.0 + (double)rows * splits * d * 8 / 4e6 : 0.0);
+        if (splits > 1 && t >= least) continue;
+        least = t;
+        best = k;
+    }
+    return best * 64;
+}
+
 // Keys of a split where rows are few and contexts short: the least of what the workgroups' tiles take,
 // one after the other and in as many rounds as there are workgroups for three quarters of the places
 // (which is where uneven ones began to count), the reads, of half the longest context, and the join of
@@ -733,9 +754,9 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     // (5 prompts of 47 tokens on average, 2 heads of 256, 100 keys: 16.8 us for 21.5 with 64 rows; over
     // 8K keys the reads count, 60 us with 64 rows for 94)
     p.decode = total * G <= 32 * (int64_t)n_seqs || (!bf16 && max_kv <= 512 && (total * G / 64 + n_seqs) * h_kv < 128);
-    // bf16: 256 rows share a tile of keys where sequences have them, for one workgroup a CU.  fp32
-    // products take sixteen times as long and the reads beside them do not count: 64 rows, and splits
-    // for several workgroups a CU, for their even spread.
+    // bf16: 256 rows share a tile of keys where sequences have them.  fp32 products take sixteen times as
+    // long and the reads beside them do not count: 64 rows, and splits for several workgroups a CU, for
+    // their even spread.
     // Few rows: 32 to a workgroup read the keys once where 16 would twice (32 ragged sequences of up to
     // 8K keys, 32 query heads on each of 2 cache heads, d = 64: 32.3 us for 40.4; 16 sequences, 24 heads
     // on one, d = 256: 31.3 for 42.2).  At d = 128 the first call takes 67.4 us for 59.2 with 16, and
@@ -743,19 +764,28 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     if (p.decode) p.rows = bf16 && d != 128 && total * G > 16 * (int64_t)n_seqs ? 32 : 16;
     else p.rows = !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
+    const int64_t active = total * G / p.rows > n_seqs ? total * G / p.rows : n_seqs;
     if (p.decode && max_kv < 4096) {
-        const int64_t least = total * G / p.rows > n_seqs ? total * G / p.rows : n_seqs;
-        p.split_keys = short_splits(total * h_q, least * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16);
+        p.split_keys = short_splits(total * h_q, active * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16);
+    } else if (bf16 && !p.decode) {
+        // of a sequence's last tile of rows half is expected to be empty
+        const int64_t filled = (total * G + p.rows - 1) / p.rows + (n_seqs - 1) / 2;
+        p.split_keys = long_splits(total * h_q, filled * h_kv, 256 * (256 / p.rows), d, max_kv);
+    } else if (p.decode) {
+        // Long contexts may be ragged, and the longest then runs alone: splits of 1024 keys (40 requests of
+        // up to 12000 keys, 8 cache heads of 128: 225 us, 303 in splits of 4000; 64 of up to 16000, 2 of 64:
+        // 65 us, 83 and, in splits of 170, 69), of fewer where that makes less than two workgroups a CU,
+        // but of four tiles (one token over 8K keys: 14.9 us, 16.3 in splits of 64, 17.5 of 256).  fp32: half
+        // of both, whose tiles take twice as long (3 requests of up to 16000, 4 of 128: 19.9 us for 24.9).
+        // A loose bound makes at most some 8192 workgroups, most of them empty, and a workspace for as many.
+        const int64_t all = max_kv * (active * h_kv), few = all / (bf16 ? 512 : 1024), many = all / 8192;
+        const int64_t most = bf16 ? 1024 : 512, keys = many > most ? many : few > most ? most : few;
+        p.split_keys = (int32_t)(keys < 128 ? 128 : (keys + 127) / 128 * 128);
     } else {
-        // Long contexts may be ragged, and the longest then runs alone: splits for several workgroups a CU.
-        int64_t want = (p.decode ? 1024 : bf16 ? 256 * (256 / p.rows) : 2048) / (tiles > 0 ? tiles : 1);
-        if (want < 1) want = 1;
-        const int64_t keys = (max_kv + want - 1) / want;
-        // No join for a few tiles (4 prompts of 100 tokens over 64 cached ones, 2 cache heads: 12.5 us, 17.1
-        // in two splits of d = 128; 20.7 and 28.5 of d = 256), else at least 128 keys (one token over 8K
-        // keys: 14.9 us, 16.3 in splits of 64, 17.5 of 256; 4 prompts over 450: 22.8, 23.6 and 25.1), in
-        // fp32, whose tile takes 4 us, 64 (55 prompts of 11 tokens over 110: 16.1 us, 20.3 of 128).
-        const int64_t least = max_kv <= 256 ? 256 : !bf16 && max_kv < 4096 ? 64 : 128;
+        // fp32: for several workgroups a CU.  No join for a few tiles, else at least 128 keys, over a short
+        // context, where a tile takes 4 us, 64 (55 prompts of 11 tokens over 110: 16.1 us, 20.3 of 128).
+        const int64_t want = tiles > 0 && tiles < 2048 ? 2048 / tiles : 1, keys = (max_kv + want - 1) / want;
+        const int64_t least = max_kv <= 256 ? 256 : max_kv < 4096 ? 64 : 128;
         p.split_keys = (int32_t)((keys > least ? keys + least - 1 : least) / least * least);
     }
     p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
