@@ -468,10 +468,12 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
     const int hk = blockIdx.x % a.h_kv;
-    const int split = (blockIdx.x / a.h_kv) % a.splits;
     const int64_t tile = blockIdx.x / a.h_kv / a.splits;
     Rows r;
     if (!find_rows(a, tile, ROWS, r)) return;
+    // turned as above: by the sequence's number in bf16, so that the tiles of a sequence keep a split's keys
+    // to one XCD; by the tile's in fp32, where only the even spread counts
+    const int split = (int)((blockIdx.x / a.h_kv + (M::V == 8 ? r.n : tile)) % a.splits);
     const int32_t most = row_limit(r, r.m0 + r.count - 1);
     const int32_t k_beg = split * a.split_keys;
     if (split > 0 && k_beg >= most) return;
