@@ -9,14 +9,16 @@
 // sequence; its window of W inputs slides through registers, so only the W - 1 rows in front of
 // a thread's tokens are read twice (from L2, where the neighbouring tile left them).  All TT + W
 // - 1 loads are issued before the first use.
-// Measured: 16 suffixes, 8200 tokens of 8192 bf16 channels, 270 MB: 66 us, 4.1 TB/s (a large copy: 5.0);
-// one token of 64 requests, fp32: 4.9 us, 17 MB, the length of a launch.
+// Workgroups are single waves of 512 channels or fewer: those of neighbouring tokens then mostly run on
+// the same XCD.  Measured: 16 suffixes, 8200 tokens of 8192 bf16 channels, 270 MB: 59.5 us, 4.5 TB/s (a
+// large copy: 5.0); in workgroups of 128 threads 62, of 256 66 us; 8 tokens a thread 83 us, 24 as 16.  One
+// token of 64 requests, fp32: 4.9 us, 17 MB, the length of a launch.
 #include "gdn_ops_device.h"
 
 namespace gdn {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 64;
 
 // y / (1 + e^-y) with the hardware's exponential and reciprocal (one unit in the last place each):
 // the division's and exp's exact forms cost more instructions than the whole filter.
