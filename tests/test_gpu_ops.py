@@ -436,6 +436,9 @@ ATTN = [  # h_q, h_kv, d, page, lengths, context, heads first
     # 192 rows a sequence and more: large tiles of rows, one split, a few splits, many
     (8, 2, 128, 16, [70, 50, 130], [0, 90, 33], False), (4, 1, 256, 64, [300], [700], False),
     (8, 1, 64, 16, [41, 30, 2], [2100, 0, 64], True),
+    # long contexts, ragged, one of them empty; many rows in a few splits
+    (4, 2, 64, 16, [1, 1, 1, 0], [5000, 0, 4200, 33], False), (16, 2, 256, 64, [1, 2], [4099, 70], True),
+    (32, 8, 128, 16, [1, 1], [5300, 1100], False), (16, 2, 64, 16, [300], [1800], False),
 ]
 
 
@@ -472,7 +475,7 @@ def test_attention(dt, hq, hk, dim, ps, lens, ctx, hf):
     c = Cache(r, kv, ps, hk, dim, dt, heads_first=hf)
     q = r.n(T + 2, hq * dim + 16, dt=dt)[:, :hq * dim].unflatten(1, (hq, dim))
     o = torch.full((T + 2, hq, dim), 7.0, dtype=dt, device="cuda")
-    lse, ws = torch.full((T + 2, hq), 7.0, device="cuda"), new_ws(1 << 26)
+    lse, ws = torch.full((T + 2, hq), 7.0, device="cuda"), new_ws(1 << 28)
     say("attention", dt, hq, hk, dim, ps, lens, ctx)
     G().gdn_paged_attn(q, c.k, c.v, c.table, ints(cu_of(lens)), ints(kv), max_kv_len=max(kv), o=o, lse=lse, ws=ws)
     assert G().gdn_device_status(ws) == 0

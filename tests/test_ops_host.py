@@ -222,7 +222,7 @@ def test_python_paged_refusals(gdn):
 
 
 # ------------------------------------------------------------------ index arithmetic
-DRIVER = r"""
+PROGRAM = r"""
 #include <cstdio>
 #include <cstdlib>
 #include <vector>
@@ -266,7 +266,7 @@ def test_index_arithmetic(tmp_path, san):
     if shutil.which("g++") is None:
         pytest.skip("g++ not available")
     src, exe = tmp_path / "index.cpp", str(tmp_path / "index")
-    src.write_text(DRIVER)
+    src.write_text(PROGRAM)
     cmd = ["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "gated_deltanet_state_gdn_amd", "csrc"), str(src), "-o", exe]
     subprocess.check_call(cmd + (["-fsanitize=" + san] if san else []))
     p = subprocess.run([exe], capture_output=True, text=True, timeout=60)
