@@ -293,7 +293,8 @@ constexpr int decode_waves(int row_bytes) { return row_bytes >= 512 ? 2 : 4; }
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
 // Bound by the reads of K and V, or by latency.  Measured, 16 bf16 query heads on 2 of 256: 64 requests of
-// 1K to 32K cached tokens 412 us, 2.29 GB at 5.5 TB/s; one of 8K 10.3 us and the join's 4.2, 17 MB.
+// 1K to 32K cached tokens 412 us with the join (8), 2.29 GB at 5.6 TB/s; one of 8K 10.3 us and the
+// join's 4.2, 17 MB.
 template <class M, int D, int NB, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(AttnArgs a)
 {
@@ -449,8 +450,8 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
 // KT: keys of a tile.  Two tiles of K and V each: the next one comes in while this one is used, one
 // barrier a tile.
 // Bound by the matrix products and the softmax beside them.  Measured, 1024 tokens of 16 bf16 query heads
-// on 2 of 256 over 31744 cached ones: 583 us with the join (13), 928 TFLOP/s (a large matrix product:
-// 1355), matrix cores 37 % busy; fp32, 9 ragged sequences, 1501 tokens of 16 heads on 4 of 64, up to 4000
+// on 2 of 256 over 31744 cached ones: 475 us with the join (16), 1140 TFLOP/s (a large matrix product:
+// 1355), matrix cores 48 % busy; fp32, 9 ragged sequences, 1501 tokens of 16 heads on 4 of 64, up to 4000
 // cached: 131 us, 77 TFLOP/s (153), the join 7.
 template <class M, int D, int NB, int WAVES, int KT>
 __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
