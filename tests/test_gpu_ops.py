@@ -61,7 +61,7 @@ def new_ws(n=256):
 CONV = [  # channels, width, lengths, state0, silu, bias
     (128, 4, [1], True, True, True), (136, 2, [0, 5, 1, 0, 2, 70], True, True, False),
     (8, 3, [33, 0, 1, 4100], False, False, True), (2056, 4, [17, 64, 3], True, True, True),
-    (512, 4, [600, 1, 2, 3, 4, 0], False, True, True),
+    (512, 4, [600, 1, 2, 3, 4, 0], False, True, True), (72, 4, [0, 0], True, True, True),
 ]
 
 
