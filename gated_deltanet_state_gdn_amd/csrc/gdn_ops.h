@@ -85,6 +85,7 @@ struct AttnArgs {
 struct AttnPlan {
     bool decode;
     int32_t rows;               // rows of a workgroup
+    int32_t waves;              // of a workgroup, if decode
     int32_t splits, split_keys;
 };
 AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int32_t d, int32_t max_kv, int bf16);

@@ -13,7 +13,7 @@
 // keys with the running maximum m and sum l; long caches are cut into splits of keys whose (O, m,
 // l) a second kernel joins.  Scores are in log2 units.
 //
-// Two kernels.  Few rows per sequence (single tokens): bound by the reads of K and V; the four
+// Two kernels.  Few rows per sequence (single tokens): bound by the reads of K and V; the
 // waves of a workgroup take different keys, K goes from memory to registers as operands, V through
 // LDS for its transposition, and the waves' results are joined at the end.  Many rows: bound by
 // the matrix products; the waves take different rows and share the keys' tiles in LDS.
@@ -287,14 +287,16 @@ __device__ __forceinline__ void wait_reads() {
 
 // ------------------------------------------------------------- few rows: waves over the keys
 // Waves of a workgroup: two workgroups' tiles fit the LDS of a CU (rows of 1 KB aside), so that one's
-// first loads and last sums overlap with the other's keys.
+// first loads and last sums overlap with the other's keys; or twice as many waves for a workgroup of its
+// own CU, where workgroups are few (rows of 1 KB do not fit twice).
 constexpr int decode_waves(int row_bytes) { return row_bytes >= 512 ? 2 : 4; }
+constexpr bool decode_wide(int row_bytes) { return row_bytes < 1024; }
 
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
 // Bound by the reads of K and V, or by latency.  Measured, 16 bf16 query heads on 2 of 256: 64 requests of
-// 1K to 32K cached tokens 412 us with the join (8), 2.29 GB at 5.6 TB/s; one of 8K 10.3 us and the
-// join's 4.2, 17 MB.
+// 1K to 32K cached tokens 412 us with the join (8), 2.29 GB at 5.6 TB/s; one of 8K 14.2 us, of
+// which the join is 4.2, 17 MB.
 template <class M, int D, int NB, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(AttnArgs a)
 {
@@ -665,6 +667,14 @@ hipError_t start(K k, int64_t blocks, const AttnArgs &a, hipStream_t stream, int
     return hipGetLastError();
 }
 
+template <class M, int D, int WAVES>
+hipError_t decode_n(const AttnArgs &a, const AttnPlan &p, int64_t blocks, hipStream_t stream)
+{
+    if (p.rows == 16) return start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
+    if constexpr (M::V == 8 && D != 128) return start(decode_kernel<M, D, 2, WAVES>, blocks, a, stream, 64 * WAVES);
+    return hipErrorNotSupported;                         // the plan has no such rows
+}
+
 template <class M, int D>
 hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
@@ -673,9 +683,9 @@ hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
     if (p.decode) {
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         constexpr int WAVES = decode_waves(Tile<M, D>::RB);
-        if (p.rows == 16) e = start(decode_kernel<M, D, 1, WAVES>, blocks, a, stream, 64 * WAVES);
-        else if constexpr (M::V == 8 && D != 128) e = start(decode_kernel<M, D, 2, WAVES>, blocks, a, stream, 64 * WAVES);
-        else e = hipErrorNotSupported;                   // the plan has no such rows
+        if (p.waves == WAVES) e = decode_n<M, D, WAVES>(a, p, blocks, stream);
+        else if constexpr (decode_wide(Tile<M, D>::RB)) e = decode_n<M, D, 2 * WAVES>(a, p, blocks, stream);
+        else e = hipErrorNotSupported;                   // the plan has no such waves
     } else {
         const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         if constexpr (M::V == 4) e = start(prefill_kernel<M, D, 1, 4, 32>, blocks, a, stream, 256);
@@ -726,15 +736,18 @@ int32_t long_splits(int64_t rows, int64_t tiles, int64_t places, int d, int32_t 
 // (which is where uneven ones began to count), the reads, of half the longest context, and the join of
 // more than one split.  In microseconds, fitted to times of 6 to 300 sequences of 96 to 4000 keys, equal
 // and ragged; d = 128, bf16, 2 cache heads: 20 sequences of 256 keys 6.6 us in one split and 9.3 in two,
-// of 1000 keys 13.6 in one and 10.3 in eight; 160 of 500 keys 17.0 in one and 23.0 in three.
-int32_t short_splits(int64_t rows, int64_t tiles, int64_t heads, int d, int32_t max_kv, int bf16)
+// of 1000 keys 13.6 in one and 10.3 in eight; 160 of 500 keys 17.0 in one and 23.0 in three.  Twice the
+// waves: 6 sequences of 128 keys, d = 256, 7.2 us for 8.7 with two; of 512, d = 128, 8.2 for 8.9 with four.
+int32_t short_splits(int64_t rows, int64_t tiles, int64_t heads, int d, int32_t max_kv, int bf16, int waves, double &least)
 {
-    const int row = d * (bf16 ? 2 : 4), waves = decode_waves(row);
+    const int row = d * (bf16 ? 2 : 4);
     const int64_t places = 192 * (waves * 64 * row <= 80 * 1024 ? 2 : 1);
-    const double tile = bf16 ? 0.3 + 0.006 * d : 0.6 + 0.018 * d, reads = (double)heads * max_kv * row / 5e6;
+    // a tile: a wave's 32 keys; with eight waves a SIMD has two, which hold each other up
+    const double tile = (bf16 ? 0.3 + 0.006 * d : 0.6 + 0.018 * d) * (waves == 8 ? 1.5 : 1.0);
+    const double reads = (double)heads * max_kv * row / 5e6;
     const int32_t all = max_kv > 0 ? (max_kv + 32 * waves - 1) / (32 * waves) : 1;    // tiles of a wave
     int32_t best = all;
-    double least = 0.0;
+    least = 0.0;
     for (int32_t splits = 1; splits <= all; ++splits) {
         const int32_t k = (all + splits - 1) / splits;
         const double products = (double)((tiles * splits + places - 1) / places) * (2.0 + k * tile);
@@ -767,9 +780,16 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
     if (p.decode) p.rows = bf16 && d != 128 && total * G > 16 * (int64_t)n_seqs ? 32 : 16;
     else p.rows = !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
     const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
+    const int row = d * (bf16 ? 2 : 4);
+    p.waves = decode_waves(row);
     const int64_t active = total * G / p.rows > n_seqs ? total * G / p.rows : n_seqs;
     if (p.decode && max_kv < 4096) {
-        p.split_keys = short_splits(total * h_q, active * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16);
+        double t, wide;
+        p.split_keys = short_splits(total * h_q, active * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16, p.waves, t);
+        if (decode_wide(row)) {
+            const int32_t keys = short_splits(total * h_q, active * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16, 2 * p.waves, wide);
+            if (wide < t) p.waves *= 2, p.split_keys = keys;
+        }
     } else if (bf16 && !p.decode) {
         // of a sequence's last tile of rows half is expected to be empty
         const int64_t filled = (total * G + p.rows - 1) / p.rows + (n_seqs - 1) / 2;
@@ -784,6 +804,8 @@ AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int
         const int64_t all = max_kv * (active * h_kv), few = all / (bf16 ? 512 : 1024), many = all / 8192;
         const int64_t most = bf16 ? 1024 : 512, keys = many > most ? many : few > most ? most : few;
         p.split_keys = (int32_t)(keys < 128 ? 128 : (keys + 127) / 128 * 128);
+        const int64_t blocks = active * h_kv * ((max_kv + p.split_keys - 1) / p.split_keys);
+        if (decode_wide(row) && blocks <= 256 && p.split_keys >= 64 * p.waves) p.waves *= 2;
     } else {
         // fp32: for several workgroups a CU.  No join for a few tiles, else at least 128 keys, over a short
         // context, where a tile takes 4 us, 64 (55 prompts of 11 tokens over 110: 16.1 us, 20.3 of 128).

@@ -436,6 +436,8 @@ ATTN = [  # h_q, h_kv, d, page, lengths, context, heads first
     # 192 rows a sequence and more: large tiles of rows, one split, a few splits, many
     (8, 2, 128, 16, [70, 50, 130], [0, 90, 33], False), (4, 1, 256, 64, [300], [700], False),
     (8, 1, 64, 16, [41, 30, 2], [2100, 0, 64], True),
+    # contexts that one workgroup takes whole
+    (8, 2, 128, 16, [1, 1], [500, 3], False), (4, 2, 64, 16, [1, 1, 1], [700, 0, 65], True), (16, 2, 256, 64, [1, 1], [200, 31], False),
     # long contexts, ragged, one of them empty; many rows in a few splits
     (4, 2, 64, 16, [1, 1, 1, 0], [5000, 0, 4200, 33], False), (16, 2, 256, 64, [1, 2], [4099, 70], True),
     (32, 8, 128, 16, [1, 1], [5300, 1100], False), (16, 2, 64, 16, [300], [1800], False),
