@@ -5,6 +5,7 @@ use for tiles of packed sequences and places in a paged cache, compiled for the 
 """
 import ctypes
 import os
+import random
 import shutil
 import subprocess
 
@@ -141,6 +142,27 @@ def test_workspace_sizes(gdn):
     assert need > 256 and _call(gdn, "gdn_paged_attn", d, 8, ws_bytes=need - 1) == WORKSPACE
     assert gdn.gdn_paged_workspace_bytes(_paged(gdn, max_kv_len=1)) == 256
     assert gdn.gdn_paged_workspace_bytes(_paged(gdn, d=80)) == 0
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_workspace_sizes_of_any_shape(gdn, dtype):
+    # the plans behind them, from nothing to the largest sizes: at most a row's part for every 64 keys,
+    # a state for every chunk of 64 tokens
+    r = random.Random(dtype)
+    for _ in range(3000):
+        n, total = r.choice([0, 1, 2, 17, 300, 100000]), r.choice([0, 1, 5, 64, 1000, 70000, 1 << 24])
+        h_kv, G, d = r.choice([1, 2, 8]), r.choice([1, 3, 8, 32]), r.choice([64, 128, 256])
+        kv = r.choice([0, 1, 63, 64, 257, 4095, 4096, 100001, 1 << 30])
+        if total * h_kv * G <= 0x7fffffff:
+            s = _paged(gdn, n_seqs=n, total_tokens=total, h_q=h_kv * G, h_kv=h_kv, d=d, max_kv_len=kv, dtype=dtype,
+                       token_stride=2048, head_stride=256, page_stride=32768)
+            need, part = gdn.gdn_paged_workspace_bytes(s), total * h_kv * G * (d + 2) * 4
+            assert 256 <= need <= 512 + part * max(1, -(-kv // 64)), (n, total, h_kv, G, d, kv)
+        k, v = r.choice([64, 128]), r.choice([64, 128])
+        s = _ssm(gdn, n_seqs=n, h_qk=h_kv, h_v=h_kv * G, d_k=k, d_v=v, total_tokens=total, total_out_tokens=total, dtype=dtype,
+                 x_stride=h_kv * G * v, y_stride=h_kv * G * v, b_stride=h_kv * k, c_stride=h_kv * k, dt_stride=h_kv * G)
+        state = n * h_kv * G * (k * v + 1) * 4
+        assert 256 <= gdn.gdn_ssm_workspace_bytes(s) <= 512 + state * max(1, -(-total // 64)), (n, total, h_kv, G, k, v)
 
 
 def test_gated_delta_step_refusals(gdn):
