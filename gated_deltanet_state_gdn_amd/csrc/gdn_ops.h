@@ -3,6 +3,7 @@
 // side and the gfx950 kernels.  Not part of the public interface (that is include/gdn.h).
 #pragma once
 #include "gdn_common.h"
+#include "gdn_plan.h"
 
 namespace gdn {
 
@@ -53,8 +54,6 @@ struct ScanArgs {
     int64_t xs, bs, cs, dts, ys, total, total_out;
     int32_t n_seqs, h_qk, h_v, softplus, segs;
 };
-// Segments that each window is cut into: the host's choice from sizes alone.
-int32_t scan_segments(int32_t n_seqs, int32_t h_v, int32_t d_k, int32_t d_v, int bf16, int64_t tokens);
 hipError_t launch_scan(const ScanArgs &a, int bf16, int d_k, int d_v, hipStream_t stream);
 
 struct RopeArgs {
@@ -81,14 +80,6 @@ struct AttnArgs {
     int32_t splits, split_keys; // split s covers keys [s split_keys, (s + 1) split_keys)
     float scale;
 };
-// How a call is cut: the host's choice from sizes alone, the same for the workspace query.
-struct AttnPlan {
-    bool decode;
-    int32_t rows;               // rows of a workgroup
-    int32_t waves;              // of a workgroup, if decode
-    int32_t splits, split_keys;
-};
-AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int32_t d, int32_t max_kv, int bf16);
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int bf16, int d, hipStream_t stream);
 
 }  // namespace gdn

@@ -286,12 +286,6 @@ __device__ __forceinline__ void wait_reads() {
 }
 
 // ------------------------------------------------------------- few rows: waves over the keys
-// Waves of a workgroup: two workgroups' tiles fit the LDS of a CU (rows of 1 KB aside), so that one's
-// first loads and last sums overlap with the other's keys; or twice as many waves for a workgroup of its
-// own CU, where workgroups are few (rows of 1 KB do not fit twice).
-constexpr int decode_waves(int row_bytes) { return row_bytes >= 512 ? 2 : 4; }
-constexpr bool decode_wide(int row_bytes) { return row_bytes < 1024; }
-
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
 // Bound by the reads of K and V, or by latency.  Measured, 16 bf16 query heads on 2 of 256: 64 requests of
@@ -710,112 +704,7 @@ hipError_t attn_m(const AttnArgs &a, const AttnPlan &p, int d, hipStream_t strea
     }
 }
 
-// Keys of a split for many bf16 rows: the least of the rounds of workgroups, each as long as its tiles of
-// 64 keys (3.7 us for 256 rows of d = 256 and by d) and 3 us of start and end, and the join.  The chip
-// holds one workgroup of 256 rows a CU, or two of 128 in as long: 1024 tokens of 8 heads on each of 2 cache
-// heads over 32K, 64 workgroups, take 480 us in four splits, 583 in three, 726 in five, 503 in eight.
-int32_t long_splits(int64_t rows, int64_t tiles, int64_t places, int d, int32_t max_kv)
-{
-    const int32_t all = max_kv > 0 ? (max_kv + 63) / 64 : 1;
-    const double tile = 3.7 * d / 256;
-    int32_t best = all;
-    double least = 0.0;
-    for (int32_t splits = 1; splits == 1 || (2 * splits <= all + 1 && splits <= 64); ++splits) {
-        const int32_t k = (all + splits - 1) / splits;
-        const double rounds = (double)((tiles * splits + places - 1) / places);
-        const double t = rounds * (k * tile + 3.0) + (splits > 1 ? 5.0 + (double)rows * splits * d * 8 / 4e6 : 0.0);
-        if (splits > 1 && t >= least) continue;
-        least = t;
-        best = k;
-    }
-    return best * 64;
-}
-
-// Keys of a split where rows are few and contexts short: the least of what the workgroups' tiles take,
-// one after the other and in as many rounds as there are workgroups for three quarters of the places
-// (which is where uneven ones began to count), the reads, of half the longest context, and the join of
-// more than one split.  In microseconds, fitted to times of 6 to 300 sequences of 96 to 4000 keys, equal
-// and ragged; d = 128, bf16, 2 cache heads: 20 sequences of 256 keys 6.6 us in one split and 9.3 in two,
-// of 1000 keys 13.6 in one and 10.3 in eight; 160 of 500 keys 17.0 in one and 23.0 in three.  Twice the
-// waves: 6 sequences of 128 keys, d = 256, 7.2 us for 8.7 with two; of 512, d = 128, 8.2 for 8.9 with four.
-int32_t short_splits(int64_t rows, int64_t tiles, int64_t heads, int d, int32_t max_kv, int bf16, int waves, double &least)
-{
-    const int row = d * (bf16 ? 2 : 4);
-    const int64_t places = 192 * (waves * 64 * row <= 80 * 1024 ? 2 : 1);
-    // a tile: a wave's 32 keys; with eight waves a SIMD has two, which hold each other up
-    const double tile = (bf16 ? 0.3 + 0.006 * d : 0.6 + 0.018 * d) * (waves == 8 ? 1.5 : 1.0);
-    const double reads = (double)heads * max_kv * row / 5e6;
-    const int32_t all = max_kv > 0 ? (max_kv + 32 * waves - 1) / (32 * waves) : 1;    // tiles of a wave
-    int32_t best = all;
-    least = 0.0;
-    for (int32_t splits = 1; splits <= all; ++splits) {
-        const int32_t k = (all + splits - 1) / splits;
-        const double products = (double)((tiles * splits + places - 1) / places) * (2.0 + k * tile);
-        const double join = splits > 1 ? 5.0 + (double)rows * splits * d * 8 / 4e6 : 0.0;
-        const double t = products + reads + join;
-        if (splits > 1 && t >= least) continue;
-        least = t;
-        best = k;
-    }
-    return best * 32 * waves;
-}
-
 }  // namespace
-
-AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_kv, int32_t d, int32_t max_kv, int bf16)
-{
-    const int64_t G = h_q / h_kv;
-    AttnPlan p;
-    // fp32 in few workgroups over short contexts too: 16 rows to a workgroup whose waves share the keys
-    // (5 prompts of 47 tokens on average, 2 heads of 256, 100 keys: 16.8 us for 21.5 with 64 rows; over
-    // 8K keys the reads count, 60 us with 64 rows for 94)
-    p.decode = total * G <= 32 * (int64_t)n_seqs || (!bf16 && max_kv <= 512 && (total * G / 64 + n_seqs) * h_kv < 128);
-    // bf16: 256 rows share a tile of keys where sequences have them.  fp32 products take sixteen times as
-    // long and the reads beside them do not count: 64 rows, and splits for several workgroups a CU, for
-    // their even spread.
-    // Few rows: 32 to a workgroup read the keys once where 16 would twice (32 ragged sequences of up to
-    // 8K keys, 32 query heads on each of 2 cache heads, d = 64: 32.3 us for 40.4; 16 sequences, 24 heads
-    // on one, d = 256: 31.3 for 42.2).  At d = 128 the first call takes 67.4 us for 59.2 with 16, and
-    // fp32 gains nothing (25.2 for 25.6).
-    if (p.decode) p.rows = bf16 && d != 128 && total * G > 16 * (int64_t)n_seqs ? 32 : 16;
-    else p.rows = !bf16 ? 64 : total * G >= 192 * (int64_t)n_seqs ? 256 : 128;
-    const int64_t tiles = (total * G / p.rows + n_seqs) * h_kv;
-    const int row = d * (bf16 ? 2 : 4);
-    p.waves = decode_waves(row);
-    const int64_t active = total * G / p.rows > n_seqs ? total * G / p.rows : n_seqs;
-    if (p.decode && max_kv < 4096) {
-        double t, wide;
-        p.split_keys = short_splits(total * h_q, active * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16, p.waves, t);
-        if (decode_wide(row)) {
-            const int32_t keys = short_splits(total * h_q, active * h_kv, (int64_t)n_seqs * h_kv, d, max_kv, bf16, 2 * p.waves, wide);
-            if (wide < t) p.waves *= 2, p.split_keys = keys;
-        }
-    } else if (bf16 && !p.decode) {
-        // of a sequence's last tile of rows half is expected to be empty
-        const int64_t filled = (total * G + p.rows - 1) / p.rows + (n_seqs - 1) / 2;
-        p.split_keys = long_splits(total * h_q, filled * h_kv, 256 * (256 / p.rows), d, max_kv);
-    } else if (p.decode) {
-        // Long contexts may be ragged, and the longest then runs alone: splits of 1024 keys (40 requests of
-        // up to 12000 keys, 8 cache heads of 128: 225 us, 303 in splits of 4000; 64 of up to 16000, 2 of 64:
-        // 65 us, 83 and, in splits of 170, 69), of fewer where that makes less than two workgroups a CU,
-        // but of four tiles (one token over 8K keys: 14.9 us, 16.3 in splits of 64, 17.5 of 256).  fp32: half
-        // of both, whose tiles take twice as long (3 requests of up to 16000, 4 of 128: 19.9 us for 24.9).
-        // A loose bound makes at most some 8192 workgroups, most of them empty, and a workspace for as many.
-        const int64_t all = max_kv * (active * h_kv), few = all / (bf16 ? 512 : 1024), many = all / 8192;
-        const int64_t most = bf16 ? 1024 : 512, keys = many > most ? many : few > most ? most : few;
-        p.split_keys = (int32_t)(keys < 128 ? 128 : (keys + 127) / 128 * 128);
-        const int64_t blocks = active * h_kv * ((max_kv + p.split_keys - 1) / p.split_keys);
-        if (decode_wide(row) && blocks <= 256 && p.split_keys >= 64 * p.waves) p.waves *= 2;
-    } else {
-        // fp32: for several workgroups a CU.  No join for a few tiles, else at least 128 keys, over a short
-        // context, where a tile takes 4 us, 64 (55 prompts of 11 tokens over 110: 16.1 us, 20.3 of 128).
-        const int64_t want = tiles > 0 && tiles < 2048 ? 2048 / tiles : 1, keys = (max_kv + want - 1) / want;
-        const int64_t least = max_kv <= 256 ? 256 : max_kv < 4096 ? 64 : 128;
-        p.split_keys = (int32_t)((keys > least ? keys + least - 1 : least) / least * least);
-    }
-    p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
-    return p;
-}
 
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int bf16, int d, hipStream_t stream)
 {

@@ -35,7 +35,7 @@
 namespace gdn {
 namespace {
 
-constexpr int CH = 64;      // tokens of a chunk
+constexpr int CH = kScanChunk;   // tokens of a chunk
 constexpr int NT = 256;
 constexpr int MODE_FULL = 0, MODE_STATE = 1, MODE_OUT = 2;
 
@@ -575,55 +575,7 @@ hipError_t scan_v(const ScanArgs &a, int d_v, hipStream_t stream)
     return d_v == 128 ? scan_c<M, DK, 128, 64>(a, stream) : scan_c<M, DK, 64, 64>(a, stream);
 }
 
-
-// Time of a scan whose longest sequence has `longest` chunks, cut into s segments: one launch, or the
-// states, their chain and the outputs in three.  In microseconds, fitted; `work` is the chunks of 64
-// columns that a CU has.  Alone on its CU a bf16 chunk of d_k = 128 takes 3.6 us in one launch and 4.3 in
-// two, 1.5 and 2.0 of it the CU's own for every other workgroup there; fp32, bound by its products, 9.3
-// and 11.4 alone and 10.3 and 13.5 of the CU.  Three launches cost 7.5 us more than one, and every
-// segment's state is written twice and read twice.
-double scan_time(int64_t s, int64_t longest, double work, double states, int32_t d_k, int bf16)
-{
-    const double k = (double)((longest + s - 1) / s);
-    const double alone = k * (s == 1 ? (bf16 ? 3.6 : 9.3) : bf16 ? 4.3 : 11.4);
-    const double shared = s == 1 ? (bf16 ? k * 2.1 + work * 1.5 : work * 10.3) : bf16 ? k * 2.3 + work * 2.0 : work * 13.5;
-    const double moved = (double)(s < longest ? s : longest) * states * d_k * 64 * 4 * 4 / 8e6;
-    return (alone > shared ? alone : shared) * (0.5 + d_k / 256.0) + (s == 1 ? 4.0 : 11.5 + moved);
-}
-
 }  // namespace
-
-// Segments a sequence is cut into: the least time, as the mean of equal sequences and of ragged ones
-// whose longest is 3.5 times the mean (the host does not know them); one where every CU has two workgroups
-// without.  At most four workgroups a CU that are not empty (bf16: what runs at once) or eight (fp32,
-// whose chunks are long beside their states).
-// One sequence of 32768 tokens, 32 heads: 192 us in 32 segments (21: 254, 64: 225); 16 of 512 tokens, 8
-// heads, 34.1 in one launch and 32.7 in four segments; one of 512 tokens, 4 heads, 32.5 in one and 15.9 in
-// eight; 16 of 512 with 32 heads 44.7 in one and 69.5 in two; fp32, 24 ragged ones of 292 on average, 4
-// heads of 64: 109 in one, 39.3 in twelve, 42.6 in 21.
-int32_t scan_segments(int32_t n_seqs, int32_t h_v, int32_t d_k, int32_t d_v, int bf16, int64_t tokens)
-{
-    if (n_seqs <= 0 || tokens <= CH) return 1;
-    const int64_t chunks = (tokens + CH - 1) / CH, mean = (chunks + n_seqs - 1) / n_seqs;
-    const int64_t longest = mean * 7 / 2 < chunks ? mean * 7 / 2 : chunks;
-    const double chains = (double)n_seqs * h_v * d_v / 64;               // of 64 columns
-    if (chains >= 512) return 1;
-    const double work = (double)chunks * h_v * d_v / 64 / 256, part = (double)chunks / (double)(n_seqs * longest);
-    const double filled = chains * (part < 1.0 ? part : 1.0);            // workgroups a segment that are not empty
-    const int64_t places = (int64_t)((bf16 ? 1024 : 2048) / filled), most = places < longest ? places : longest;
-    int64_t best = 1;
-    double least = 0.0;
-    for (int64_t s = 1; s == 1 || s <= most;) {
-        const double t = scan_time(s, mean, work, chains, d_k, bf16) + scan_time(s, longest, work, filled, d_k, bf16);
-        if (s == 1 || t < least) {
-            least = t;
-            best = s;
-        }
-        const int64_t next = s + s / 8 + 1;
-        s = s < most && next > most ? most : next;
-    }
-    return (int32_t)best;
-}
 
 hipError_t launch_scan(const ScanArgs &a, int bf16, int d_k, int d_v, hipStream_t stream)
 {
