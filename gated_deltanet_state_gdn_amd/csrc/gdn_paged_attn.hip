@@ -655,8 +655,7 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
 template <class K>
 hipError_t start(K k, int64_t blocks, const AttnArgs &a, hipStream_t stream, int threads)
 {
-    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-    if (blocks <= 0) return hipSuccess;
+    if (blocks < 1 || blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
 }

@@ -158,11 +158,13 @@ inline AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_
         // 65 us, 83 and, in splits of 170, 69), of fewer where that makes less than two workgroups a CU,
         // but of four tiles (one token over 8K keys: 14.9 us, 16.3 in splits of 64, 17.5 of 256).  fp32: half
         // of both, whose tiles take twice as long (3 requests of up to 16000, 4 of 128: 19.9 us for 24.9).
-        // A loose bound makes at most some 8192 workgroups, most of them empty, and a workspace for as many.
-        const int64_t all = max_kv * (active * h_kv), few = all / (bf16 ? 512 : 1024), many = all / 8192;
+        // A loose bound makes at most some 8192 workgroups, most of them empty, and a workspace for as many;
+        // where there are as many without splits, none are split.
+        const int64_t chains = active * h_kv, all = max_kv * (chains < 8192 ? chains : 8192);
+        const int64_t few = all / (bf16 ? 512 : 1024), many = all / 8192;
         const int64_t most = bf16 ? 1024 : 512, keys = many > most ? many : few > most ? most : few;
         p.split_keys = (int32_t)(keys < 128 ? 128 : (keys + 127) / 128 * 128);
-        const int64_t blocks = active * h_kv * ((max_kv + p.split_keys - 1) / p.split_keys);
+        const int64_t blocks = chains * (((int64_t)max_kv + p.split_keys - 1) / p.split_keys);
         if (decode_wide(row) && blocks <= 256 && p.split_keys >= 64 * p.waves) p.waves *= 2;
     } else {
         // fp32: for several workgroups a CU.  No join for a few tiles, else at least 128 keys, over a short
@@ -171,7 +173,7 @@ inline AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_
         const int64_t least = max_kv <= 256 ? 256 : max_kv < 4096 ? 64 : 128;
         p.split_keys = (int32_t)((keys > least ? keys + least - 1 : least) / least * least);
     }
-    p.splits = max_kv > 0 ? (max_kv + p.split_keys - 1) / p.split_keys : 1;
+    p.splits = max_kv > 0 ? (int32_t)(((int64_t)max_kv + p.split_keys - 1) / p.split_keys) : 1;
     return p;
 }
 
