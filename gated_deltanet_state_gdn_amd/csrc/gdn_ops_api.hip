@@ -109,10 +109,11 @@ int32_t check_paged(const gdn_paged_desc *d)
     if (!known_dtype(d->dtype)) return refuse(GDN_ERR_DTYPE, "unknown dtype code");
     if (d->n_seqs < 0 || d->h_q <= 0 || d->h_kv <= 0 || d->h_q % d->h_kv != 0 || d->d <= 0 || d->page_size <= 0 ||
         d->n_pages < 0 || d->max_pages < 0 || d->max_kv_len < 0 || d->max_kv_len > (1 << 30) ||
-        d->total_tokens < 0 || d->total_tokens * (int64_t)d->h_q > 0x7fffffffLL)
+        d->total_tokens < 0 || d->total_tokens > 0x7fffffffLL || d->total_tokens * d->h_q > 0x7fffffffLL)
         return refuse(GDN_ERR_SHAPE, "paged cache: bad sizes, h_q not a multiple of h_kv, or too many rows");
     if (d->d != 64 && d->d != 128 && d->d != 256)
         return refuse(GDN_ERR_UNSUPPORTED, "unsupported head dim: d must be 64, 128 or 256");
+    if ((int64_t)d->h_q * d->d > 0x7fffffffLL) return refuse(GDN_ERR_SHAPE, "a token's row is longer than a stride may be");
     const int64_t e = elem_bytes(d->dtype);
     if (d->page_stride < 0 || d->token_stride < d->d || d->head_stride < d->d ||
         d->page_stride >= (1LL << 40) || d->token_stride >= (1LL << 40) || d->head_stride >= (1LL << 40) ||
