@@ -139,7 +139,7 @@ hipError_t conv_w(const ConvArgs &a, bool step, hipStream_t stream)
     const int vecs = a.channels / E::V;
     if (step) {
         const int64_t wide = (vecs + 63) / 64;
-        if (wide * a.n_seqs > kMaxBlocks) return hipErrorInvalidConfiguration;
+        if (!grid_ok(wide * a.n_seqs, 64)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((conv_step_kernel<E, W>), dim3((unsigned)(wide * a.n_seqs)), dim3(64), 0, stream, a, (uint32_t)wide);
         return hipGetLastError();
     }
@@ -150,7 +150,7 @@ hipError_t conv_w(const ConvArgs &a, bool step, hipStream_t stream)
     auto tiles = [&](int tt) { return a.total / (groups * tt) + a.n_seqs; };
     const bool small = wide * tiles(16) < 512;
     const int64_t n = tiles(small ? 4 : 16) * wide;
-    if (n > kMaxBlocks) return hipErrorInvalidConfiguration;
+    if (!grid_ok(n, NT)) return hipErrorInvalidConfiguration;
     if (small) hipLaunchKernelGGL((conv_kernel<E, W, 4>), dim3((unsigned)n), dim3(NT), 0, stream, a, cols, (uint32_t)wide);
     else hipLaunchKernelGGL((conv_kernel<E, W, 16>), dim3((unsigned)n), dim3(NT), 0, stream, a, cols, (uint32_t)wide);
     return hipGetLastError();

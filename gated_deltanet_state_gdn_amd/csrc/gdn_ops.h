@@ -7,8 +7,9 @@
 
 namespace gdn {
 
-// Blocks of one launch: a grid holds fewer than 2^32 threads, 256 to a block here.
-constexpr int64_t kMaxBlocks = (1LL << 24) - 1;
+// Whether one launch holds so many blocks: a grid has at least one and fewer than 2^32 threads.  Every
+// launch of a call is checked before the first one is enqueued.
+constexpr bool grid_ok(int64_t blocks, int threads) { return blocks >= 1 && blocks <= 0xffffffffLL / threads; }
 
 struct ConvArgs {
     const void *x;              // [T, channels], rows x_stride apart

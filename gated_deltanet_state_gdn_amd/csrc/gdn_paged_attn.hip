@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
 template <class K>
 hipError_t start(K k, int64_t blocks, const AttnArgs &a, hipStream_t stream, int threads)
 {
-    if (blocks < 1 || blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
+    if (!grid_ok(blocks, threads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
 }
@@ -672,24 +672,26 @@ template <class M, int D>
 hipError_t attn_d(const AttnArgs &a, const AttnPlan &p, hipStream_t stream)
 {
     const int G = a.h_q / a.h_kv;
+    constexpr int R = NT / (D / 4);                      // rows of a join's workgroup without slices
+    // slices where splits are many, or rows few (48 rows of 8 splits: 9.1 us with the attention, 12.0 without)
+    const bool sliced = a.splits > 8 || (a.splits > 2 && a.total * a.h_q <= 4096);
+    const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
+    const int64_t joins = a.splits == 1 ? 1 : a.total * (sliced ? a.h_q : (a.h_q + R - 1) / R);
+    if (!grid_ok(joins, NT)) return hipErrorInvalidConfiguration;
     hipError_t e;
     if (p.decode) {
-        const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         constexpr int WAVES = decode_waves(Tile<M, D>::RB);
         if (p.waves == WAVES) e = decode_n<M, D, WAVES>(a, p, blocks, stream);
         else if constexpr (decode_wide(Tile<M, D>::RB)) e = decode_n<M, D, 2 * WAVES>(a, p, blocks, stream);
         else e = hipErrorNotSupported;                   // the plan has no such waves
     } else {
-        const int64_t blocks = (a.total * G / p.rows + a.n_seqs) * a.splits * a.h_kv;
         if constexpr (M::V == 4) e = start(prefill_kernel<M, D, 1, 4, 32>, blocks, a, stream, 256);
         else if (p.rows == 256) e = start(prefill_kernel<M, D, 2, 8, 64>, blocks, a, stream, 512);
         else e = start(prefill_kernel<M, D, 2, 4, 64>, blocks, a, stream, 256);
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    constexpr int R = NT / (D / 4);                      // rows of a workgroup without slices
-    // slices where splits are many, or rows few (48 rows of 8 splits: 9.1 us with the attention, 12.0 without)
-    if (a.splits <= 2 || (a.splits <= 8 && a.total * a.h_q > 4096)) return start(join_kernel<M, D, 1>, a.total * ((a.h_q + R - 1) / R), a, stream, NT);
-    return start(join_kernel<M, D, R>, a.total * a.h_q, a, stream, NT);
+    if (sliced) return start(join_kernel<M, D, R>, joins, a, stream, NT);
+    return start(join_kernel<M, D, 1>, joins, a, stream, NT);
 }
 
 template <class M>

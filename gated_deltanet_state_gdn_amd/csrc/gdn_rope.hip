@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(NT) rope_kernel(RopeArgs a)
 template <class E, bool INTER>
 hipError_t rope_e(const RopeArgs &a, int d, hipStream_t stream)
 {
-    if (a.total > kMaxBlocks) return hipErrorInvalidConfiguration;
+    if (!grid_ok(a.total, NT)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)a.total);
     switch (d) {
     case 64: hipLaunchKernelGGL((rope_kernel<E, 64, INTER>), grid, dim3(NT), 0, stream, a); break;

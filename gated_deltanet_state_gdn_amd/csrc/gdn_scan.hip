@@ -537,19 +537,22 @@ __global__ void __launch_bounds__(64) offsets_kernel(ScanArgs a)
     }
 }
 
+template <int DV, int COLS>
+int64_t scan_blocks(const ScanArgs &a) { return (int64_t)a.n_seqs * a.segs * ((int64_t)a.h_v * DV / COLS); }
+
 template <class M, int DK, int DV, int COLS, int MODE>
 hipError_t scan_m(const ScanArgs &a, hipStream_t stream)
 {
-    const int64_t blocks = (int64_t)a.n_seqs * a.segs * ((int64_t)a.h_v * DV / COLS);
-    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     auto k = scan_kernel<M, DK, DV, COLS, MODE>;
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(COLS * 4 / WT), 0, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)scan_blocks<DV, COLS>(a)), dim3(COLS * 4 / WT), 0, stream, a);
     return hipGetLastError();
 }
 
 template <class M, int DK, int DV, int COLS>
 hipError_t scan_c(const ScanArgs &a, hipStream_t stream)
 {
+    const int64_t chains = a.segs > 1 ? ((int64_t)a.n_seqs * a.h_v * (DK * DV / 4) + NT - 1) / NT : 1;   // blocks of chain_kernel
+    if (!grid_ok(scan_blocks<DV, COLS>(a), COLS * 4 / WT) || !grid_ok(chains, NT)) return hipErrorInvalidConfiguration;
     if (a.cu_out) {
         hipLaunchKernelGGL(offsets_kernel, dim3(1), dim3(64), 0, stream, a);
         const hipError_t e = hipGetLastError();
@@ -558,9 +561,7 @@ hipError_t scan_c(const ScanArgs &a, hipStream_t stream)
     if (a.segs == 1) return a.y ? scan_m<M, DK, DV, COLS, MODE_FULL>(a, stream) : scan_m<M, DK, DV, COLS, MODE_STATE>(a, stream);
     hipError_t e = scan_m<M, DK, DV, COLS, MODE_STATE>(a, stream);
     if (e != hipSuccess) return e;
-    const int64_t blocks = ((int64_t)a.n_seqs * a.h_v * (DK * DV / 4) + NT - 1) / NT;
-    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(chain_kernel, dim3((unsigned)blocks), dim3(NT), 0, stream, a, DK * DV);
+    hipLaunchKernelGGL(chain_kernel, dim3((unsigned)chains), dim3(NT), 0, stream, a, DK * DV);
     e = hipGetLastError();
     if (e != hipSuccess || !a.y) return e;
     return scan_m<M, DK, DV, COLS, MODE_OUT>(a, stream);

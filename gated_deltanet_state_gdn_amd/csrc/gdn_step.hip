@@ -102,7 +102,7 @@ template <class E, bool DELTA>
 hipError_t step_e(const StepArgs &a, int d_k, int d_v, hipStream_t stream)
 {
     const int64_t blocks = ((int64_t)a.rows * a.h_v * (d_v / 32) + 3) / 4;
-    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
+    if (!grid_ok(blocks, 256)) return hipErrorInvalidConfiguration;
     if (d_k == 64) hipLaunchKernelGGL((step_kernel<E, 64, DELTA>), dim3((unsigned)blocks), dim3(256), 0, stream, a, d_v);
     else hipLaunchKernelGGL((step_kernel<E, 128, DELTA>), dim3((unsigned)blocks), dim3(256), 0, stream, a, d_v);
     return hipGetLastError();
