@@ -61,14 +61,19 @@ __device__ __forceinline__ uint32_t xcd_block(uint32_t unit) {
     return ((i / unit) * 8 + x) * unit + i % unit;
 }
 
-// ln(1 + e^x) = max(x, 0) + ln(1 + z), z = e^-|x| in (0, 1].  The exponential's argument is kept in two
-// floats; ln(1 + z) = 2 atanh(s), s = z / (2 + z) <= 1/3, by its series up to s^15 (the next term is
-// below 3e-9 of the sum), which also keeps the small values of very negative x.
-__device__ __forceinline__ float softplus(float x) {
-    const float a = -fabsf(x);
+// e^a for a <= 0, below 2^-126 0.  The exponential's argument is kept in two floats.  Arguments under -150 are
+// taken as that (0 as well): the second float's product would overflow at the type's lowest.  NaN stays NaN.
+__device__ __forceinline__ float exp_down(float a) {
+    a = a < -150.0f ? -150.0f : a;
     const float p = a * 1.4426950408889634f;
     const float r = fmaf(a, 1.4426950408889634f, -p) + a * 1.925963033500e-8f;     // log2 e in two floats
-    const float z = __builtin_amdgcn_exp2f(p) * fmaf(r, 0.6931471805599453f, 1.0f);
+    return __builtin_amdgcn_exp2f(p) * fmaf(r, 0.6931471805599453f, 1.0f);
+}
+// ln(1 + e^x) = max(x, 0) + ln(1 + z), z = e^-|x| in [0, 1]; ln(1 + z) = 2 atanh(s), s = z / (2 + z) <= 1/3, by its
+// series up to s^15 (the next term is below 3e-9 of the sum), which also keeps the small values of very
+// negative x.
+__device__ __forceinline__ float softplus(float x) {
+    const float z = exp_down(-fabsf(x));
     const float d = 2.0f + z;
     float q = __builtin_amdgcn_rcpf(d);
     q = fmaf(fmaf(-d, q, 1.0f), q, q);

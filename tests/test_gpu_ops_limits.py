@@ -1,0 +1,48 @@
+"""GPU: the suffix and decode operators at the ends of their types, and the roundings that they state."""
+import math
+
+import pytest
+import torch
+
+import ops_reference as R
+from gpu_helpers import say
+from test_gpu_ops import BF, F32, TYPES, G, Rand, ints, new_ws, scan_check, scan_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@TYPES
+def test_gates_of_the_types_ends(dt):
+    """softplus at the type's lowest value is 0: the token leaves the state as it is (a masked token).  At its
+    highest, with B = x = 0, the token clears the state.  Both are finite and stay out of their neighbours."""
+    g, h, k, p, T = 1, 2, 64, 64, 200
+    r = Rand(13)
+    inp = {n: t.contiguous() for n, t in scan_inputs(r, T, g, h, k, p, dt, True).items()}
+    low, high = torch.finfo(dt).min, torch.finfo(dt).max
+    inp["dt"][[0, 3, 64, 70, 199]] = low
+    inp["dt"][[10, 11], 0] = -200.0
+    inp["dt"][12, 1] = -1e30
+    for t in (40, 130):
+        inp["dt"][t] = high
+        inp["B"][t], inp["x"][t] = 0, 0
+    S0 = r.n(1, h, k, p)
+    S, y, _ = G().gdn_ssm_scan(**inp, cu_seqlens=ints([0, T]), S0=S0)
+    scan_check(y, S[0], 0, inp, 0, T, R.d(S0[0]), dt, True, "gates")
+    # the same values in the single-token form, a row each
+    rows = [0, 10, 12, 40, 41]
+    pool = r.n(len(rows), h, k, p)
+    before = pool.clone()
+    a = [inp[n][rows].contiguous() for n in ("x", "B", "C", "dt")]
+    y = G().gdn_ssm_step(*a, inp["A"], pool, D=inp["D"], dt_bias=inp["dt_bias"])
+    for i in range(len(rows)):
+        ref = R.ssm_tokens(*(R.d(t[i:i + 1]) for t in a), R.d(inp["A"]), R.d(inp["D"]), R.d(inp["dt_bias"]), R.d(before[i]))
+        R.within(pool[i], ref[2], 20 * R.U32 * ref[3] + 1e-30, "S of row %d" % i)
+        R.within(y[i:i + 1], ref[0], R.u(dt) * ref[0].abs() + (30 + k) * R.U32 * ref[1] + 1e-30, "y of row %d" % i)
+    # NaN stays NaN
+    inp["dt"][5, 0] = math.nan
+    S, y, _ = G().gdn_ssm_scan(**inp, cu_seqlens=ints([0, T]), S0=S0)
+    assert y[5, 0].isnan().all() and S[0, 0].isnan().all() and not S[0, 1].isnan().any() and not y[:, 1].isnan().any()
+    nan = inp["dt"][5:6].contiguous()
+    pool = before[:1].clone()
+    y = G().gdn_ssm_step(*(inp[n][5:6].contiguous() for n in ("x", "B", "C")), nan, inp["A"], pool, D=inp["D"], dt_bias=inp["dt_bias"])
+    assert y[0, 0].isnan().all() and pool[0, 0].isnan().all() and not y[0, 1].isnan().any()
