@@ -20,10 +20,19 @@ namespace {
 
 constexpr int NT = 64;
 
-// y / (1 + e^-y) with the hardware's exponential and reciprocal (one unit in the last place each):
-// the division's and exp's exact forms cost more instructions than the whole filter.
+// y / (1 + e^-y).  fp32: as y (1 or z) / (1 + z) with z = e^-|y|, whose argument is kept in two floats: at most
+// 10 halves of a step off down to y = -87, where z passes 2^-126 and is 0 (the form below, 64 at y = -80: the
+// argument's rounding grows with |y|).  bf16: with the hardware's exponential and reciprocal alone, 2^-18 off
+// there, a 1000th of the output's half step.
+template <class E>
 __device__ __forceinline__ float act(float y, int silu) {
-    return silu ? y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.4426950408889634f)) : y;
+    if (!silu) return y;
+    if constexpr (E::V == 8) {
+        return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.4426950408889634f));
+    } else {
+        const float z = exp_down(-fabsf(y));
+        return (y < 0.0f ? y * z : y) * __builtin_amdgcn_rcpf(1.0f + z);
+    }
 }
 
 // W taps of V channels, [channels, W] row-major
@@ -97,7 +106,7 @@ __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a, int cols, uint32_t
             acc[v] = b[v];
 #pragma unroll
             for (int j = 0; j < W; ++j) acc[v] = fmaf(tap[j][v], win[(i + j) % W][v], acc[v]);
-            acc[v] = act(acc[v], a.silu);
+            acc[v] = act<E>(acc[v], a.silu);
         }
         store16(y + t * a.ys, E::pack(acc));
     }
@@ -127,7 +136,7 @@ __global__ void __launch_bounds__(64) conv_step_kernel(ConvArgs a, uint32_t wide
         for (int v = 0; v < V; ++v) acc[v] = fmaf(tap[j][v], f[v], acc[v]);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = act(acc[v], a.silu);
+    for (int v = 0; v < V; ++v) acc[v] = act<E>(acc[v], a.silu);
     store16(static_cast<T *>(a.y) + row * a.ys + c, E::pack(acc));
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store16(s + (int64_t)j * a.channels, in[j + 1]);

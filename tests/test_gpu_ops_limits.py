@@ -46,3 +46,21 @@ def test_gates_of_the_types_ends(dt):
     pool = before[:1].clone()
     y = G().gdn_ssm_step(*(inp[n][5:6].contiguous() for n in ("x", "B", "C")), nan, inp["A"], pool, D=inp["D"], dt_bias=inp["dt_bias"])
     assert y[0, 0].isnan().all() and pool[0, 0].isnan().all() and not y[0, 1].isnan().any()
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_silu_in_fp32(step):
+    """SiLU of known arguments (the taps are zero, the bias is the argument).  Roundings: the exponential (2, and
+    3 of its argument's), 1 + z, the reciprocal (2), two products, each at most one: 10 halves of a step; the
+    exponential is 0 below 2^-126, which is worth |y| 2^-126."""
+    arg = torch.cat([torch.linspace(-100, 100, 4001), torch.tensor([0.0, -1e-30, 1e-30, 3e38, -3e38, -87.3, -87.4])]).cuda()
+    arg = torch.cat([arg, torch.zeros(-arg.numel() % 4, device="cuda")])
+    ch = arg.numel()
+    x, w = Rand(2).n(3, ch), torch.zeros(ch, 2, device="cuda")
+    if step:
+        y = G().gdn_conv_step(x, w, torch.zeros(3, 1, ch, device="cuda"), bias=arg)
+    else:
+        y, _ = G().gdn_conv(x, w, ints([0, 3]), bias=arg)
+    a = R.d(arg)
+    ref = torch.where(a < -700, torch.zeros_like(a), a * torch.sigmoid(a.clamp(min=-700)))
+    R.within(y, ref.expand(3, -1), 10 * R.U32 * ref.abs() + 90 * 2.0 ** -126, "SiLU")
