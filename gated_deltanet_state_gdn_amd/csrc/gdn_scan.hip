@@ -22,9 +22,10 @@
 // them (S_start(s+1) = decay_s S_start(s) + local_s), and a third forms the outputs.
 //
 // Precision: S, G and every sum are fp32 or wider.  bf16 inputs enter the matrix products as they
-// are; M, and S in C S, are rounded to bf16 once (half a bf16 step, as the output itself is).  The
-// state is an fp32 output: there diag(w) X is split into three bf16 terms, 24 bits, and multiplied
-// with B exactly as B is.  fp32 inputs use fp32 products throughout.
+// are; M, and S in C S, are rounded to bf16 once (half a bf16 step of each term, as the output itself is
+// of the sum).  The state is an fp32 output: there diag(w) X is split into three bf16 terms, 24 bits, and
+// multiplied with B exactly as B is; the launch that only forms outputs takes two terms, 16 bits.  fp32
+// inputs use fp32 products throughout.
 //
 // Measured: one bf16 sequence of 32768 tokens, 32 heads of 128 x 64: 195 us (states 71, chain 13, outputs
 // 118 alone; 305 MB, of which the copy would take 61 us).  A chunk's products wait for each other, so a
@@ -423,7 +424,8 @@ __global__ void __launch_bounds__(COLS * 4 / WT, M::V == 8 && COLS == 128 ? 4 : 
                 }
             }
         }
-        // the state; the outputs alone (MODE_OUT) only need it to the precision of C S
+        // the state; the outputs alone (MODE_OUT) need it to less than the rounding of S in C S: two terms,
+        // 16 bits (one would be a third rounding of y, and one that is there only in segments)
         if (MODE == MODE_OUT && ch + 1 == nch) break;
         const float last = gt.last;
 #pragma unroll
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(COLS * 4 / WT, M::V == 8 && COLS == 128 ? 4 : 
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             if (beyond(32 * kb)) break;
-            constexpr int TERMS = V == 4 || MODE == MODE_OUT ? 1 : 3;
+            constexpr int TERMS = V == 4 ? 1 : MODE == MODE_OUT ? 2 : 3;
             const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + Bt::LANE * g]);
             const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&gt.w[32 * kb + Bt::LANE * g + Bt::HALF]);
             Frag wx[WT][TERMS];

@@ -64,3 +64,36 @@ def test_silu_in_fp32(step):
     a = R.d(arg)
     ref = torch.where(a < -700, torch.zeros_like(a), a * torch.sigmoid(a.clamp(min=-700)))
     R.within(y, ref.expand(3, -1), 10 * R.U32 * ref.abs() + 90 * 2.0 ** -126, "SiLU")
+
+
+@pytest.mark.parametrize("k,p,h", [(64, 64, 32), (64, 128, 32), (128, 64, 15), (128, 64, 32), (128, 128, 16)])
+def test_scan_in_segments_rounds_the_state_once(k, p, h):
+    """bf16, cut into segments: M and S are rounded to bf16 for their products with x and C, and nothing else
+    is.  Gates of 1 + 2^-7, no decay, and inputs 1 + j 2^-7 (40 <= j < 64): the state's terms dt x lie j 2^-14
+    above a bf16 value, so that rounding them to bf16 would make every state, and y, smaller by
+    j 2^-14 / (1 + j 2^-7), 1.5e-3 and more.  The roundings of S and M have no common sign: of at least 2^13 of them, 2^-8
+    at most, the mean is beyond 2^-11 with a probability below 1e-12 (Hoeffding: 2 exp(-2^13 / (2 * 64)))."""
+    r = Rand(k + p)
+    T = 8192
+    x = (1 + torch.randint(40, 64, (T, h, p), generator=r.g) * 2.0 ** -7).cuda().to(BF)
+    B, C = r.n(T, 1, k, dt=BF), r.n(T, 1, k, dt=BF)
+    dt = torch.full((T, h), 1 + 2.0 ** -7, dtype=BF, device="cuda")
+    A = torch.zeros(h, device="cuda")
+    need = G().gdn_ssm_workspace_bytes(G().make_ssm_desc(x, B, 1))
+    segs = (need - 256) // (h * (k * p + 1) * 4)
+    assert segs > 1
+    per = -(-(T // 64) // segs) * 64
+    say("scan in", segs, "segments of", per)
+    assert per >= 128
+    S, y, _ = G().gdn_ssm_scan(x, B, C, dt, A, ints([0, T]), softplus=False, ws=new_ws(need))
+    xs = x.double() * dt.double()[..., None]
+    ref = torch.empty(T, h, p, dtype=torch.float64, device="cuda")
+    low = torch.ones(T, T, dtype=torch.bool, device="cuda").tril()
+    M = torch.where(low, C[:, 0].double() @ B[:, 0].double().t(), torch.zeros((), dtype=torch.float64, device="cuda"))
+    for i in range(h):
+        ref[:, i] = M @ xs[:, i]
+    # rows whose state comes from their own segment in part: all but a segment's first chunk; in the first one all of it does
+    got, want = y[64:per].double(), ref[64:per]
+    bias = float((got * want).sum() / (want * want).sum()) - 1
+    say("  common part of the outputs' error %.2e" % bias)
+    assert abs(bias) <= 2.0 ** -11
