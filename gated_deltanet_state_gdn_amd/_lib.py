@@ -73,8 +73,14 @@ def load() -> ctypes.CDLL:
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
     i32, i64 = ctypes.c_int32, ctypes.c_int64
     dptr = ctypes.POINTER(GdnDesc)
-    lib.gdn_abi_version.argtypes = []
-    lib.gdn_abi_version.restype = i32
+    if hasattr(lib, "gdn_abi_version"):
+        lib.gdn_abi_version.argtypes = []
+        lib.gdn_abi_version.restype = i32
+        if lib.gdn_abi_version() != ABI_VERSION:
+            raise ImportError("libgdn.so ABI version mismatch")
+    missing = [n for n in EXPORTS if not hasattr(lib, n)]
+    if missing:
+        raise ImportError("libgdn.so is built from older sources, without %s: build it again" % ", ".join(missing))
     lib.gdn_status_str.argtypes = [i32]
     lib.gdn_status_str.restype = ctypes.c_char_p
     lib.gdn_replay_len.argtypes = [i32, ctypes.c_double]
@@ -110,8 +116,6 @@ def load() -> ctypes.CDLL:
     lib.gdn_ssm_workspace_bytes.restype = sz
     lib.gdn_paged_workspace_bytes.argtypes = [pptr]
     lib.gdn_paged_workspace_bytes.restype = sz
-    if lib.gdn_abi_version() != ABI_VERSION:
-        raise ImportError("libgdn.so ABI version mismatch")
     _lib = lib
     return lib
 
