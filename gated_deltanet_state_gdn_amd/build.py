@@ -1,6 +1,9 @@
 """Build the gfx950 HIP library ``libgdn.so`` (hipcc) and the binding ``_gdn_torch.so`` in-tree, no JIT cache.
 
-    python -m gated_deltanet_state_gdn_amd.build [--jobs N]
+    python -m gated_deltanet_state_gdn_amd.build [--jobs N] [--library]
+
+``--library``: the C library alone, for which hipcc is enough (the binding takes g++ and the headers of torch
+and Python).
 """
 from __future__ import annotations
 
@@ -58,7 +61,7 @@ def build_binding() -> str:
     root = os.path.dirname(torch.__file__)
     inc = [p for p in cpp_extension.include_paths() if os.path.isdir(p)] + [sysconfig.get_paths()["include"]]
     tmp = BINDING + ".tmp%d" % os.getpid()
-    subprocess.check_call([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+    subprocess.check_call([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra",
                            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
                           + [a for p in inc for a in ("-isystem", p)]
                           + [os.path.join(CSRC, "gdn_torch.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
@@ -67,18 +70,31 @@ def build_binding() -> str:
     return BINDING
 
 
-def build(jobs: int = 4, verbose: bool = True) -> str:
+def build_library(jobs: int = 4, verbose: bool = True) -> str:
+    """The C library alone: hipcc, nothing of torch or Python."""
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=max(1, jobs) + 1) as ex:
-        binding = ex.submit(build_binding)
+    with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
         objs = list(ex.map(_compile, SOURCES))
-        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
     if verbose:
-        print("built", LIB, "and", BINDING)
+        print("built", LIB)
+    return LIB
+
+
+def build(jobs: int = 4, verbose: bool = True) -> str:
+    """The library and the binding.  The library is made whether or not the binding can be."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(build_binding)
+        build_library(jobs, verbose)
+        try:
+            binding.result()
+        except Exception as e:
+            raise RuntimeError("%s is built; the torch binding of the suffix and decode operators is not: %s" % (LIB, e)) from e
+    if verbose:
+        print("built", BINDING)
     return LIB
 
 
@@ -127,4 +143,6 @@ def clang_asan_runtime() -> str:
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--jobs", type=int, default=4)
-    build(ap.parse_args().jobs)
+    ap.add_argument("--library", action="store_true", help="the C library alone, without the torch binding")
+    args = ap.parse_args()
+    (build_library if args.library else build)(args.jobs)

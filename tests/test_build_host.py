@@ -9,6 +9,32 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
+def test_the_library_is_built_without_the_binding(tmp_path, monkeypatch):
+    """No g++, no torch or Python headers: the C library is made all the same, and the failure is said."""
+    from gated_deltanet_state_gdn_amd import build as b
+    made = []
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libgdn.so"))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    monkeypatch.setattr(b, "hipcc", lambda: "hipcc")
+    monkeypatch.setattr(b, "_compile", lambda src: src + ".o")
+
+    def link(cmd, *a, **kw):
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(b.subprocess, "check_call", link)
+
+    def no_headers():
+        raise OSError("no g++ here")
+
+    monkeypatch.setattr(b, "build_binding", no_headers)
+    with pytest.raises(RuntimeError, match="no g\\+\\+ here"):
+        b.build(verbose=False)
+    assert os.path.exists(b.LIB) and len(made) == 1 and made[0][0] == "hipcc"
+    os.remove(b.LIB)
+    assert b.build_library(verbose=False) == b.LIB and os.path.exists(b.LIB)
+
+
 def _load(tmp_path, source):
     if shutil.which("gcc") is None:
         pytest.skip("gcc not available")
