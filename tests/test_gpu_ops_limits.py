@@ -1,4 +1,5 @@
 """GPU: the suffix and decode operators at the ends of their types, and the roundings that they state."""
+import ctypes
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 import ops_reference as R
 from gpu_helpers import say
-from test_gpu_ops import BF, F32, TYPES, G, Rand, ints, new_ws, scan_check, scan_inputs
+from test_gpu_ops import BF, F32, TYPES, Cache, G, Rand, attn_check, ints, new_ws, scan_check, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,28 @@ def test_scan_in_segments_rounds_the_state_once(k, p, h):
     bias = float((got * want).sum() / (want * want).sum()) - 1
     say("  common part of the outputs' error %.2e" % bias)
     assert abs(bias) <= 2.0 ** -11
+
+
+@TYPES
+@pytest.mark.parametrize("n,hk,bound", [(1100, 8, 1 << 30), (600, 8, 1 << 30), (2, 2, 1 << 30), (1100, 8, 1 << 27)])
+def test_attention_under_the_loosest_bound(dt, n, hk, bound):
+    """max_kv_len as large as it may be, beside few cached tokens: the C call, whose bound no table limits."""
+    g, r, hq, dim, ps = G(), Rand(n), 2 * hk, 64, 16
+    kv = [1 + (7 * i) % 20 for i in range(n)]
+    kv[-1] = 45
+    c = Cache(r, kv, ps, hk, dim, dt)
+    q, o, lse = r.n(n, hq, dim, dt=dt), torch.full((n, hq, dim), 7.0, dtype=dt, device="cuda"), torch.empty(n, hq, device="cuda")
+    d = g.make_paged_desc(q, c.k, c.table, n)
+    d.max_kv_len = bound
+    need = g.gdn_paged_workspace_bytes(d)
+    say("attention under a bound of", bound, dt, n, hk, "workspace", need)
+    assert 256 <= need <= 1 << 30
+    ws, cu, kvt = new_ws(need), ints(list(range(n + 1))), ints(kv)
+    p = [ctypes.c_void_p(t.data_ptr()) for t in (q, c.k, c.v, c.table, cu, kvt, o, lse, ws)]
+    code = g.load().gdn_paged_attn(ctypes.byref(d), *p, need, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert code == 0 and g.gdn_device_status(ws) == 0
+    some = [0, 1, n // 2, n - 1]
+    part = Cache.__new__(Cache)
+    part.keys, part.vals = [c.keys[i] for i in some], [c.vals[i] for i in some]
+    attn_check(part, q[some], o[some], lse[some], [1] * len(some), [kv[i] for i in some], dim ** -0.5, dt)
+    assert not o.isnan().any() and not lse.isnan().any()
