@@ -5,7 +5,9 @@ arguments.  Checks of dtypes, shapes, strides and devices, output allocation and
 in the native module (csrc/gdn_torch.cpp): a refusal raises GdnError with the matching status before
 anything is enqueued.  ``ws`` is a zero-filled uint8 workspace that the caller keeps (one for each
 stream or graph that may run at the same time); a call without it makes a new one.  Calls run on
-torch's current stream of the tensors' device, or on ``stream``.
+torch's current stream of the tensors' device, or on ``stream``.  As everywhere in this package, autograd is
+not involved: outputs carry no gradient, whatever the inputs require, and what is updated in place (states,
+caches, given outputs) is so without a new version of the tensor.
 """
 from __future__ import annotations
 

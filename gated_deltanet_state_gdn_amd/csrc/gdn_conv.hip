@@ -10,9 +10,9 @@
 // a thread's tokens are read twice (from L2, where the neighbouring tile left them).  All TT + W
 // - 1 loads are issued before the first use.
 // Workgroups are single waves of 512 channels or fewer: those of neighbouring tokens then mostly run on
-// the same XCD.  Measured: 16 suffixes, 8200 tokens of 8192 bf16 channels, 270 MB: 59.5 us, 4.5 TB/s (a
+// the same XCD.  Measured: 16 suffixes, 8200 tokens of 8192 bf16 channels, 270 MB: 61 us, 4.4 TB/s (a
 // large copy: 5.0); in workgroups of 128 threads 62, of 256 66 us; 8 tokens a thread 83 us, 24 as 16.  One
-// token of 64 requests, fp32: 4.9 us, 17 MB, the length of a launch.
+// token of 64 requests, fp32: 5.0 us, 17 MB, the length of a launch.
 #include "gdn_ops_device.h"
 
 namespace gdn {

@@ -19,8 +19,10 @@
 // the matrix products; the waves take different rows and share the keys' tiles in LDS.
 //
 // Precision: scores, maximum, sum, O are fp32.  With bf16 elements the products take q, k and v as
-// they are; P is rounded to bf16 once where the products are the bound (half a bf16 step, as the
-// output is), and taken in two bf16 terms where memory is.  The sum l takes the unrounded P.
+// they are; P is rounded to bf16 once where the products are the bound (half a bf16 step of each term p v; a
+// second term would be half as many products again), and taken in two bf16 terms where memory is.  The
+// sum l takes the unrounded P.  Relative error of the outputs, 2-norm, in the measured cases: 2.3e-3 with one
+// term, 1.7e-3 with two, which is the outputs' own rounding.
 // Keys behind kv_len are never read: whatever a page holds there (or an unused page) does not matter.
 #include "gdn_mfma.h"
 
@@ -289,7 +291,7 @@ __device__ __forceinline__ void wait_reads() {
 // A wave has 32 keys at a time, and a tile of K and one of V of its own: the next keys' K comes in
 // from the moment the scores are formed, their V from the moment O is.  No barrier before the join.
 // Bound by the reads of K and V, or by latency.  Measured, 16 bf16 query heads on 2 of 256: 64 requests of
-// 1K to 32K cached tokens 412 us with the join (8), 2.29 GB at 5.6 TB/s; one of 8K 14.2 us, of
+// 1K to 32K cached tokens 412 us with the join (8), 2.29 GB at 5.6 TB/s; one of 8K 13.5 us, of
 // which the join is 4.2, 17 MB.
 template <class M, int D, int NB, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(AttnArgs a)
@@ -446,9 +448,9 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
 // KT: keys of a tile.  Two tiles of K and V each: the next one comes in while this one is used, one
 // barrier a tile.
 // Bound by the matrix products and the softmax beside them.  Measured, 1024 tokens of 16 bf16 query heads
-// on 2 of 256 over 31744 cached ones: 475 us with the join (16), 1140 TFLOP/s (a large matrix product:
-// 1355), matrix cores 48 % busy; fp32, 9 ragged sequences, 1501 tokens of 16 heads on 4 of 64, up to 4000
-// cached: 131 us, 77 TFLOP/s (153), the join 7.
+// on 2 of 256 over 31744 cached ones: 485 to 500 us with the join (16), 1080 to 1115 TFLOP/s (a large
+// matrix product: 1355), matrix cores 48 % busy; fp32, 9 ragged sequences, 1501 tokens of 16 heads on 4 of 64,
+// up to 4000 cached: 133 us, 76 TFLOP/s (153), the join 7.
 template <class M, int D, int NB, int WAVES, int KT>
 __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 {

@@ -25,13 +25,15 @@ inline double scan_time(int64_t s, int64_t longest, double work, double states, 
 }
 
 // Segments a sequence is cut into: the least time, as the mean of equal sequences and of ragged ones
-// whose longest is 3.5 times the mean (the host does not know them); one where every CU has two workgroups
-// without.  At most four workgroups a CU that are not empty (bf16: what runs at once) or eight (fp32,
-// whose chunks are long beside their states).
-// One sequence of 32768 tokens, 32 heads: 192 us in 32 segments (21: 254, 64: 225); 16 of 512 tokens, 8
-// heads, 34.1 in one launch and 32.7 in four segments; one of 512 tokens, 4 heads, 32.5 in one and 15.9 in
-// eight; 16 of 512 with 32 heads 44.7 in one and 69.5 in two; fp32, 24 ragged ones of 292 on average, 4
-// heads of 64: 109 in one, 39.3 in twelve, 42.6 in 21.
+// whose longest is 3.5 times the mean; one where every CU has two workgroups without.  The host does not
+// know the lengths: 3.5 comes from the ragged batches that this was fitted with (lengths by the square of a
+// uniform number, one in ten empty: 2.8 to 3.7); others have their answer too, if not in the least time.
+// At most four workgroups a CU that are not empty (bf16: what runs at once) or eight (fp32, whose chunks
+// are long beside their states).
+// One sequence of 32768 tokens, 32 heads: 192 us in 32 segments, 254 in 21, 225 in 64 (all before the outputs'
+// second term, which adds 7); 16 of 512 tokens, 8 heads, 34.1 in one launch and 32.7 in four segments; one of
+// 512 tokens, 4 heads, 32.5 in one and 15.9 in eight; 16 of 512 with 32 heads 44.7 in one and 69.5 in two;
+// fp32, 24 ragged ones of 292 on average, 4 heads of 64: 109 in one, 39.3 in twelve, 42.6 in 21.
 inline int32_t scan_segments(int32_t n_seqs, int32_t h_v, int32_t d_k, int32_t d_v, int bf16, int64_t tokens)
 {
     if (n_seqs <= 0 || tokens <= kScanChunk) return 1;
@@ -93,8 +95,9 @@ inline int32_t long_splits(int64_t rows, int64_t tiles, int64_t places, int d, i
 
 // Keys of a split where rows are few and contexts short: the least of what the workgroups' tiles take,
 // one after the other and in as many rounds as there are workgroups for three quarters of the places
-// (which is where uneven ones began to count), the reads, of half the longest context, and the join of
-// more than one split.  In microseconds, fitted to times of 6 to 300 sequences of 96 to 4000 keys, equal
+// (which is where uneven ones began to count), the reads, of half the longest context (of contexts
+// spread evenly up to it, the ragged ones that this was fitted with), and the join of more than one
+// split.  In microseconds, fitted to times of 6 to 300 sequences of 96 to 4000 keys, equal
 // and ragged; d = 128, bf16, 2 cache heads: 20 sequences of 256 keys 6.6 us in one split and 9.3 in two,
 // of 1000 keys 13.6 in one and 10.3 in eight; 160 of 500 keys 17.0 in one and 23.0 in three.  Twice the
 // waves: 6 sequences of 128 keys, d = 256, 7.2 us for 8.7 with two; of 512, d = 128, 8.2 for 8.9 with four.

@@ -8,8 +8,8 @@
 // other half is a lane exchange (rot is a multiple of 16, so it is a whole lane away).  A block
 // takes one token, so its sequence and page are found once, and its groups of lanes share the
 // token's heads out among them.
-// Measured: 1024 tokens of 16 + 2 + 2 bf16 heads of 256: 8.9 us, 21 MB, of which some 5 are the launch and
-// the chain sequence - table - place - store; 33 single tokens, fp32: 4.9 us.
+// Measured: 1024 tokens of 16 + 2 + 2 bf16 heads of 256: 9.0 us, 21 MB, of which some 5 are the launch and
+// the chain sequence - table - place - store; 33 single tokens, fp32: 5.3 us.
 #include "gdn_ops_device.h"
 
 namespace gdn {

@@ -27,10 +27,11 @@
 // multiplied with B exactly as B is; the launch that only forms outputs takes two terms, 16 bits.  fp32
 // inputs use fp32 products throughout.
 //
-// Measured: one bf16 sequence of 32768 tokens, 32 heads of 128 x 64: 195 us (states 71, chain 13, outputs
-// 118 alone; 305 MB, of which the copy would take 61 us).  A chunk's products wait for each other, so a
-// CU's four waves a SIMD are bound by that chain and its LDS reads (42 % of the LDS cycles, a fifth of
-// them conflicts; matrix cores 30 % busy).  fp32, 24 ragged sequences, 7001 tokens, 4 heads of 64 x 64: 43 us.
+// Measured: one bf16 sequence of 32768 tokens, 32 heads of 128 x 64: 194 to 201 us by the box (305 MB, which the
+// copy would take 61 us for); in a trace states 71 to 83, chain 13, outputs 126 to 150.  Half of the waves'
+// cycles are waits, at a chunk's three barriers and for one product's operands from another; no unit is
+// full (outputs: LDS 42 % of its cycles, a quarter of them conflicts, vector issue 37 %, matrix cores 21 %;
+// states: 32, 34 and 29 %).  fp32, 24 ragged sequences, 7001 tokens, 4 heads of 64 x 64: 44 us.
 #include "gdn_mfma.h"
 
 namespace gdn {
@@ -132,7 +133,7 @@ struct Lds {
 };
 // 16-column tiles of S that a wave owns.  Two would halve the reads of C and B^T (which every wave
 // reads whole) and leave two waves a SIMD instead of four: one sequence of 32768 tokens, 32 heads took
-// 82 + 143 us with two and 75 + 133 us with one (states, outputs).
+// 82 + 143 us with two and 75 + 133 us with one (states, outputs; the latter's state then in one term).
 constexpr int WT = 1;
 
 template <class M, int DK, int DV, int COLS, int MODE>
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(COLS * 4 / WT, M::V == 8 && COLS == 128 ? 4 : 
             }
         }
         // the state; the outputs alone (MODE_OUT) need it to less than the rounding of S in C S: two terms,
-        // 16 bits (one would be a third rounding of y, and one that is there only in segments)
+        // 16 bits (one would be a third rounding of y, and one that is there only in segments; the second
+        // costs the long sequence above 7 us)
         if (MODE == MODE_OUT && ch + 1 == nch) break;
         const float last = gt.last;
 #pragma unroll

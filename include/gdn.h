@@ -304,8 +304,10 @@ size_t gdn_ssm_workspace_bytes(const gdn_ssm_desc *desc);
 /* Prompts.  r NULL: whole sequences from S0 (nullable: zero).  r [n_seqs]: the last r[n] tokens of
  * each, as gdn_replay takes them (S0 is then the state in front of the window), y's rows packed
  * per window and cu_out (nullable) [n_seqs + 1] their offsets.  y is nullable; S_out may be S0.
- * bf16: products take bf16 operands with fp32 sums; M and S are rounded to bf16 once in y, and
- * S_out is accurate to fp32 (its operands enter in three bf16 terms). */
+ * bf16: products take bf16 operands with fp32 sums; M (the chunk's C_i . B_j and gates) and S are
+ * rounded to bf16 once for their products in y, half a bf16 step of each term, and nothing else is
+ * rounded to less than 16 bits, however the batch is cut; S_out is accurate to fp32 (its operands
+ * enter in three bf16 terms). */
 int32_t gdn_ssm_scan(const gdn_ssm_desc *desc, const void *x, const void *B, const void *C, const void *dt,
                      const float *A, const float *dt_bias, const float *D, const int32_t *cu_seqlens,
                      const int32_t *r, const float *S0, float *S_out, void *y, int32_t *cu_out,
@@ -366,8 +368,10 @@ size_t gdn_paged_workspace_bytes(const gdn_paged_desc *desc);
  *     o = sum_j softmax_j(scale q . k_j) v_j,  lse = ln sum_j exp(scale q . k_j)  (nullable, [T, h_q] fp32),
  * query head h with cache head floor(h h_kv / h_q).  A token in front of the cache's first one
  * (kv_len < L) sees nothing: o = 0, lse = -inf.  A bad cu_seqlens, kv_len or page sets the status
- * bit; the outputs of those sequences are unspecified.  bf16: products take q, k, v as they are,
- * probabilities rounded to bf16 once, with fp32 scores, sums and outputs before the final rounding. */
+ * bit; the outputs of those sequences are unspecified.  bf16: products take q, k, v as they are, with
+ * fp32 scores, sums and outputs before the final rounding.  Probabilities have 16 bits in batches of up
+ * to 32 rows a sequence on average (rows: tokens times query heads on a cache head); in larger ones they
+ * are rounded to bf16 once, half a bf16 step of each term p_j v_j. */
 int32_t gdn_paged_attn(const gdn_paged_desc *desc, const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *kv_len,
                        void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
