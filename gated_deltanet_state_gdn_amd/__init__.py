@@ -18,15 +18,19 @@ import torch
 from . import _lib
 from ._lib import (GDN_BF16, GDN_F32, GdnDesc, GdnError, GDN_ERR_DEVICE_INPUT, GDN_OK,
                    LIB_PATH, load)
-from ._ops import (gdn_conv, gdn_conv_step, gdn_paged_attn, gdn_paged_workspace_bytes, gdn_qk_norm_rope,
-                   gdn_ssm_scan, gdn_ssm_step, gdn_ssm_workspace_bytes, gdn_step, make_paged_desc, make_ssm_desc)
+from ._ops import (gdn_cache_extend, gdn_conv, gdn_conv_step, gdn_extend_workspace_bytes, gdn_paged_attn,
+                   gdn_paged_workspace_bytes, gdn_qk_norm_rope, gdn_sample, gdn_sample_workspace_bytes, gdn_shared_attn,
+                   gdn_shared_workspace_bytes, gdn_ssm_scan, gdn_ssm_step, gdn_ssm_workspace_bytes, gdn_step,
+                   make_paged_desc, make_sample_desc, make_shared_desc, make_ssm_desc)
 
 __all__ = ["gdn_replay", "gdn_prefill", "gdn_state_relerr", "gdn_device_status",
            "gdn_replay_segmented", "gdn_segmented_workspace_bytes",
            "gdn_adaptive_replay_len", "gdn_adaptive_replay_len_static",
            "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_ssm_workspace_bytes",
            "gdn_step", "gdn_qk_norm_rope", "gdn_paged_attn", "gdn_paged_workspace_bytes",
-           "make_ssm_desc", "make_paged_desc",
+           "gdn_cache_extend", "gdn_extend_workspace_bytes", "gdn_shared_attn", "gdn_shared_workspace_bytes",
+           "gdn_sample", "gdn_sample_workspace_bytes",
+           "make_ssm_desc", "make_paged_desc", "make_shared_desc", "make_sample_desc",
            "gdn_workspace_bytes", "gdn_replay_len", "gdn_status_str", "gdn_abi_version",
            "GdnError", "make_desc", "workspace", "LIB_PATH", "load"]
 

@@ -20,7 +20,9 @@ EXPORTS = ("gdn_abi_version", "gdn_status_str", "gdn_replay_len", "gdn_workspace
            "gdn_adaptive_replay_len", "gdn_adaptive_replay_len_static",
            "gdn_segmented_workspace_bytes", "gdn_replay_segmented",
            "gdn_conv", "gdn_conv_step", "gdn_ssm_workspace_bytes", "gdn_ssm_scan", "gdn_ssm_step",
-           "gdn_step", "gdn_qk_norm_rope", "gdn_paged_workspace_bytes", "gdn_paged_attn")
+           "gdn_step", "gdn_qk_norm_rope", "gdn_paged_workspace_bytes", "gdn_paged_attn",
+           "gdn_extend_workspace_bytes", "gdn_cache_extend", "gdn_shared_workspace_bytes", "gdn_shared_attn",
+           "gdn_sample_workspace_bytes", "gdn_sample")
 
 
 class GdnDesc(ctypes.Structure):
@@ -50,6 +52,19 @@ class GdnPagedDesc(ctypes.Structure):
         ("eps", _F32), ("scale", _F32)] + [
         (f, _I64) for f in ("total_tokens", "q_stride", "k_stride", "v_stride", "o_stride", "page_stride",
                             "token_stride", "head_stride")]
+
+
+class GdnExtendDesc(ctypes.Structure):
+    _fields_ = [(f, _I32) for f in ("n_seqs", "page_size", "max_pages", "n_free", "n_prefixes", "max_prefix_pages")] + [
+        ("total_tokens", _I64)]
+
+
+class GdnSharedDesc(ctypes.Structure):
+    _fields_ = [("cache", GdnPagedDesc)] + [(f, _I32) for f in ("n_groups", "max_prefix_len", "max_own_len")]
+
+
+class GdnSampleDesc(ctypes.Structure):
+    _fields_ = [(f, _I32) for f in ("rows", "vocab", "dtype")] + [("stride", _I64)]
 
 
 class GdnError(RuntimeError):
@@ -104,9 +119,11 @@ def load() -> ctypes.CDLL:
     lib.gdn_replay_segmented.argtypes = [dptr, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     lib.gdn_replay_segmented.restype = i32
     cptr, sptr, pptr = (ctypes.POINTER(t) for t in (GdnConvDesc, GdnSsmDesc, GdnPagedDesc))
+    eptr, shptr, saptr = (ctypes.POINTER(t) for t in (GdnExtendDesc, GdnSharedDesc, GdnSampleDesc))
     for name, desc, pointers in (("gdn_conv", cptr, 7), ("gdn_conv_step", cptr, 6), ("gdn_ssm_scan", sptr, 13),
                                  ("gdn_ssm_step", sptr, 10), ("gdn_qk_norm_rope", pptr, 13),
-                                 ("gdn_paged_attn", pptr, 8)):
+                                 ("gdn_paged_attn", pptr, 8), ("gdn_cache_extend", eptr, 13),
+                                 ("gdn_shared_attn", shptr, 10), ("gdn_sample", saptr, 8)):
         f = getattr(lib, name)
         f.argtypes = [desc] + [vp] * pointers + [vp, sz, vp]
         f.restype = i32
@@ -116,6 +133,12 @@ def load() -> ctypes.CDLL:
     lib.gdn_ssm_workspace_bytes.restype = sz
     lib.gdn_paged_workspace_bytes.argtypes = [pptr]
     lib.gdn_paged_workspace_bytes.restype = sz
+    lib.gdn_extend_workspace_bytes.argtypes = [i32]
+    lib.gdn_extend_workspace_bytes.restype = sz
+    lib.gdn_shared_workspace_bytes.argtypes = [shptr]
+    lib.gdn_shared_workspace_bytes.restype = sz
+    lib.gdn_sample_workspace_bytes.argtypes = [saptr]
+    lib.gdn_sample_workspace_bytes.restype = sz
     _lib = lib
     return lib
 

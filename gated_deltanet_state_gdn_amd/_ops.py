@@ -17,7 +17,8 @@ import os
 
 import torch
 
-from ._lib import (GDN_BF16, GDN_ERR_DTYPE, GDN_ERR_SHAPE, GDN_F32, GdnError, GdnPagedDesc, GdnSsmDesc, load)
+from ._lib import (GDN_BF16, GDN_ERR_DTYPE, GDN_ERR_SHAPE, GDN_F32, GdnError, GdnPagedDesc, GdnSampleDesc, GdnSharedDesc,
+                   GdnSsmDesc, load)
 
 _DT = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_gdn_torch.so")
@@ -38,7 +39,9 @@ def _load():
         m.bind(GdnError, _raw_stream,
                *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
                    "gdn_conv", "gdn_conv_step", "gdn_ssm_scan", "gdn_ssm_step", "gdn_step", "gdn_qk_norm_rope",
-                   "gdn_paged_attn", "gdn_ssm_workspace_bytes", "gdn_paged_workspace_bytes")))
+                   "gdn_paged_attn", "gdn_ssm_workspace_bytes", "gdn_paged_workspace_bytes", "gdn_cache_extend",
+                   "gdn_shared_attn", "gdn_sample", "gdn_extend_workspace_bytes", "gdn_shared_workspace_bytes",
+                   "gdn_sample_workspace_bytes")))
         _native = m
     return _native
 
@@ -203,3 +206,87 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_len, *, max_
                                   scale=scale, o=o, lse=lse, ws=ws)
     return (_native or _load()).attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_len, max_kv_len, scale, o, lse,
                                      ws)
+
+
+def gdn_extend_workspace_bytes(n_seqs: int) -> int:
+    return int(load().gdn_extend_workspace_bytes(int(n_seqs)))
+
+
+def gdn_cache_extend(new_len, kv_len, block_table, free_pages, free_at, page_size: int, total_tokens: int, *, prefix_of=None,
+                     prefix_table=None, prefix_len=None, kv_out=None, free_out=None, cu_seqlens=None, slots=True,
+                     positions=True, ws=None, stream=None):
+    """A step's bookkeeping on the GPU: new_len, kv_len [n_seqs] int32, ``block_table`` [n_seqs, max_pages] int32
+    (updated in place), ``free_pages`` int32 of which the first free_at[0] are taken.
+
+    ``prefix_of`` [n_seqs]: the prefix that a request starts behind, -1 for one that goes on (None: all);
+    prefix_table [n_prefixes, max_prefix_pages] and prefix_len [n_prefixes], whole pages.  ``total_tokens``: a
+    bound on the sum of new_len, and the length of slots and positions.  ``kv_out`` may be kv_len, ``free_out``
+    free_at.  ``slots`` (int64), ``positions``: a tensor, True (allocate) or None.
+    Returns (cu_seqlens, kv_out, free_out, slots, positions).
+    """
+    if stream is not None:
+        with _on(stream, new_len):
+            return gdn_cache_extend(new_len, kv_len, block_table, free_pages, free_at, page_size, total_tokens,
+                                    prefix_of=prefix_of, prefix_table=prefix_table, prefix_len=prefix_len, kv_out=kv_out,
+                                    free_out=free_out, cu_seqlens=cu_seqlens, slots=slots, positions=positions, ws=ws)
+    return (_native or _load()).extend(new_len, kv_len, block_table, free_pages, free_at, page_size, total_tokens, prefix_of,
+                                       prefix_table, prefix_len, kv_out, free_out, cu_seqlens, slots, positions, ws)
+
+
+def make_shared_desc(q, k_cache, block_table, n_seqs, n_groups, *, max_kv_len=None, max_prefix_len=None,
+                     max_own_len=None) -> GdnSharedDesc:
+    """Sizes of a gdn_shared_attn call, for its workspace; the bounds as that call takes them."""
+    cache = make_paged_desc(q, k_cache, block_table, n_seqs, max_kv_len=max_kv_len)
+    most = cache.max_kv_len
+    return GdnSharedDesc(cache=cache, n_groups=int(n_groups),
+                         max_prefix_len=most if max_prefix_len is None else min(int(max_prefix_len), most),
+                         max_own_len=most if max_own_len is None else min(int(max_own_len), most))
+
+
+def gdn_shared_workspace_bytes(desc: GdnSharedDesc) -> int:
+    return int(load().gdn_shared_workspace_bytes(ctypes.byref(desc)))
+
+
+def gdn_shared_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_len, cu_groups, prefix_len, *, max_kv_len=None,
+                    max_prefix_len=None, max_own_len=None, scale=None, o=None, lse=None, ws=None, stream=None):
+    """gdn_paged_attn where the sequences cu_groups[g] .. cu_groups[g + 1] - 1 share their first prefix_len[g] tokens
+    (cu_groups [n_groups + 1], prefix_len [n_groups], int32): a prefix is read once for its group.
+
+    ``max_prefix_len``, ``max_own_len``: no prefix_len, no kv_len - prefix_len is larger (None: max_kv_len;
+    tight bounds spread the work better and need less workspace).  ``ws``, when given, holds
+    gdn_shared_workspace_bytes(make_shared_desc(...)) bytes.  The rest as gdn_paged_attn.
+    """
+    if stream is not None:
+        with _on(stream, q):
+            return gdn_shared_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_len, cu_groups, prefix_len,
+                                   max_kv_len=max_kv_len, max_prefix_len=max_prefix_len, max_own_len=max_own_len,
+                                   scale=scale, o=o, lse=lse, ws=ws)
+    return (_native or _load()).shared(q, k_cache, v_cache, block_table, cu_seqlens, kv_len, cu_groups, prefix_len, max_kv_len,
+                                       max_prefix_len, max_own_len, scale, o, lse, ws)
+
+
+def make_sample_desc(logits) -> GdnSampleDesc:
+    """Sizes of a gdn_sample call (logits [rows, vocab]), for its workspace."""
+    if logits.dim() != 2:
+        raise GdnError(GDN_ERR_SHAPE, "make_sample_desc: logits [rows, vocab]")
+    return GdnSampleDesc(logits.shape[0], logits.shape[1], _code(logits), logits.shape[1])
+
+
+def gdn_sample_workspace_bytes(desc: GdnSampleDesc) -> int:
+    return int(load().gdn_sample_workspace_bytes(ctypes.byref(desc)))
+
+
+def gdn_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, token=None, logprob=None, ws=None,
+               stream=None):
+    """The next token of each row of logits [rows, vocab] with the given uniform numbers u [rows] fp32 in [0, 1).
+
+    ``temperature``, ``top_p``, ``min_p`` [rows] fp32 and ``top_k`` [rows] int32: each row's settings (None: 1, off,
+    off, off).  ``logprob``: a tensor [rows] fp32 or True (allocate).  ``ws``, when given, holds
+    gdn_sample_workspace_bytes(make_sample_desc(logits)) bytes.  Returns token [rows] int32, or (token, logprob)
+    where logprob was asked for.
+    """
+    if stream is not None:
+        with _on(stream, logits):
+            return gdn_sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, token=token,
+                              logprob=logprob, ws=ws)
+    return (_native or _load()).sample(logits, u, temperature, top_k, top_p, min_p, token, logprob, ws)

@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 BINDING = os.path.join(PKG, "_gdn_torch.so")
 SOURCES = ["gdn_api.hip", "gdn_chunk_ws.hip", "gdn_relerr.hip", "gdn_adaptive.hip", "gdn_segment.hip",
-           "gdn_ops_api.hip", "gdn_conv.hip", "gdn_scan.hip", "gdn_step.hip", "gdn_rope.hip", "gdn_paged_attn.hip"]
+           "gdn_ops_api.hip", "gdn_conv.hip", "gdn_scan.hip", "gdn_step.hip", "gdn_rope.hip", "gdn_paged_attn.hip",
+           "gdn_shared_attn.hip", "gdn_extend.hip", "gdn_sample.hip"]
 # host-only sources: argument validation and launches
 API_SOURCES = ["gdn_api.hip", "gdn_ops_api.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")

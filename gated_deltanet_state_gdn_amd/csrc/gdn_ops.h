@@ -80,7 +80,40 @@ struct AttnArgs {
     int32_t n_seqs, h_q, h_kv, page_size, n_pages, max_pages, max_kv;
     int32_t splits, split_keys; // split s covers keys [s split_keys, (s + 1) split_keys)
     float scale;
+    // shared prefixes: cu_groups [n_groups + 1], prefix_len [n_groups]
+    const int32_t *groups, *prefix_len;
+    int32_t n_groups, max_prefix, max_own;
+    int32_t part_first;         // the launch's first part; in the join, the first part of the own keys
+    int32_t prefix_keys;        // the join: keys of a prefix's split
 };
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int bf16, int d, hipStream_t stream);
+hipError_t launch_shared_attn(const AttnArgs &a, const SharedPlan &p, int bf16, int d, hipStream_t stream);
+
+struct ExtendArgs {
+    const int32_t *new_len, *kv_len, *free_pages, *free_at;
+    const int32_t *prefix_of, *prefix_table, *prefix_len;      // nullable together
+    int32_t *table, *kv_out, *free_out, *cu;
+    int64_t *slots;             // [total], nullable
+    int32_t *positions;         // [total], nullable
+    int32_t *status;
+    int64_t *plan;              // workspace: per request, and what the second launch has to do
+    int64_t total;
+    int32_t n_seqs, page_size, max_pages, n_free, n_prefixes, max_prefix_pages;
+};
+hipError_t launch_extend(const ExtendArgs &a, hipStream_t stream);
+
+struct SampleArgs {
+    const void *logits;
+    const float *u, *temperature, *top_p, *min_p;              // all but u nullable
+    const int32_t *top_k;       // nullable
+    int32_t *token;
+    float *logprob;             // nullable
+    int32_t *status;
+    void *heads;                // workspace: a ChunkHead for each chunk of a row
+    uint64_t *bins;             // workspace: kSampleBins for each chunk of a row
+    int64_t stride;
+    int32_t rows, vocab, chunk, chunks;
+};
+hipError_t launch_sample(const SampleArgs &a, int bf16, hipStream_t stream);
 
 }  // namespace gdn

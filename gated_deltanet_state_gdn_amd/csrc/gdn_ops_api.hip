@@ -136,6 +136,62 @@ PagedPlan paged_plan(const gdn_paged_desc *d)
     return p;
 }
 
+// ---------------------------------------------------------------- shared prefixes
+int32_t check_shared(const gdn_shared_desc *d)
+{
+    if (!d) return GDN_ERR_NULL;
+    const int32_t st = check_paged(&d->cache);
+    if (st != GDN_OK) return st;
+    if (d->n_groups < 0 || d->max_prefix_len < 0 || d->max_own_len < 0 || d->max_prefix_len > (1 << 30) || d->max_own_len > (1 << 30) ||
+        (d->cache.n_seqs > 0 && d->n_groups == 0))
+        return refuse(GDN_ERR_SHAPE, "shared prefixes: bad bounds, or sequences without a group");
+    return GDN_OK;
+}
+struct SharedSizes {
+    gdn::SharedPlan attn;
+    size_t o, ml, bytes;
+};
+SharedSizes shared_sizes(const gdn_shared_desc *s)
+{
+    const gdn_paged_desc *d = &s->cache;
+    SharedSizes p;
+    p.attn = gdn::shared_plan(d->total_tokens, d->n_seqs, s->n_groups, d->h_q, d->h_kv, d->d, s->max_prefix_len, s->max_own_len,
+                              d->dtype == GDN_BF16);
+    const size_t rows = (size_t)(p.attn.prefix.splits + p.attn.own.splits) * (size_t)d->total_tokens * (size_t)d->h_q;
+    p.o = kWorkspaceBytes;
+    p.ml = p.o + rows * (size_t)d->d * sizeof(float);
+    p.bytes = p.ml + up256(rows * 2 * sizeof(float));
+    return p;
+}
+
+// ---------------------------------------------------------------- block tables
+size_t extend_bytes(int32_t n_seqs) { return kWorkspaceBytes + 256 + up256((size_t)n_seqs * 16); }
+
+// ---------------------------------------------------------------- next token
+int32_t check_sample(const gdn_sample_desc *d)
+{
+    if (!d) return GDN_ERR_NULL;
+    if (!known_dtype(d->dtype)) return refuse(GDN_ERR_DTYPE, "unknown dtype code");
+    if (d->rows < 0 || d->vocab <= 0 || d->vocab > (1 << 24) || d->stride < d->vocab || d->stride >= (1LL << 40))
+        return refuse(GDN_ERR_SHAPE, "sample: rows >= 0, a vocabulary of 1 to 2^24 tokens, stride >= vocab");
+    return GDN_OK;
+}
+struct SamplePlan {
+    int32_t chunk, chunks;
+    size_t bins, bytes;
+};
+SamplePlan sample_plan(const gdn_sample_desc *d)
+{
+    SamplePlan p;
+    p.chunk = gdn::sample_chunk(d->rows, d->vocab);
+    // a row may start inside a 16-byte piece
+    p.chunks = (int32_t)((d->vocab + 16 / elem_bytes(d->dtype) - 1 + p.chunk - 1) / p.chunk);
+    const size_t all = (size_t)d->rows * (size_t)p.chunks;
+    p.bins = kWorkspaceBytes + up256(all * 16);
+    p.bytes = p.bins + all * gdn::kSampleBins * sizeof(uint64_t);
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -340,6 +396,110 @@ int32_t gdn_paged_attn(const gdn_paged_desc *d, const void *q, const void *k_cac
     a.splits = p.attn.splits; a.split_keys = p.attn.split_keys;
     a.scale = d->scale;
     return launched(gdn::launch_attn(a, p.attn, d->dtype == GDN_BF16, d->d, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_shared_workspace_bytes(const gdn_shared_desc *d)
+{
+    return check_shared(d) == GDN_OK ? shared_sizes(d).bytes : 0;
+}
+
+int32_t gdn_shared_attn(const gdn_shared_desc *s, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                        const int32_t *cu, const int32_t *kv_len, const int32_t *cu_groups, const int32_t *prefix_len, void *o,
+                        float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    int32_t st = check_shared(s);
+    if (st != GDN_OK) return st;
+    const gdn_paged_desc *d = &s->cache;
+    if (!isfinite(d->scale)) return refuse(GDN_ERR_SHAPE, "the score scale is not finite");
+    const int64_t row = (int64_t)d->h_q * d->d;
+    if (!stride_ok(d->q_stride, row, d->dtype) || !stride_ok(d->o_stride, row, d->dtype))
+        return refuse(GDN_ERR_ALIGN, "q and output strides: at least a token's row, a multiple of 16 bytes");
+    if (!cu || !kv_len || !cu_groups || !prefix_len || (d->total_tokens > 0 && (!q || !o)) ||
+        (d->total_tokens > 0 && d->max_kv_len > 0 && (!k_cache || !v_cache || !block_table)))
+        return GDN_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(lse) || !aligned4(block_table) ||
+        !aligned4(cu) || !aligned4(kv_len) || !aligned4(cu_groups) || !aligned4(prefix_len))
+        return refuse(GDN_ERR_ALIGN, "pointer alignment: 16 bytes required (4 for lse and integer arrays)");
+    const SharedSizes p = shared_sizes(s);
+    st = check_ws(ws, ws_bytes, p.bytes);
+    if (st != GDN_OK || d->n_seqs == 0 || d->total_tokens == 0) return st;
+    char *w = static_cast<char *>(ws);
+    gdn::AttnArgs a = {};
+    a.q = q; a.kc = k_cache; a.vc = v_cache; a.table = block_table; a.cu = cu; a.kv_len = kv_len;
+    a.o = o; a.lse = lse; a.status = reinterpret_cast<int32_t *>(w);
+    a.part_o = reinterpret_cast<float *>(w + p.o);
+    a.part_ml = reinterpret_cast<float *>(w + p.ml);
+    a.qs = d->q_stride; a.os = d->o_stride;
+    a.page_stride = d->page_stride; a.token_stride = d->token_stride; a.head_stride = d->head_stride;
+    a.total = d->total_tokens;
+    a.n_seqs = d->n_seqs; a.h_q = d->h_q; a.h_kv = d->h_kv;
+    a.page_size = d->page_size; a.n_pages = d->n_pages; a.max_pages = d->max_pages; a.max_kv = d->max_kv_len;
+    a.scale = d->scale;
+    a.groups = cu_groups; a.prefix_len = prefix_len;
+    a.n_groups = s->n_groups; a.max_prefix = s->max_prefix_len; a.max_own = s->max_own_len;
+    return launched(gdn::launch_shared_attn(a, p.attn, d->dtype == GDN_BF16, d->d, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_extend_workspace_bytes(int32_t n_seqs) { return n_seqs >= 0 ? extend_bytes(n_seqs) : 0; }
+
+int32_t gdn_cache_extend(const gdn_extend_desc *d, const int32_t *new_len, const int32_t *kv_len, int32_t *block_table,
+                         const int32_t *free_pages, const int32_t *free_at, const int32_t *prefix_of, const int32_t *prefix_table,
+                         const int32_t *prefix_len, int32_t *kv_out, int32_t *free_out, int32_t *cu_seqlens, int64_t *slots,
+                         int32_t *positions, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!d) return GDN_ERR_NULL;
+    if (d->n_seqs < 0 || d->page_size <= 0 || d->max_pages < 0 || d->n_free < 0 || d->n_prefixes < 0 || d->max_prefix_pages < 0 ||
+        d->total_tokens < 0 || d->total_tokens > 0x7fffffffLL)
+        return refuse(GDN_ERR_SHAPE, "cache extension: bad sizes");
+    if (!free_at || !free_out || !cu_seqlens || (d->n_seqs > 0 && (!new_len || !kv_len || !kv_out)) ||
+        (d->n_seqs > 0 && d->max_pages > 0 && !block_table) || (d->n_free > 0 && !free_pages) ||
+        (d->n_prefixes > 0 && (!prefix_of || !prefix_len || (d->max_prefix_pages > 0 && !prefix_table))))
+        return GDN_ERR_NULL;
+    if (!aligned4(new_len) || !aligned4(kv_len) || !aligned4(block_table) || !aligned4(free_pages) || !aligned4(free_at) ||
+        !aligned4(prefix_of) || !aligned4(prefix_table) || !aligned4(prefix_len) || !aligned4(kv_out) || !aligned4(free_out) ||
+        !aligned4(cu_seqlens) || ((uintptr_t)slots & 7u) || !aligned4(positions))
+        return refuse(GDN_ERR_ALIGN, "pointer alignment: an element's");
+    const int32_t st = check_ws(ws, ws_bytes, extend_bytes(d->n_seqs));
+    if (st != GDN_OK) return st;
+    gdn::ExtendArgs a = {};
+    a.new_len = new_len; a.kv_len = kv_len; a.free_pages = free_pages; a.free_at = free_at;
+    a.prefix_of = d->n_prefixes > 0 ? prefix_of : nullptr; a.prefix_table = prefix_table; a.prefix_len = prefix_len;
+    a.table = block_table; a.kv_out = kv_out; a.free_out = free_out; a.cu = cu_seqlens; a.slots = slots; a.positions = positions;
+    a.status = static_cast<int32_t *>(ws);
+    a.plan = reinterpret_cast<int64_t *>(static_cast<char *>(ws) + kWorkspaceBytes);
+    a.total = d->total_tokens;
+    a.n_seqs = d->n_seqs; a.page_size = d->page_size; a.max_pages = d->max_pages; a.n_free = d->n_free;
+    a.n_prefixes = d->n_prefixes; a.max_prefix_pages = d->max_prefix_pages;
+    return launched(gdn::launch_extend(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_sample_workspace_bytes(const gdn_sample_desc *d)
+{
+    return check_sample(d) == GDN_OK ? sample_plan(d).bytes : 0;
+}
+
+int32_t gdn_sample(const gdn_sample_desc *d, const void *logits, const float *u, const float *temperature, const int32_t *top_k,
+                   const float *top_p, const float *min_p, int32_t *token, float *logprob, void *ws, size_t ws_bytes, void *stream)
+{
+    int32_t st = check_sample(d);
+    if (st != GDN_OK) return st;
+    if (d->rows > 0 && (!logits || !u || !token)) return GDN_ERR_NULL;
+    if (((uintptr_t)logits & (uintptr_t)(elem_bytes(d->dtype) - 1)) || !aligned4(u) || !aligned4(temperature) || !aligned4(top_k) ||
+        !aligned4(top_p) || !aligned4(min_p) || !aligned4(token) || !aligned4(logprob))
+        return refuse(GDN_ERR_ALIGN, "pointer alignment: an element's");
+    const SamplePlan p = sample_plan(d);
+    st = check_ws(ws, ws_bytes, p.bytes);
+    if (st != GDN_OK || d->rows == 0) return st;
+    char *w = static_cast<char *>(ws);
+    gdn::SampleArgs a = {};
+    a.logits = logits; a.u = u; a.temperature = temperature; a.top_p = top_p; a.min_p = min_p; a.top_k = top_k;
+    a.token = token; a.logprob = logprob;
+    a.status = reinterpret_cast<int32_t *>(w);
+    a.heads = w + kWorkspaceBytes;
+    a.bins = reinterpret_cast<uint64_t *>(w + p.bins);
+    a.stride = d->stride;
+    a.rows = d->rows; a.vocab = d->vocab; a.chunk = p.chunk; a.chunks = p.chunks;
+    return launched(gdn::launch_sample(a, d->dtype == GDN_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

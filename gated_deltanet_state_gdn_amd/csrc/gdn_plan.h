@@ -180,4 +180,28 @@ inline AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_
     return p;
 }
 
+// ------------------------------------------------------------- attention behind shared prefixes
+struct SharedPlan {
+    AttnPlan prefix, own;       // no splits: the side has no keys
+};
+inline SharedPlan shared_plan(int64_t total, int32_t n_seqs, int32_t n_groups, int32_t h_q, int32_t h_kv, int32_t d,
+                              int32_t max_prefix, int32_t max_own, int bf16)
+{
+    SharedPlan p;
+    p.prefix = attn_plan(total, n_groups, h_q, h_kv, d, max_prefix, bf16);
+    p.own = attn_plan(total, n_seqs, h_q, h_kv, d, max_own, bf16);
+    if (max_prefix == 0) p.prefix.splits = 0;
+    if (max_own == 0) p.own.splits = 0;
+    return p;
+}
+
+// ------------------------------------------------------------- next token
+constexpr int kSampleBins = 256;
+
+// Elements of a chunk, one workgroup's.
+inline int32_t sample_chunk(int64_t rows, int32_t vocab)
+{
+    return rows * ((vocab + 8191) / 8192) < 512 ? 2048 : 8192;
+}
+
 }  // namespace gdn

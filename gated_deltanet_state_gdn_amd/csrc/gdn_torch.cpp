@@ -36,6 +36,12 @@ typedef decltype(&gdn_qk_norm_rope) rope_fn;
 typedef decltype(&gdn_paged_attn) attn_fn;
 typedef decltype(&gdn_ssm_workspace_bytes) scan_ws_fn;
 typedef decltype(&gdn_paged_workspace_bytes) attn_ws_fn;
+typedef decltype(&gdn_cache_extend) extend_fn;
+typedef decltype(&gdn_shared_attn) shared_fn;
+typedef decltype(&gdn_sample) sample_fn;
+typedef decltype(&gdn_extend_workspace_bytes) extend_ws_fn;
+typedef decltype(&gdn_shared_workspace_bytes) shared_ws_fn;
+typedef decltype(&gdn_sample_workspace_bytes) sample_ws_fn;
 conv_fn f_conv;
 conv_step_fn f_conv_step;
 scan_fn f_scan;
@@ -45,10 +51,18 @@ rope_fn f_rope;
 attn_fn f_attn;
 scan_ws_fn f_scan_ws;
 attn_ws_fn f_attn_ws;
+extend_fn f_extend;
+shared_fn f_shared;
+sample_fn f_sample;
+extend_ws_fn f_extend_ws;
+shared_ws_fn f_shared_ws;
+sample_ws_fn f_sample_ws;
 
 const at::Tensor none;
 constexpr auto F32 = at::kFloat;
 constexpr auto I32 = at::kInt;
+constexpr auto I64 = at::kLong;
+constexpr int kFunctions = 15;   // of the C library
 
 // The call's name and what its tensors have in common.
 struct Call {
@@ -492,11 +506,125 @@ PyObject *attn(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
     });
 }
 
-// GdnError, the raw-stream function, and the addresses of the nine C functions in this order.
+// A bound on a device array's values, at most `most`.
+int32_t bound(const Call &c, PyObject *o, int32_t most, const char *arg) {
+    if (o == Py_None) return most;
+    const int64_t v = integer(o);
+    if (v < 0 || v > (1 << 30)) c.refuse(GDN_ERR_SHAPE, arg, "out of range");
+    return v < most ? (int32_t)v : most;
+}
+
+// q, k_cache, v_cache, table, cu, kv_len, cu_groups, prefix_len, max_kv, max_prefix, max_own, scale, o, lse, ws
+PyObject *shared(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
+    return guarded(nargs, 15, [&] {
+        Call c{"gdn_shared_attn"};
+        Paged p(c, v[0], v[1], v[2], v[3], v[4], v[5], v[8]);
+        const at::Tensor &groups = c.tensor(v[6], "cu_groups"), &prefix = c.tensor(v[7], "prefix_len");
+        c.need(groups.dim() == 1 && groups.numel() > 0, "cu_groups [n_groups + 1]");
+        const int64_t n = groups.numel() - 1, T = p.d.total_tokens;
+        c.whole(groups, {n + 1}, I32, "cu_groups");
+        c.whole(prefix, {n}, I32, "prefix_len");
+        const auto e = p.q.scalar_type();
+        if (v[11] != Py_None) p.d.scale = (float)number(v[11]);
+        at::Tensor o, lse;
+        if (v[12] != Py_None) p.d.o_stride = c.rows(o = c.tensor(v[12], "o"), {T, p.d.h_q, p.d.d}, e, "o");
+        const Out kind = out_kind(v[13]);
+        if (kind == Out::given) c.whole(lse = c.tensor(v[13], "lse"), {T, p.d.h_q}, F32, "lse");
+        const int32_t most = p.d.max_kv_len;
+        gdn_shared_desc d = {p.d, c.size32(n), bound(c, v[9], most, "max_prefix_len"), bound(c, v[10], most, "max_own_len")};
+        c.on_gpu();
+        c10::DeviceGuard guard(c.device);
+        if (!o.defined()) o = c.make({T, p.d.h_q, p.d.d}, e);
+        if (kind == Out::make) lse = c.make({T, p.d.h_q}, F32);
+        const at::Tensor ws = c.workspace(v[14], v[14] == Py_None ? f_shared_ws(&d) : 0);
+        c.check(f_shared(&d, ptr(p.q), ptr(p.kc), ptr(p.vc), ptr<int32_t>(p.table), ptr<int32_t>(p.cu), ptr<int32_t>(p.kv),
+                         ptr<int32_t>(groups), ptr<int32_t>(prefix), ptr(o), ptr<float>(lse), ptr(ws), ws.numel(), c.stream()));
+        return lse.defined() ? pack({wrap(o), wrap(lse)}) : wrap(o);
+    });
+}
+
+// new_len, kv_len, table, free_pages, free_at, page_size, total_tokens, prefix_of, prefix_table, prefix_len, kv_out, free_out, cu, slots,
+// positions, ws
+PyObject *extend(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
+    return guarded(nargs, 16, [&] {
+        Call c{"gdn_cache_extend"};
+        const at::Tensor &add = c.tensor(v[0], "new_len"), &kv = c.tensor(v[1], "kv_len"), &table = c.tensor(v[2], "block_table");
+        const at::Tensor &pages = c.tensor(v[3], "free_pages"), &taken = c.tensor(v[4], "free_at");
+        const at::Tensor &of = c.tensor(v[7], "prefix_of", true), &pt = c.tensor(v[8], "prefix_table", true), &pl = c.tensor(v[9], "prefix_len", true);
+        c.need(add.dim() == 1 && table.dim() == 2 && pages.dim() == 1, "new_len [n_seqs], block_table [n_seqs, max_pages], free_pages [n]");
+        const int64_t n = add.size(0), most = table.size(1), ps = integer(v[5]), T = integer(v[6]);
+        c.need(ps > 0 && T >= 0, "page_size is positive, total_tokens not negative");
+        c.whole(add, {n}, I32, "new_len");
+        c.whole(kv, {n}, I32, "kv_len");
+        c.whole(table, {n, most}, I32, "block_table");
+        c.whole(pages, {pages.size(0)}, I32, "free_pages");
+        c.whole(taken, {1}, I32, "free_at");
+        gdn_extend_desc d = {c.size32(n), c.size32(ps), c.size32(most), c.size32(pages.size(0)), 0, 0, T};
+        if (of.defined() || pt.defined() || pl.defined()) {
+            c.need(of.defined() && pt.defined() && pl.defined() && pt.dim() == 2, "prefix_of, prefix_table [n_prefixes, max_prefix_pages], prefix_len: all or none");
+            d.n_prefixes = c.size32(pt.size(0));
+            d.max_prefix_pages = c.size32(pt.size(1));
+            c.whole(of, {n}, I32, "prefix_of");
+            c.whole(pt, {pt.size(0), pt.size(1)}, I32, "prefix_table");
+            c.whole(pl, {pt.size(0)}, I32, "prefix_len");
+        }
+        at::Tensor kvo, fo, cu, slots, pos;
+        if (v[10] != Py_None) c.whole(kvo = c.tensor(v[10], "kv_out"), {n}, I32, "kv_out");
+        if (v[11] != Py_None) c.whole(fo = c.tensor(v[11], "free_out"), {1}, I32, "free_out");
+        if (v[12] != Py_None) c.whole(cu = c.tensor(v[12], "cu_seqlens"), {n + 1}, I32, "cu_seqlens");
+        const Out sk = out_kind(v[13]), pk = out_kind(v[14]);
+        if (sk == Out::given) c.whole(slots = c.tensor(v[13], "slots"), {T}, I64, "slots");
+        if (pk == Out::given) c.whole(pos = c.tensor(v[14], "positions"), {T}, I32, "positions");
+        c.on_gpu();
+        c10::DeviceGuard guard(c.device);
+        if (!kvo.defined()) kvo = c.make({n}, I32);
+        if (!fo.defined()) fo = c.make({1}, I32);
+        if (!cu.defined()) cu = c.make({n + 1}, I32);
+        if (sk == Out::make) slots = c.make({T}, I64);
+        if (pk == Out::make) pos = c.make({T}, I32);
+        const at::Tensor ws = c.workspace(v[15], v[15] == Py_None ? f_extend_ws(d.n_seqs) : 0);
+        c.check(f_extend(&d, ptr<int32_t>(add), ptr<int32_t>(kv), ptr<int32_t>(table), ptr<int32_t>(pages), ptr<int32_t>(taken),
+                         ptr<int32_t>(of), ptr<int32_t>(pt), ptr<int32_t>(pl), ptr<int32_t>(kvo), ptr<int32_t>(fo), ptr<int32_t>(cu),
+                         ptr<int64_t>(slots), ptr<int32_t>(pos), ptr(ws), ws.numel(), c.stream()));
+        return pack({wrap(cu), wrap(kvo), wrap(fo), wrap(slots), wrap(pos)});
+    });
+}
+
+// logits, u, temperature, top_k, top_p, min_p, token, logprob, ws
+PyObject *sample(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
+    return guarded(nargs, 9, [&] {
+        Call c{"gdn_sample"};
+        const at::Tensor &x = c.tensor(v[0], "logits"), &u = c.tensor(v[1], "u"), &t = c.tensor(v[2], "temperature", true);
+        const at::Tensor &k = c.tensor(v[3], "top_k", true), &p = c.tensor(v[4], "top_p", true), &m = c.tensor(v[5], "min_p", true);
+        const int32_t dt = c.code(x);
+        c.need(x.dim() == 2, "logits [rows, vocab]");
+        const int64_t n = x.size(0), vocab = x.size(1);
+        gdn_sample_desc d = {c.size32(n), c.size32(vocab), dt, c.rows(x, {n, vocab}, x.scalar_type(), "logits")};
+        c.whole(u, {n}, F32, "u");
+        c.whole(t, {n}, F32, "temperature");
+        c.whole(k, {n}, I32, "top_k");
+        c.whole(p, {n}, F32, "top_p");
+        c.whole(m, {n}, F32, "min_p");
+        at::Tensor token, lp;
+        if (v[6] != Py_None) c.whole(token = c.tensor(v[6], "token"), {n}, I32, "token");
+        const Out kind = out_kind(v[7]);
+        if (kind == Out::given) c.whole(lp = c.tensor(v[7], "logprob"), {n}, F32, "logprob");
+        c.on_gpu();
+        c10::DeviceGuard guard(c.device);
+        if (!token.defined()) token = c.make({n}, I32);
+        if (kind == Out::make) lp = c.make({n}, F32);
+        const at::Tensor ws = c.workspace(v[8], v[8] == Py_None ? f_sample_ws(&d) : 0);
+        c.check(f_sample(&d, ptr(x), ptr<float>(u), ptr<float>(t), ptr<int32_t>(k), ptr<float>(p), ptr<float>(m), ptr<int32_t>(token),
+                         ptr<float>(lp), ptr(ws), ws.numel(), c.stream()));
+        return lp.defined() ? pack({wrap(token), wrap(lp)}) : wrap(token);
+    });
+}
+
+// GdnError, the raw-stream function, and the addresses of the C functions in this order.
 PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
-    return guarded(nargs, 11, [&]() -> PyObject * {
-        void *f[9];
-        for (int i = 0; i < 9; ++i) {
+    return guarded(nargs, 2 + kFunctions, [&]() -> PyObject * {
+        void *f[kFunctions];
+        for (int i = 0; i < kFunctions; ++i) {
             f[i] = PyLong_AsVoidPtr(v[2 + i]);
             if (!f[i]) {
                 if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a function's address is zero");
@@ -516,13 +644,20 @@ PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
         f_attn = (attn_fn)f[6];
         f_scan_ws = (scan_ws_fn)f[7];
         f_attn_ws = (attn_ws_fn)f[8];
+        f_extend = (extend_fn)f[9];
+        f_shared = (shared_fn)f[10];
+        f_sample = (sample_fn)f[11];
+        f_extend_ws = (extend_ws_fn)f[12];
+        f_shared_ws = (shared_ws_fn)f[13];
+        f_sample_ws = (sample_ws_fn)f[14];
         Py_RETURN_NONE;
     });
 }
 
 #define GDN_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GDN_METHOD(bind), GDN_METHOD(conv), GDN_METHOD(conv_step), GDN_METHOD(scan), GDN_METHOD(ssm_step),
-                         GDN_METHOD(step), GDN_METHOD(rope), GDN_METHOD(attn), {nullptr, nullptr, 0, nullptr}};
+                         GDN_METHOD(step), GDN_METHOD(rope), GDN_METHOD(attn), GDN_METHOD(shared), GDN_METHOD(extend), GDN_METHOD(sample),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

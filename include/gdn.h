@@ -376,6 +376,83 @@ int32_t gdn_paged_attn(const gdn_paged_desc *desc, const void *q, const void *k_
                        const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *kv_len,
                        void *o, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Around the steps of a server that keeps prefixes (technical summary, "Mecanismos Principais": the
+ * full-attention keys and values of a matched prefix are kept exactly, and requests that match it read
+ * them): the bookkeeping of a step, attention of requests that share prefixes, and the draw of
+ * the next token.  Conventions as above.
+ * --------------------------------------------------------------------------------------- */
+
+/* What follows from the requests' new lengths, on the device.  Request n has kv_len[n] cached tokens, or
+ * with prefix_of[n] = p >= 0 (prefix_of NULL or -1: none) starts behind prefix p: base = prefix_len[p] (whole pages),
+ * and its table's first entries are those of prefix_table [n_prefixes, max_prefix_pages].  It gets
+ * new_len[n] >= 0 tokens more, and the pages that these begin, from the list of free ones: free_pages[*free_at] on, in
+ * the order of the requests.  Results:
+ *   block_table [n_seqs, max_pages]  the prefixes' and the taken pages' entries (others are left as they were),
+ *   kv_out [n_seqs]      base + new_len (may be kv_len),
+ *   free_out [1]         *free_at + the pages taken (may be free_at),
+ *   cu_seqlens [n_seqs + 1]  offsets of the requests' new tokens,
+ *   slots (nullable) [total_tokens] int64   page * page_size + place in the page of each new token,
+ *   positions (nullable) [total_tokens]     and its position; -1 in both behind the last new token.
+ * total_tokens: at least the sum of new_len (known on the host as a bound; larger under a captured graph).
+ * A step that does not fit (a length or prefix out of range, a prefix that ends inside a page, more than
+ * max_pages, n_free or total_tokens) sets the status bit and takes nothing: tables as they were, kv_out =
+ * kv_len, free_out = free_at, cu_seqlens 0, slots and positions -1.  Page numbers are taken as they are. */
+typedef struct {
+    int32_t n_seqs, page_size, max_pages;
+    int32_t n_free;            /* entries of free_pages, the taken ones among them */
+    int32_t n_prefixes, max_prefix_pages;
+    int64_t total_tokens;
+} gdn_extend_desc;
+size_t gdn_extend_workspace_bytes(int32_t n_seqs);
+int32_t gdn_cache_extend(const gdn_extend_desc *desc, const int32_t *new_len, const int32_t *kv_len, int32_t *block_table,
+                         const int32_t *free_pages, const int32_t *free_at, const int32_t *prefix_of,
+                         const int32_t *prefix_table, const int32_t *prefix_len, int32_t *kv_out, int32_t *free_out,
+                         int32_t *cu_seqlens, int64_t *slots, int32_t *positions, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* gdn_paged_attn for sequences in groups: those of group g, [cu_groups[g], cu_groups[g + 1]), hold the same
+ * keys and values in their first prefix_len[g] tokens (the same pages; where a prefix ends inside a page, copies of
+ * its part), which are read once for all of them, through the block table of the group's first sequence.  The result is
+ * gdn_paged_attn's on the same tables, to rounding.  cu_groups [n_groups + 1] covers all sequences; a group may
+ * be one sequence, or have no prefix (0).  Causality holds inside the prefix too: a token whose position is
+ * in it sees the keys at its position and before, and its sequence's kv_len may be less than the prefix.  The
+ * first sequence's table names all of the prefix's pages even then, or if it has no new token.  A bad cu_groups,
+ * prefix_len, cu_seqlens, kv_len or page sets the status bit; the outputs of those groups are unspecified.
+ * Precision as of gdn_paged_attn, the rows of a prefix being those of its group. */
+typedef struct {
+    gdn_paged_desc cache;
+    int32_t n_groups;
+    int32_t max_prefix_len;    /* no prefix_len is larger (host copy), at most 2^30 */
+    int32_t max_own_len;       /* no kv_len - prefix_len is larger, at most 2^30 */
+} gdn_shared_desc;
+size_t gdn_shared_workspace_bytes(const gdn_shared_desc *desc);
+int32_t gdn_shared_attn(const gdn_shared_desc *desc, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *kv_len,
+                        const int32_t *cu_groups, const int32_t *prefix_len, void *o, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* The next token of each row of logits [rows, vocab] (rows `stride` elements apart, any alignment).  Settings are
+ * per row, nullable: temperature T >= 0 (NULL: 1), top_k >= 0 (0: off), top_p in (0, 1] (1: off), min_p in [0, 1]
+ * (0: off), u in [0, 1) the given uniform numbers.  In the order of falling logits, ties by rising index,
+ * with weights w_i = exp((x_i - max x) / T), stay: the first top_k; of these the first so many that their mass is at
+ * least top_p of theirs; and of these those with w_i >= min_p.  token: the first at which the running mass passes
+ * u times the mass of what stayed, so u = 0 is the likeliest.  T = 0: the first of the largest.  logprob
+ * (nullable): ln of the token's share of the mass that stayed, 0 for T = 0.  Logits of -inf are never
+ * drawn; NaN counts as -inf and +inf as the highest fp32 value.  A row without any other gives -1, and
+ * a logprob of -inf; so does one whose settings are out of range, which also sets the status bit.
+ * Computed in 64 bits: the token is the formula's unless u or top_p is closer than about 2^-36 to where
+ * the next one begins; weights under e^-32 of the largest count as 0. */
+typedef struct {
+    int32_t rows, vocab;       /* vocab at most 2^24 */
+    int32_t dtype;             /* gdn_dtype of the logits */
+    int64_t stride;
+} gdn_sample_desc;
+size_t gdn_sample_workspace_bytes(const gdn_sample_desc *desc);
+int32_t gdn_sample(const gdn_sample_desc *desc, const void *logits, const float *u, const float *temperature,
+                   const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *logprob,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
