@@ -23,7 +23,7 @@
 namespace gdn {
 namespace {
 
-constexpr int BINS = kSampleBins, NT1 = 256, NT2 = 1024, CAP = 4096;
+constexpr int BINS = kSampleBins, NT1 = 256, NT2 = 1024, CAP = 12288, FEW = 256;
 constexpr double kUnit = 34359738368.0;                  // 2^35 units: a weight of 1
 constexpr float kHighest = 3.402823466e38f;
 constexpr uint64_t kMass = (1ull << 49) - 1;             // a chunk's bin: mass below, count from bit 49
@@ -55,12 +55,9 @@ __device__ __forceinline__ Row settings(const SampleArgs &a, int row)
     return r;
 }
 
-// A logit: NaN is taken as -inf, +inf as the highest value, -0 as 0.
-__device__ __forceinline__ float logit(float x) { return x != x ? -INFINITY : fminf(x, kHighest) + 0.0f; }
-
-// exp(f / 8) in units, |f| <= 1/2: the series to the sixth power, off by 7.4e-13 = 2^-40 at most.  `far`: bins so far
-// from 0 that a bin is a single value of x; all of them weigh the same.
-__device__ __forceinline__ uint64_t units(double f, bool far)
+// exp(f / 8) in units, |f| <= 1/2, as the low 52 bits of a number of exponent 2^52: the series to the sixth power,
+// off by 7.4e-13 = 2^-40 at most.
+__device__ __forceinline__ uint64_t units_bits(double f)
 {
     double p = 1.0 / 188743680.0;                        // 8^-6 / 6!
     p = fma(p, f, 1.0 / 3932160.0);
@@ -69,36 +66,50 @@ __device__ __forceinline__ uint64_t units(double f, bool far)
     p = fma(p, f, 1.0 / 128.0);
     p = fma(p, f, 1.0 / 8.0);
     p = fma(p, f, 1.0);
-    // 2^52 + p 2^35, whose last bits are the rounded units
-    const uint64_t bits = (uint64_t)__double_as_longlong(fma(p, kUnit, 4503599627370496.0)) & ((1ull << 52) - 1);
-    return far ? 1ull << 35 : bits;
+    return (uint64_t)__double_as_longlong(fma(p, kUnit, 4503599627370496.0));
+}
+constexpr uint64_t kExp52 = 0x4330000000000000ull;       // the bits of 2^52
+
+// Bins so far from 0 that neighbouring values of x are many apart: all tokens of the first 256 are equal.
+__device__ __forceinline__ bool is_far(double t) { return fabs(t) > 1125899906842624.0; }     // 2^50
+// rint(d scale): in the low bits of the sum with 1.5 2^52, unless it is far.  The bin of a token is found by this alone,
+// so that every kernel and pass puts it in the same one.
+constexpr double kRound = 6755399441055744.0;
+__device__ __forceinline__ double bin_of_logit(double d, double scale, bool far)
+{
+    return far ? rint(d * scale) : fma(d, scale, kRound) - kRound;
 }
 
-// A row's tokens in 16-byte pieces: piece v holds the elements [v V - lead, v V - lead + V), whole or at the row's ends in
+// A row's tokens in 16-byte pieces: piece v holds the elements [v V - lead, v V - lead + V), at the row's ends in
 // part (rows start anywhere).  Elements that are not the row's are -inf.
 template <class E>
 struct RowReader {
     typedef typename E::T T;
     const T *base;
-    int32_t vocab, lead;
+    int32_t vocab, lead, whole0, whole1;                 // pieces [whole0, whole1) are whole
     __device__ __forceinline__ RowReader(const SampleArgs &a, int row)
     {
         base = static_cast<const T *>(a.logits) + (int64_t)row * a.stride;
         vocab = a.vocab;
         lead = (int32_t)(((uintptr_t)base & 15) / sizeof(T));
+        whole0 = lead ? 1 : 0;
+        whole1 = (vocab + lead) / E::V;
     }
     __device__ __forceinline__ int32_t first(int32_t v) const { return v * E::V - lead; }
-    __device__ __forceinline__ int32_t pieces() const { return (vocab + lead + E::V - 1) / E::V; }
-    __device__ __forceinline__ void read(int32_t v, float *x) const
+    __device__ __forceinline__ bool is_whole(int32_t v) const { return v >= whole0 && v < whole1; }
+    // any whole piece for one that is not, so that no load waits for a branch
+    __device__ __forceinline__ u32x4 load(int32_t v) const
     {
-        const int32_t i0 = first(v);
-        if (i0 >= 0 && i0 + E::V <= vocab) {
-            E::unpack(load16(base + i0), x);
+        if (whole0 >= whole1) return u32x4{0, 0, 0, 0};
+        return load16(base + first(v < whole0 ? whole0 : v < whole1 ? v : whole1 - 1));
+    }
+    __device__ __forceinline__ float one(int32_t i) const { return i >= 0 && i < vocab ? E::one(base + i) : -INFINITY; }
+    __device__ __forceinline__ void unpack(int32_t v, u32x4 raw, float *x) const
+    {
+        E::unpack(raw, x);
+        if (!is_whole(v)) {
 #pragma unroll
-            for (int i = 0; i < E::V; ++i) x[i] = logit(x[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E::V; ++i) x[i] = i0 + i >= 0 && i0 + i < vocab ? logit(E::one(base + i0 + i)) : -INFINITY;
+            for (int i = 0; i < E::V; ++i) x[i] = one(first(v) + i);
         }
     }
 };
@@ -108,26 +119,31 @@ template <class E, int PIECES>
 __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
 {
     constexpr int N = PIECES * E::V;                     // elements of a thread
-    __shared__ uint64_t bins[BINS];
+    __shared__ uint64_t bins[BINS + 1];                  // and one that takes what is behind the last
     __shared__ float wmax[NT1 / 64];
     __shared__ int first;
     const int row = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
     const Row r = settings(a, row);
     if (!r.ok) return;
     const RowReader<E> in(a, row);
+    const int32_t v0 = c * PIECES * NT1 + (int)threadIdx.x;
+    u32x4 raw[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) raw[i] = in.load(v0 + i * NT1);
     float x[N];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) in.read((c * PIECES + i) * NT1 + (int)threadIdx.x, x + i * E::V);
-    float m = x[0];
+    for (int i = 0; i < PIECES; ++i) in.unpack(v0 + i * NT1, raw[i], x + i * E::V);
+    // NaN loses against any number here, and every comparison below
+    float m = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+    for (int i = 0; i < N; ++i) m = fmaxf(m, x[i]);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
     bins[threadIdx.x] = 0;
     if (threadIdx.x == 0) first = 0x7fffffff;
     if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+    m = fminf(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), kHighest);
     ChunkHead *head = static_cast<ChunkHead *>(a.heads) + blockIdx.x;
     if (m == -INFINITY) {
         if (threadIdx.x == 0) head->max = m;
@@ -137,7 +153,7 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
         int at = 0x7fffffff;
 #pragma unroll
         for (int i = N - 1; i >= 0; --i)
-            if (x[i] == m) at = in.first((c * PIECES + i / E::V) * NT1 + (int)threadIdx.x) + i % E::V;
+            if (fminf(x[i], kHighest) == m) at = in.first(v0 + i / E::V * NT1) + i % E::V;
         if (at != 0x7fffffff) atomicMin(&first, at);
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -146,12 +162,27 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
         }
         return;
     }
-    const double t0 = (double)m * r.scale, top = rint(t0);
-    const bool far = fabs(t0) > 1125899906842624.0;      // 2^50
+    typedef unsigned long long u64;
+    const bool far = is_far((double)m * r.scale);
+    const double top = bin_of_logit((double)m, r.scale, far);
+    if (far) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const double d = (double)x[i], b = rint(d * r.scale), below = top - b;
-        if (below < (double)BINS) atomicAdd(reinterpret_cast<unsigned long long *>(&bins[(int)below]), (unsigned long long)(units(fma(d, r.scale, -b), far) + (1ull << 49)));
+        for (int i = 0; i < N; ++i)
+            if (fminf(x[i], kHighest) == m) atomicAdd(reinterpret_cast<u64 *>(&bins[0]), (u64)((1ull << 49) + (1ull << 35)));
+    } else {
+        // what lies below has no bin; with min-p and without top-p, which wants the mass of all, what min-p drops
+        double below = 33.0 * (double)r.T;
+        if (r.min_p > 0.0f && r.top_p >= 1.0f) below = fmin(below, -1.001 * (double)r.T * log((double)r.min_p));
+        const float low = (float)((double)m - below - 1e-6 * fabs((double)m));
+        const uint32_t top_bits = (uint32_t)__double_as_longlong(top + kRound);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (x[i] >= low) {
+                const double d = (double)fminf(x[i], kHighest), k = fma(d, r.scale, kRound);
+                const uint32_t at = top_bits - (uint32_t)__double_as_longlong(k);
+                atomicAdd(reinterpret_cast<u64 *>(&bins[at < BINS ? at : BINS]),
+                          (u64)(units_bits(fma(d, r.scale, kRound - k)) + ((1ull << 49) - kExp52)));
+            }
     }
     __syncthreads();
     a.bins[(int64_t)blockIdx.x * BINS + threadIdx.x] = bins[threadIdx.x];
@@ -175,35 +206,12 @@ __device__ __forceinline__ float logit_of(uint64_t o)
 }
 __device__ __forceinline__ int32_t index_of(uint64_t o) { return (int32_t)(uint32_t)o; }
 
-// The first i in [lo, hi) with is(i), which holds from some i on; hi if none.
-template <class F>
-__device__ __forceinline__ int first_that(int lo, int hi, F is)
-{
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (is(mid)) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
-struct Shared {
-    uint64_t list[CAP];         // tokens of the bins that are looked at, in order
-    double run[CAP];            // the row's mass through each of them
-    double mass[BINS];          // the row's mass through each bin
-    uint32_t count[BINS];
-    uint64_t sub[NT2];          // units and counts of the bins, then of a bin's parts
-    uint32_t subcount[NT2];
-    double wsum[NT2 / 64];
-    uint32_t n;
-};
-
 // Where a first part of the order ends: at its count-th token, at the first token through which the mass is at least or
 // more than so much, or behind the last token that is not behind `order`.
 struct Border {
     enum Kind { kCount, kMass, kPassed, kOrder } kind;
-    double mass;
     uint32_t count;
+    double mass;
     uint64_t order;
     // whether tokens of so much mass and count together, the last of them not behind `end`, reach it
     __device__ __forceinline__ bool reached(double m, uint32_t c, uint64_t end) const
@@ -212,195 +220,560 @@ struct Border {
     }
 };
 
+// What the first wave wants to see next.  All at once: the tokens of the wanted bins.  Else: those of bin j0, or of so much
+// of it that a border is in.
+struct Plan {
+    Border border;
+    uint64_t to;                // no token behind this
+    double front;               // mass and count in front of the part (-1: all earlier bins')
+    uint32_t before;
+    float lo[2], hi[2];         // the wanted tokens' logits are in one of these ranges,
+    uint64_t units;             // and they in these parts of the row
+    int j0;
+    bool once, listed, done;
+};
+
+struct Shared {
+    uint64_t list[CAP];         // tokens about the borders, in no order
+    uint64_t few[FEW];          // the tokens that are looked at, in order,
+    double run[FEW];            // and the row's mass through each of them
+    double factor[BINS];        // exp(-j / 8)
+    double mass[BINS];          // the row's mass and count through each bin
+    uint32_t count[BINS];
+    uint64_t units[BINS];       // the parts of the row that have tokens of a bin
+    uint8_t want[BINS];
+    uint64_t sub[NT2];          // units and counts of the bins, then of a bin's parts
+    uint32_t subcount[NT2];
+    double wsum[NT2 / 64];
+    uint32_t wcount[NT2 / 64];
+    Plan plan;
+    uint32_t n, listed;
+};
+constexpr int HEADS = CAP * 8 / 16;                      // heads that fit where the list will be
+
 template <class E>
 struct Picker {
     Shared &s;
-    const SampleArgs &a;
     const Row &r;
-    RowReader<E> in;
+    const RowReader<E> &in;
     double top;                 // the bin of the row's largest logit
     bool far;
-    double base;                // mass and count in front of the list
-    uint32_t before;
-    int n;                      // tokens in the list
+    int units, group;           // the row in units of a piece a thread; so many of them have a bit
+    int n;                      // tokens that are looked at
 
     __device__ __forceinline__ double through(int j) const { return j < 0 ? 0.0 : s.mass[j]; }
     __device__ __forceinline__ uint32_t counted(int j) const { return j < 0 ? 0u : s.count[j]; }
-    __device__ __forceinline__ double below(float x) const { return top - rint((double)x * r.scale); }
+    __device__ __forceinline__ double below(float x) const { return top - bin_of_logit((double)x, r.scale, far); }
     __device__ __forceinline__ uint64_t weight_units(float x) const
     {
         const double d = (double)x;
-        return units(fma(d, r.scale, -rint(d * r.scale)), far);
+        return far ? 1ull << 35 : units_bits(fma(d, r.scale, -bin_of_logit(d, r.scale, false))) - kExp52;
     }
-    __device__ __forceinline__ double weight(float x) const
+    static __device__ __forceinline__ int some_bin(double b) { return b >= 0.0 && b < (double)BINS ? (int)b : 0; }
+    // All logits of the bins [j0, j1] are in [lo, hi], which is little wider.
+    __device__ __forceinline__ void span(int j0, int j1, float &lo, float &hi) const
     {
-        return (double)weight_units(x) * (1.0 / kUnit) * exp(-0.125 * below(x));
+        const double l = (top - j1 - 0.75) / r.scale, h = (top - j0 + 0.75) / r.scale;
+        lo = (float)(l - fabs(l) * 1e-6);
+        hi = (float)(h + fabs(h) * 1e-6);
+        hi = hi >= kHighest ? INFINITY : hi;             // +inf counts as the highest value
     }
-
-    // All logits of the bins [j0, j1] are in [xlo, xhi], which is little wider.
-    __device__ __forceinline__ void span(int j0, int j1, float &xlo, float &xhi) const
-    {
-        const double lo = (top - j1 - 0.75) / r.scale, hi = (top - j0 + 0.75) / r.scale;
-        xlo = (float)(lo - fabs(lo) * 1e-6);
-        xhi = fminf((float)(hi + fabs(hi) * 1e-6), kHighest);
-    }
-    // f(token, logit) for every token of the bins [j0, j1]
+    // The tokens of the row whose logits are in the plan's ranges.  Few are: a thread marks those of some pieces without a
+    // branch, and takes them one at a time in a short loop, since code that is not in the instruction cache yet costs
+    // more than the tokens.  take(marks, order of mark k): called by whole waves.
     template <class F>
-    __device__ __forceinline__ void each(int j0, int j1, F f) const
+    __device__ __forceinline__ void each(F take) const
     {
-        float xlo, xhi;                                  // a coarse test in 32 bits in front of the exact one
-        span(j0, j1, xlo, xhi);
-        const int pieces = in.pieces();
-        for (int v = threadIdx.x; v < pieces; v += NT2) {
-            float x[E::V];
-            in.read(v, x);
+        const float lo0 = s.plan.lo[0], hi0 = s.plan.hi[0], lo1 = s.plan.lo[1], hi1 = s.plan.hi[1];
+        auto meant = [&](float x) { return (x >= lo0 && x <= hi0) || (x >= lo1 && x <= hi1); };
+        auto order = [](float x, int32_t i) { return order_of(fminf(x, kHighest) + 0.0f, i); };      // -0 counts as 0
+        constexpr int AHEAD = 4;
+        const uint64_t has = s.plan.units;
+        int next = 0;
+        auto unit = [&] {                                // the next one that has such tokens
+            while (next < units && !(has >> (next / group) & 1)) ++next;
+            return next++;
+        };
+#pragma unroll 1
+        for (;;) {
+            int32_t v[AHEAD];
 #pragma unroll
-            for (int i = 0; i < E::V; ++i)
-                if (x[i] >= xlo && x[i] <= xhi) {
-                    const double b = below(x[i]);
-                    if (b >= (double)j0 && b <= (double)j1) f(in.first(v) + i, x[i]);
+            for (int i = 0; i < AHEAD; ++i) v[i] = unit() * NT2 + (int)threadIdx.x;
+            if (v[0] - (int)threadIdx.x >= units * NT2) break;
+            u32x4 raw[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) raw[i] = in.load(v[i]);
+            uint32_t marks = 0;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                float x[E::V];
+                E::unpack(raw[i], x);
+                uint32_t mine = 0;
+#pragma unroll
+                for (int k = 0; k < E::V; ++k) mine |= meant(x[k]) ? 1u << k : 0u;
+                marks |= in.is_whole(v[i]) ? mine << (E::V * i) : 0u;
+            }
+            if (!__any(marks != 0)) continue;
+            take(marks, [&](int k) {
+                const int at = k / (E::V / 4);           // of the 16 words
+                auto one_of = [](bool second, uint32_t a, uint32_t b) { return second ? b : a; };    // (values: an address would put them in memory)
+                auto one_of32 = [](bool second, int32_t a, int32_t b) { return second ? b : a; };
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = one_of(at & 8, one_of(at & 4, raw[0][i], raw[1][i]), one_of(at & 4, raw[2][i], raw[3][i]));
+                const uint32_t word = one_of(at & 2, one_of(at & 1, w[0], w[1]), one_of(at & 1, w[2], w[3]));
+                float x;
+                if constexpr (E::V == 8) x = k & 1 ? bf16_hi(word) : bf16_lo(word);
+                else x = __uint_as_float(word);
+                const int i = k / E::V;
+                const int32_t piece = one_of32(i & 2, one_of32(i & 1, v[0], v[1]), one_of32(i & 1, v[2], v[3]));
+                return order(x, in.first(piece) + k % E::V);
+            });
+        }
+        // the row's ends: elements in front of the first whole piece, and behind the last
+        const bool any = in.whole0 < in.whole1;
+        const int32_t front = any ? in.first(in.whole0) : in.vocab, back = any ? in.first(in.whole1) : in.vocab;
+        const int32_t e = (int)threadIdx.x < front ? (int)threadIdx.x : back + (int)threadIdx.x - front;
+        const float x = in.one(e);
+        const uint32_t marks = meant(x) ? 1u : 0u;
+        if (__any(marks != 0)) take(marks, [&](int) { return order(x, e); });
+    }
+    // f(order, logit, bin) for the tokens of the list, or of the row.
+    template <class F>
+    __device__ __forceinline__ void some(bool listed, F f) const
+    {
+        auto look = [&](uint64_t o) {
+            const float x = logit_of(o);
+            const double b = below(x);
+            if (b >= 0.0 && b < (double)BINS) f(o, x, (int)b);
+        };
+        if (listed) {
+            const int all = (int)s.listed;
+#pragma unroll 1
+            for (int i = threadIdx.x; i < all; i += NT2) look(s.list[i]);
+        } else {
+            each([&](uint32_t marks, auto order) {
+                while (marks) {
+                    look(order(__ffs((int)marks) - 1));
+                    marks &= marks - 1;
                 }
+            });
         }
     }
-    // Sums over the workgroup in front of each thread, and of all.
-    __device__ __forceinline__ double scan(double v, double &all)
+    // The list; false if it does not hold them all.
+    __device__ __forceinline__ bool make_list()
+    {
+        each([&](uint32_t marks, auto order) {
+            // a place for every mark of the wave: the marks of the lanes in front, by the bits of their numbers
+            const int lane = threadIdx.x & 63, mine = __popc(marks);
+            uint32_t at = 0, all = 0;
+#pragma unroll
+            for (int b = 0; b < 6; ++b) {
+                const uint64_t who = __ballot(mine >> b & 1);
+                at += (uint32_t)__popcll(who & ((1ull << lane) - 1)) << b;
+                all += (uint32_t)__popcll(who) << b;
+            }
+            uint32_t first = 0;
+            if (lane == 0) first = atomicAdd(&s.listed, all);
+            at += (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
+            while (marks) {
+                if (at < CAP) s.list[at] = order(__ffs((int)marks) - 1);
+                ++at;
+                marks &= marks - 1;
+            }
+        });
+        __syncthreads();
+        return s.listed <= CAP;
+    }
+    // Sums over the workgroup in front of each thread.
+    __device__ __forceinline__ void scan(double v, uint32_t c, double &front, uint32_t &cfront) const
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         double t = v;
-#pragma unroll
+        uint32_t n = c;
+#pragma unroll 1
         for (int off = 1; off < 64; off <<= 1) {
             const double o = __shfl_up(t, off);
-            if (lane >= off) t += o;
+            const uint32_t on = __shfl_up(n, off);
+            if (lane >= off) {
+                t += o;
+                n += on;
+            }
         }
         __syncthreads();
-        if (lane == 63) s.wsum[wave] = t;
-        const double in_front = __shfl_up(t, 1);
-        __syncthreads();
-        double front = 0.0;
-        all = 0.0;
-#pragma unroll
-        for (int w = 0; w < NT2 / 64; ++w) {
-            if (w == wave) front = all;
-            all += s.wsum[w];
+        if (lane == 63) {
+            s.wsum[wave] = t;
+            s.wcount[wave] = n;
         }
-        return front + (lane ? in_front : 0.0);
+        front = __shfl_up(t, 1);
+        cfront = n - c;
+        if (lane == 0) front = 0.0;
+        __syncthreads();
+#pragma unroll 1
+        for (int w = 0; w < wave; ++w) {
+            front += s.wsum[w];
+            cfront += s.wcount[w];
+        }
     }
-    // The list: the tokens of the bins [j0, j1] from `from` to `to`, at most CAP, sorted, with the running mass from `mass0`.
-    __device__ __forceinline__ void gather(int j0, int j1, uint64_t from, uint64_t to, double mass0, uint32_t count0)
+    // The mass that a token brings: its own, and that of the bins in front of it that none of the few is of.
+    __device__ __forceinline__ double brings(int i) const
     {
+        const float x = logit_of(s.few[i]);
+        const double b = below(x);
+        double w = (double)weight_units(x) * (1.0 / kUnit) * s.factor[some_bin(b)];
+        if (i == 0) {
+            w += s.plan.front >= 0.0 ? s.plan.front : through(some_bin(b) - 1);
+        } else {
+            const double last = below(logit_of(s.few[i - 1]));
+            if (b > last + 1.0) w += through(some_bin(b) - 1) - through(some_bin(last));
+        }
+        return w;
+    }
+    // Puts the few in order.  A token's place is the number of earlier ones, which four threads count; then the first wave has
+    // the mass through each.
+    __device__ __forceinline__ void sort_few()
+    {
+        n = s.n < FEW ? (int)s.n : FEW;
+        const int t = (int)threadIdx.x >> 2, part = (int)threadIdx.x & 3;
+        const uint64_t mine = t < n ? s.few[t] : 0;
+        int at = 0;
+        if ((int)threadIdx.x < 4 * n) {
+#pragma unroll 4
+            for (int i = part; i < n; i += 4) at += s.few[i] < mine ? 1 : 0;
+            at += __shfl_xor(at, 1);
+            at += __shfl_xor(at, 2);
+        }
         __syncthreads();
-        if (threadIdx.x == 0) s.n = 0;
+        if (part == 0 && t < n) s.few[at] = mine;
         __syncthreads();
-        each(j0, j1, [&](int32_t i, float x) {
-            const uint64_t o = order_of(x, i);
-            if (o < from || o > to) return;
+        if (threadIdx.x >= 64) return;
+        double run = 0.0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += 64) {
+            const int i = i0 + (int)threadIdx.x;
+            double w = i < n ? brings(i) : 0.0;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_up(w, off);
+                if ((int)threadIdx.x >= off) w += o;
+            }
+            w += run;
+            if (i < n) s.run[i] = w;
+            run = __shfl(w, 63);
+        }
+        wave_sync();
+    }
+    // The few: the tokens that the plan wants, at most FEW, in order.
+    __device__ __forceinline__ void look(bool listed)
+    {
+        uint64_t from = 0, to = s.plan.to;
+        if (!s.plan.once) narrow(listed, from, to);
+        const bool once = s.plan.once;
+        const int j = s.plan.j0;
+        some(listed, [&](uint64_t o, float, int b) {
+            if (o < from || o > to || !(once ? s.want[b] : b == j)) return;
             const uint32_t at = atomicAdd(&s.n, 1u);
-            if (at < CAP) s.list[at] = o;
+            if (at < FEW) s.few[at] = o;
         });
         __syncthreads();
-        n = s.n < CAP ? (int)s.n : CAP;
-        int all = 64;
-        while (all < n) all <<= 1;
-        for (int i = n + threadIdx.x; i < all; i += NT2) s.list[i] = ~0ull;
-        for (int k = 2; k <= all; k <<= 1)
-            for (int j = k >> 1; j > 0; j >>= 1) {
-                __syncthreads();
-                for (int p = threadIdx.x; p < all / 2; p += NT2) {
-                    const int i = (p & ~(j - 1)) * 2 + (p & (j - 1)), o = i | j;
-                    const uint64_t x = s.list[i], y = s.list[o];
-                    if ((x > y) == ((i & k) == 0)) {
-                        s.list[i] = y;
-                        s.list[o] = x;
-                    }
-                }
-            }
-        __syncthreads();
-        constexpr int PER = CAP / NT2;
-        double w[PER], sum = 0.0, ignored;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int at = threadIdx.x * PER + i;
-            w[i] = at < n ? weight(logit_of(s.list[at])) : 0.0;
-            sum += w[i];
-        }
-        double run = mass0 + scan(sum, ignored);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int at = threadIdx.x * PER + i;
-            run += w[i];
-            if (at < n) s.run[at] = run;
-        }
-        base = mass0;
-        before = count0;
-        __syncthreads();
+        sort_few();
     }
-    // The list of a single bin; where it holds more than CAP tokens, of the part of it that the border is in.
-    __device__ __forceinline__ void open(int j, const Border &b)
+    // While the bin holds more than FEW tokens from `from` to `to`: the part of them that the border is in.
+    __device__ __forceinline__ void narrow(bool listed, uint64_t &from, uint64_t &to)
     {
-        uint64_t from = 0, to = ~0ull;
+        const int j = s.plan.j0;
+        {
+            float lo, hi;
+            span(j, j, lo, hi);
+            from = order_of(fminf(hi, kHighest) + 0.0f, 0);
+            const uint64_t end = order_of(lo + 0.0f, -1);
+            to = end < to ? end : to;
+        }
         double mass0 = through(j - 1);
         uint32_t count0 = counted(j - 1), inside = counted(j) - count0;
-        const double unit = exp(-0.125 * j) * (1.0 / kUnit);
-        if (inside > CAP) {
-            float xlo, xhi;
-            span(j, j, xlo, xhi);
-            from = order_of(xhi + 0.0f, 0);
-            to = order_of(xlo + 0.0f, -1);
-        }
-        while (inside > CAP) {                           // a 1024th of the range each time
+        const double unit = s.factor[j] * (1.0 / kUnit);
+        const Border border = s.plan.border;
+#pragma unroll 1
+        while (inside > FEW) {                           // a 1024th of the range each time
             const int bits = 64 - __clzll((long long)(to - from)), shift = bits > 10 ? bits - 10 : 0;
             __syncthreads();
             s.sub[threadIdx.x] = 0;
             s.subcount[threadIdx.x] = 0;
             if (threadIdx.x == 0) s.n = 0xffffffffu;
             __syncthreads();
-            each(j, j, [&](int32_t i, float x) {
-                const uint64_t o = order_of(x, i);
-                if (o < from || o > to) return;
+            some(listed, [&](uint64_t o, float x, int b) {
+                if (b != j || o < from || o > to) return;
                 const int p = (int)((o - from) >> shift);
                 atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[p]), (unsigned long long)weight_units(x));
                 atomicAdd(&s.subcount[p], 1u);
             });
             __syncthreads();
-            // whole numbers below 2^53 and 2^24: these sums are exact
-            const double u = (double)s.sub[threadIdx.x], c = (double)s.subcount[threadIdx.x];
-            double ignored;
-            const double u0 = scan(u, ignored), c0 = scan(c, ignored);
+            // whole numbers below 2^53 in units: these sums are exact
+            const double u = (double)s.sub[threadIdx.x];
+            const uint32_t c = s.subcount[threadIdx.x];
+            double u0;
+            uint32_t c0;
+            scan(u, c, u0, c0);
             const uint64_t start = from + ((uint64_t)threadIdx.x << shift), end = start + ((1ull << shift) - 1);
             // the first part that reaches the border, else (by rounding) the last that has tokens
-            const bool reaches = b.reached(mass0 + (u0 + u) * unit, count0 + (uint32_t)(c0 + c), end);
-            if (c > 0.0 && reaches) atomicMin(&s.n, (uint32_t)threadIdx.x);
+            const bool reaches = border.reached(mass0 + (u0 + u) * unit, count0 + c0 + c, end);
+            if (c > 0 && reaches) atomicMin(&s.n, (uint32_t)threadIdx.x);
             __syncthreads();
             if (s.n == 0xffffffffu) {
                 __syncthreads();
                 if (threadIdx.x == 0) s.n = 0;
                 __syncthreads();
-                if (c > 0.0) atomicMax(&s.n, (uint32_t)threadIdx.x);
+                if (c > 0) atomicMax(&s.n, (uint32_t)threadIdx.x);
                 __syncthreads();
             }
             const uint32_t at = s.n;
             if (threadIdx.x == at) {
                 s.wsum[0] = u0;
-                s.wsum[1] = c0;
+                s.wcount[0] = c0;
             }
             __syncthreads();
             mass0 += s.wsum[0] * unit;
-            count0 += (uint32_t)s.wsum[1];
+            count0 += s.wcount[0];
             inside = s.subcount[at];
             const uint64_t first = from + ((uint64_t)at << shift), last = first + ((1ull << shift) - 1);
             from = first;
             to = last < to ? last : to;
         }
-        gather(j, j, from, to, mass0, count0);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            s.n = 0;
+            s.plan.front = mass0;
+            s.plan.before = count0;
+        }
+        __syncthreads();
     }
-    // Places in the list.
-    __device__ __forceinline__ double mass_at(int i) const { return i < 0 ? base : s.run[i < n ? i : n - 1]; }
+    // (by one wave) The first of the few with is(i), which holds from some i on; n if none.
+    template <class F>
+    __device__ __forceinline__ int first_that(F is) const
+    {
+        for (int i0 = 0; i0 < n; i0 += 64) {
+            const int i = i0 + ((int)threadIdx.x & 63);
+            const uint64_t at = __ballot(i < n && is(i < n ? i : 0));
+            if (at) return i0 + __ffsll((unsigned long long)at) - 1;
+        }
+        return n;
+    }
+    __device__ __forceinline__ double mass_at(int i) const { return s.run[i < n ? i : n - 1]; }
+};
+
+// The first wave's part: borders, the tokens to look at, and the token.
+template <class E>
+struct Chooser {
+    const Picker<E> &p;
+    float m;                    // the row's largest logit
+    double mass[4];             // through the bins 4 lane ..
+    uint32_t count[4];
+    uint64_t last;              // min-p: the last order that stays
+    int jk, jm, step;
+    double mk, kept;
+    uint32_t ahead;
+    bool once, need_k, need_p, need_m, by_p;
+
     // The bin that a border is in, one that has tokens (the first has: the largest logit).
     __device__ __forceinline__ int bin_of(const Border &b) const
     {
-        int j = first_that(0, BINS - 1, [&](int i) { return b.reached(s.mass[i], s.count[i], 0); });
-        while (j > 0 && s.count[j] == s.count[j - 1]) --j;
+        const int lane = threadIdx.x & 63;
+        int mine = 4 * lane + 3;
+#pragma unroll
+        for (int i = 2; i >= 0; --i) mine = b.reached(mass[i], count[i], 0) ? 4 * lane + i : mine;
+        const uint64_t at = __ballot(b.reached(mass[3], count[3], 0));
+        int j = at ? __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)at) - 1) : BINS - 1;
+        while (j > 0 && p.s.count[j] == p.s.count[j - 1]) --j;
         return j;
+    }
+    __device__ __forceinline__ void start()
+    {
+        Shared &s = p.s;
+        const Row &r = p.r;
+        const int lane = threadIdx.x & 63;
+        double v = 0.0;
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v += (double)s.sub[4 * lane + i] * (1.0 / kUnit) * s.factor[4 * lane + i];
+            c += s.subcount[4 * lane + i];
+            mass[i] = v;
+            count[i] = c;
+        }
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(v, off);
+            const uint32_t oc = __shfl_up(c, off);
+            if (lane >= off) {
+                v += o;
+                c += oc;
+            }
+        }
+        v = __shfl_up(v, 1);
+        c = __shfl_up(c, 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mass[i] += lane ? v : 0.0;
+            count[i] += lane ? c : 0;
+            s.mass[4 * lane + i] = mass[i];
+            s.count[4 * lane + i] = count[i];
+        }
+        wave_sync();
+        // Between which masses each filter's part ends, and the bins that this may be in.  The running mass of
+        // the bins carries rounding errors of 2^-50; `slack` covers them.
+        const double total = s.mass[BINS - 1], slack = 1e-13;
+        last = ~0ull;
+        const bool by_k = r.top_k > 0 && (uint32_t)r.top_k < s.count[BINS - 1];
+        by_p = r.top_p < 1.0f;
+        jk = 0;
+        double klo = total, khi = total, plo = total, phi = total, mlo = total, mhi = total;
+        if (by_k) {
+            jk = bin_of(Border{Border::kCount, (uint32_t)r.top_k, 0.0, 0});
+            klo = p.through(jk - 1);
+            khi = p.through(jk);
+        }
+        int jp0 = 0, jp1 = 0;
+        if (by_p) {
+            jp0 = jp1 = bin_of(Border{Border::kMass, 0, (double)r.top_p * klo * (1.0 - slack), 0});
+            const double most = (double)r.top_p * khi * (1.0 + slack);
+            if (!(s.mass[jp1] >= most)) jp1 = bin_of(Border{Border::kMass, 0, most, 0});
+            plo = p.through(jp0 - 1);
+            phi = p.through(jp1);
+        }
+        jm = 0;
+        bool by_m = false;
+        if (r.min_p > 0.0f) {                            // w >= min-p: the least logit that stays
+            const double least = (double)m + (double)r.T * log((double)r.min_p);
+            float x = (float)least + 0.0f;
+            if ((double)x < least) x = x < 0.0f ? __uint_as_float(__float_as_uint(x) - 1) : __uint_as_float(__float_as_uint(x) + 1);
+            last = order_of(x + 0.0f, -1);
+            const double b = p.top - bin_of_logit(least, r.scale, p.far);
+            by_m = b < (double)BINS;
+            if (by_m) {
+                jm = b > 0.0 ? __builtin_amdgcn_readfirstlane((int)b) : 0;
+                mlo = p.through(jm - 1);
+                mhi = p.through(jm);
+            }
+        }
+        const double hi = fmin(fmin(khi, phi), mhi), lo = fmin(fmin(klo, plo), mlo);
+        need_p = by_p && plo < hi;
+        need_m = by_m && mlo < hi;
+        need_k = by_k && (klo < hi || need_p);
+        const int js0 = bin_of(Border{Border::kPassed, 0, (double)r.u * lo * (1.0 - slack), 0});
+        const double most = (double)r.u * hi * (1.0 + slack);
+        int js1 = js0;
+        if (!(s.mass[js0] > most)) js1 = bin_of(Border{Border::kPassed, 0, most, 0});
+        mk = total;
+        kept = hi;                                       // (a filter that needs no looking keeps at least hi)
+        // One reading of the row for all borders if their bins have not too many tokens, else one for each.
+        uint32_t looked = 0, prev = __shfl_up(count[3], 1);
+        uint64_t units = 0;
+        ahead = 0;
+        if (lane == 0) prev = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 4 * lane + i;
+            const bool want = (j >= js0 && j <= js1) || (need_k && j == jk) || (need_p && j >= jp0 && j <= jp1) || (need_m && j == jm);
+            s.want[j] = want;
+            looked += want ? count[i] - prev : 0;
+            ahead += want && j < jk ? count[i] - prev : 0;   // the list's tokens in front of the bin jk
+            prev = count[i];
+            units |= want ? s.units[j] : 0;
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            looked += __shfl_xor(looked, off);
+            ahead += __shfl_xor(ahead, off);
+            units |= __shfl_xor(units, off);
+        }
+        looked = (uint32_t)__builtin_amdgcn_readfirstlane((int)looked);
+        once = looked <= FEW;
+        step = 0;
+        // the bins' logits in two ranges: the token's, and the filters'
+        int j0 = BINS, j1 = -1;
+        if (need_k) { j0 = jk < j0 ? jk : j0; j1 = jk > j1 ? jk : j1; }
+        if (need_p) { j0 = jp0 < j0 ? jp0 : j0; j1 = jp1 > j1 ? jp1 : j1; }
+        if (need_m) { j0 = jm < j0 ? jm : j0; j1 = jm > j1 ? jm : j1; }
+        if (j0 <= js1 + 1 && j1 >= js0 - 1) {            // they meet
+            j0 = j0 < js0 ? j0 : js0;
+            j1 = j1 > js1 ? j1 : js1;
+            range(0, j0, j1);
+            range(1, BINS, -1);
+        } else {
+            range(0, js0, js1);
+            range(1, j0, j1);
+        }
+        if (lane == 0) {
+            s.plan.once = once;
+            s.plan.listed = !once && looked <= CAP * 2 / 3;      // (the ranges hold some more)
+            s.plan.units = units;
+            s.plan.done = false;
+            s.listed = 0;
+        }
+        if (once) ask(0, Border{Border::kCount, 0, 0.0, 0});
+        else next();
+    }
+    __device__ __forceinline__ void range(int i, int j0, int j1)
+    {
+        float lo = INFINITY, hi = -INFINITY;
+        if (j0 <= j1) p.span(j0, j1, lo, hi);
+        if ((threadIdx.x & 63) == 0) {
+            p.s.plan.lo[i] = lo;
+            p.s.plan.hi[i] = hi;
+        }
+    }
+    __device__ __forceinline__ void ask(int j, Border b)
+    {
+        Shared &s = p.s;
+        if ((threadIdx.x & 63) == 0) {
+            // without top-p, the bins lack some of what min-p drops: it stays out
+            s.plan.border = b;
+            s.plan.to = by_p ? ~0ull : last;
+            s.plan.front = -1.0;
+            s.plan.j0 = j;
+            s.n = 0;
+        }
+    }
+    __device__ __forceinline__ bool needed() const { return step == 0 ? need_k : step == 1 ? need_p : step == 2 ? need_m : true; }
+    // Asks for the tokens of the next step's bin.
+    __device__ __forceinline__ void next()
+    {
+        while (!needed()) ++step;
+        Border b;
+        b.kind = step == 0 ? Border::kCount : step == 1 ? Border::kMass : step == 2 ? Border::kOrder : Border::kPassed;
+        b.count = (uint32_t)p.r.top_k;
+        b.mass = step == 1 ? (double)p.r.top_p * mk : (double)p.r.u * kept;
+        b.order = last;
+        const int j = step == 0 ? jk : step == 2 ? jm : bin_of(b);
+        ask(j, b);
+    }
+    // Takes a step, or all of them, on the list; the token's place in it, or -1 if there are more steps.
+    __device__ __forceinline__ int take()
+    {
+        Shared &s = p.s;
+        for (;; ++step) {
+            if (!needed()) continue;
+            if (step == 0) {
+                // the count-th token: in the list the tokens of the wanted bins in front of its own, and of its own, are before it
+                mk = p.mass_at((int)((uint32_t)p.r.top_k - 1 + (once ? ahead - p.counted(jk - 1) : 0u - s.plan.before)));
+                kept = fmin(kept, mk);
+            } else if (step == 1) {
+                const double want = (double)p.r.top_p * mk;
+                kept = fmin(kept, p.mass_at(p.first_that([&](int i) { return s.run[i] >= want; })));
+            } else if (step == 2) {
+                const int end = p.first_that([&](int i) { return s.few[i] > last; });
+                kept = fmin(kept, fmax(end > 0 ? p.mass_at(end - 1) : 0.0, once ? p.through(jm - 1) : s.plan.front));
+            } else {
+                const double want = (double)p.r.u * kept;
+                const int at = p.first_that([&](int i) { return s.run[i] > want; });
+                return at < p.n ? at : p.n > 0 ? p.n - 1 : 0;
+            }
+            if (!once) {
+                ++step;
+                next();
+                return -1;
+            }
+        }
     }
 };
 
@@ -410,7 +783,7 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
     __shared__ Shared s;
     __shared__ float wmax[NT2 / 64];
     __shared__ int first;
-    const int row = blockIdx.x;
+    const int row = blockIdx.x, lane = threadIdx.x & 63;
     const Row r = settings(a, row);
     if (!r.ok) {
         if (threadIdx.x == 0) {
@@ -421,17 +794,28 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
         return;
     }
     const ChunkHead *heads = static_cast<const ChunkHead *>(a.heads) + (int64_t)row * a.chunks;
+    ChunkHead *near = reinterpret_cast<ChunkHead *>(s.list);
     float m = -INFINITY;
-    for (int c = threadIdx.x; c < a.chunks; c += NT2) m = fmaxf(m, heads[c].max);
+    for (int c = threadIdx.x; c < a.chunks; c += NT2) {
+        const ChunkHead h = heads[c];
+        m = fmaxf(m, h.max);
+        if (c < HEADS) near[c] = h;
+    }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+    if (lane == 0) wmax[threadIdx.x >> 6] = m;
     if (threadIdx.x == 0) first = 0x7fffffff;
-    s.sub[threadIdx.x] = 0;
-    if (threadIdx.x < BINS) s.subcount[threadIdx.x] = 0;
+    if (threadIdx.x < BINS) {
+        s.sub[threadIdx.x] = 0;
+        s.subcount[threadIdx.x] = 0;
+        s.units[threadIdx.x] = 0;
+        s.factor[threadIdx.x] = exp(-0.125 * (int)threadIdx.x);
+    }
     __syncthreads();
+    m = wmax[lane & (NT2 / 64 - 1)];
 #pragma unroll
-    for (int w = 0; w < NT2 / 64; ++w) m = fmaxf(m, wmax[w]);
+    for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    m = __uint_as_float(__builtin_amdgcn_readfirstlane((int)__float_as_uint(m)));
     if (m == -INFINITY || r.T == 0.0f) {                 // nothing to choose from, or nothing to choose
         if (m != -INFINITY) {
             for (int c = threadIdx.x; c < a.chunks; c += NT2)
@@ -444,102 +828,53 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
         }
         return;
     }
-    const double t0 = (double)m * r.scale, top = rint(t0);
+    const bool far = is_far((double)m * r.scale);
+    const double top = bin_of_logit((double)m, r.scale, far);
+    const RowReader<E> in(a, row);
+    const int units = (in.vocab + in.lead + E::V * NT2 - 1) / (E::V * NT2), group = (units + 63) / 64;
     // the chunks' bins, counted from the row's largest logit
     {
         constexpr int PARTS = NT2 / BINS;
         const int bin = threadIdx.x % BINS;
-        uint64_t mass = 0;
+        const uint64_t *bins = a.bins + (int64_t)row * a.chunks * BINS;
+        uint64_t mass = 0, has = 0;
         uint32_t count = 0;
+        const int pieces = a.chunk / E::V;               // of a chunk: 256 to 2048
+#pragma unroll 4
         for (int c = threadIdx.x / BINS; c < a.chunks; c += PARTS) {
-            const ChunkHead h = heads[c];
+            const ChunkHead h = c < HEADS ? near[c] : heads[c];
             const double off = top - h.top;
-            if (h.max == -INFINITY || !(off <= (double)bin)) continue;
-            const uint64_t b = a.bins[((int64_t)row * a.chunks + c) * BINS + bin - (int)off];
+            const bool some = h.max != -INFINITY && off <= (double)bin;
+            const uint64_t b = some ? bins[(int64_t)c * BINS + bin - (int)off] : 0;
             mass += b & kMass;
             count += (uint32_t)(b >> 49);
+            if (b >> 49) has |= 1ull << (c * pieces / NT2 / group) | 1ull << (((c + 1) * pieces - 1) / NT2 / group);
         }
+        if (has) atomicOr(reinterpret_cast<unsigned long long *>(&s.units[bin]), (unsigned long long)has);
         atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[bin]), (unsigned long long)mass);
         atomicAdd(&s.subcount[bin], count);
     }
+    Picker<E> p = {s, r, in, top, far, units, group, 0};
+    Chooser<E> choose = {p, m};
+    const bool chooses = threadIdx.x < 64;
     __syncthreads();
-    Picker<E> p = {s, a, r, RowReader<E>(a, row), top, fabs(t0) > 1125899906842624.0, 0.0, 0, 0};
-    {
-        const bool mine = threadIdx.x < BINS;
-        const double v = mine ? (double)s.sub[threadIdx.x] * (1.0 / kUnit) * exp(-0.125 * (int)threadIdx.x) : 0.0;
-        const double c = mine ? (double)s.subcount[threadIdx.x] : 0.0;
-        double all;
-        const double v0 = p.scan(v, all), c0 = p.scan(c, all);
-        if (mine) {
-            s.mass[threadIdx.x] = v0 + v;
-            s.count[threadIdx.x] = (uint32_t)(c0 + c);
-        }
-    }
+    if (chooses) choose.start();
     __syncthreads();
-    // Between which masses each filter's part ends, and the bins that this may be in.  The running mass of
-    // the bins carries rounding errors of 2^-50; `slack` covers them.
-    const double total = s.mass[BINS - 1], slack = 1e-13;
-    Border k = {Border::kCount, 0.0, (uint32_t)r.top_k, 0}, pm = {Border::kMass, 0.0, 0, 0}, u = {Border::kPassed, 0.0, 0, 0};
-    Border f = {Border::kOrder, 0.0, 0, 0};
-    const bool by_k = r.top_k > 0 && (uint32_t)r.top_k < s.count[BINS - 1], by_p = r.top_p < 1.0f;
-    const int jk = by_k ? p.bin_of(k) : 0;
-    const double klo = by_k ? p.through(jk - 1) : total, khi = by_k ? s.mass[jk] : total;
-    pm.mass = (double)r.top_p * klo * (1.0 - slack);
-    const int jp0 = by_p ? p.bin_of(pm) : 0;
-    pm.mass = (double)r.top_p * khi * (1.0 + slack);
-    const int jp1 = by_p ? p.bin_of(pm) : 0;
-    const double plo = by_p ? p.through(jp0 - 1) : total, phi = by_p ? s.mass[jp1] : total;
-    double jm_ = (double)BINS;
-    if (r.min_p > 0.0f) {                                // w >= min-p: the least logit that stays
-        const double least = (double)m + (double)r.T * log((double)r.min_p);
-        float x = (float)least + 0.0f;
-        if ((double)x < least) x = x < 0.0f ? __uint_as_float(__float_as_uint(x) - 1) : __uint_as_float(__float_as_uint(x) + 1);
-        f.order = order_of(x + 0.0f, -1);
-        jm_ = top - rint(least * r.scale);
-    }
-    const bool by_m = jm_ < (double)BINS;
-    const int jm = by_m && jm_ > 0.0 ? (int)jm_ : 0;
-    const double mlo = by_m ? p.through(jm - 1) : total, mhi = by_m ? s.mass[jm] : total;
-    const double hi = fmin(fmin(khi, phi), mhi), lo = fmin(fmin(klo, plo), mlo);
-    const bool need_p = by_p && plo < hi, need_m = by_m && mlo < hi, need_k = by_k && (klo < hi || need_p);
-    u.mass = (double)r.u * lo * (1.0 - slack);
-    int j0 = p.bin_of(u);
-    u.mass = (double)r.u * hi * (1.0 + slack);
-    int j1 = p.bin_of(u);
-    if (need_k) { j0 = jk < j0 ? jk : j0; j1 = jk > j1 ? jk : j1; }
-    if (need_p) { j0 = jp0 < j0 ? jp0 : j0; j1 = jp1 > j1 ? jp1 : j1; }
-    if (need_m) { j0 = jm < j0 ? jm : j0; j1 = jm > j1 ? jm : j1; }
-    // One reading for all of them if that is not too many tokens, else one for each.
-    const bool once = s.count[j1] - p.counted(j0 - 1) <= CAP;
-    double mk = total, mass = hi;                        // (a filter that needs no looking keeps at least hi)
-    int at = 0;
-#pragma unroll 1
-    for (int step = once ? -1 : 0; step < 4; ++step) {
-        if ((step == 0 && !need_k) || (step == 1 && !need_p) || (step == 2 && !need_m)) continue;
-        if (step == 1) pm.mass = (double)r.top_p * mk;
-        if (step == 3) u.mass = (double)r.u * mass;
-        if (step < 0) {
-            p.gather(j0, j1, 0, ~0ull, p.through(j0 - 1), p.counted(j0 - 1));
-            continue;
+    const bool listed = s.plan.listed && p.make_list();
+    for (;;) {
+        p.look(listed);
+        if (chooses) {
+            const int at = choose.take();
+            if (at >= 0 && lane == 0) {
+                const uint64_t o = s.few[at];
+                a.token[row] = index_of(o);
+                // masses are relative to the centre of the first bin
+                if (a.logprob) a.logprob[row] = (float)((far ? 0.0 : 0.125 * fma((double)logit_of(o), r.scale, -top)) - log(choose.kept));
+                s.plan.done = true;
+            }
         }
-        if (!once) p.open(step == 0 ? jk : step == 1 ? p.bin_of(pm) : step == 2 ? jm : p.bin_of(u), step == 0 ? k : step == 1 ? pm : step == 2 ? f : u);
-        if (step == 0) {
-            mk = p.mass_at((int)(k.count - 1 - p.before));
-            mass = fmin(mass, mk);
-        } else if (step == 1) {
-            mass = fmin(mass, p.mass_at(first_that(0, p.n, [&](int i) { return s.run[i] >= pm.mass; })));
-        } else if (step == 2) {
-            mass = fmin(mass, p.mass_at(first_that(0, p.n, [&](int i) { return s.list[i] > f.order; }) - 1));
-        } else {
-            at = first_that(0, p.n, [&](int i) { return s.run[i] > u.mass; });
-            at = at < p.n ? at : p.n - 1;
-        }
-    }
-    if (threadIdx.x == 0) {
-        const uint64_t o = s.list[at];
-        a.token[row] = index_of(o);
-        // masses are relative to the centre of the first bin
-        if (a.logprob) a.logprob[row] = (float)((p.far ? 0.0 : 0.125 * fma((double)logit_of(o), r.scale, -top)) - log(mass));
+        __syncthreads();
+        if (s.plan.done) return;
     }
 }
 
