@@ -97,10 +97,9 @@ struct RowReader {
     }
     __device__ __forceinline__ int32_t first(int32_t v) const { return v * E::V - lead; }
     __device__ __forceinline__ bool is_whole(int32_t v) const { return v >= whole0 && v < whole1; }
-    // any whole piece for one that is not, so that no load waits for a branch
+    // any whole piece for one that is not, so that no load waits for a branch (there is one)
     __device__ __forceinline__ u32x4 load(int32_t v) const
     {
-        if (whole0 >= whole1) return u32x4{0, 0, 0, 0};
         return load16(base + first(v < whole0 ? whole0 : v < whole1 ? v : whole1 - 1));
     }
     __device__ __forceinline__ float one(int32_t i) const { return i >= 0 && i < vocab ? E::one(base + i) : -INFINITY; }
@@ -129,7 +128,10 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
     const int32_t v0 = c * PIECES * NT1 + (int)threadIdx.x;
     u32x4 raw[PIECES];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) raw[i] = in.load(v0 + i * NT1);
+    for (int i = 0; i < PIECES; ++i) raw[i] = u32x4{0, 0, 0, 0};
+    if (in.whole0 < in.whole1)
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) raw[i] = in.load(v0 + i * NT1);
     float x[N];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) in.unpack(v0 + i * NT1, raw[i], x + i * E::V);
@@ -228,7 +230,7 @@ struct Plan {
     double front;               // mass and count in front of the part (-1: all earlier bins')
     uint32_t before;
     float lo[2], hi[2];         // the wanted tokens' logits are in one of these ranges,
-    uint64_t units;             // and they in these parts of the row
+    int parts;                  // and they in so many parts of the row
     int j0;
     bool once, listed, done;
 };
@@ -240,7 +242,8 @@ struct Shared {
     double factor[BINS];        // exp(-j / 8)
     double mass[BINS];          // the row's mass and count through each bin
     uint32_t count[BINS];
-    uint64_t units[BINS];       // the parts of the row that have tokens of a bin
+    uint64_t has[BINS];         // the parts of the row that have tokens of a bin
+    int32_t part[64];           // the parts that have wanted tokens
     uint8_t want[BINS];
     uint64_t sub[NT2];          // units and counts of the bins, then of a bin's parts
     uint32_t subcount[NT2];
@@ -249,7 +252,6 @@ struct Shared {
     Plan plan;
     uint32_t n, listed;
 };
-constexpr int HEADS = CAP * 8 / 16;                      // heads that fit where the list will be
 
 template <class E>
 struct Picker {
@@ -258,7 +260,7 @@ struct Picker {
     const RowReader<E> &in;
     double top;                 // the bin of the row's largest logit
     bool far;
-    int units, group;           // the row in units of a piece a thread; so many of them have a bit
+    int group;                  // units of a piece a thread in a part of the row
     int n;                      // tokens that are looked at
 
     __device__ __forceinline__ double through(int j) const { return j < 0 ? 0.0 : s.mass[j]; }
@@ -285,24 +287,37 @@ struct Picker {
     __device__ __forceinline__ void each(F take) const
     {
         const float lo0 = s.plan.lo[0], hi0 = s.plan.hi[0], lo1 = s.plan.lo[1], hi1 = s.plan.hi[1];
-        auto meant = [&](float x) { return (x >= lo0 && x <= hi0) || (x >= lo1 && x <= hi1); };
+        // (bits, not && and ||: no branch for each of them)
+        auto meant = [&](float x) { return (uint32_t)(((x >= lo0) & (x <= hi0)) | ((x >= lo1) & (x <= hi1))); };
         auto order = [](float x, int32_t i) { return order_of(fminf(x, kHighest) + 0.0f, i); };      // -0 counts as 0
         constexpr int AHEAD = 4;
-        const uint64_t has = s.plan.units;
-        int next = 0;
-        auto unit = [&] {                                // the next one that has such tokens
-            while (next < units && !(has >> (next / group) & 1)) ++next;
-            return next++;
-        };
-#pragma unroll 1
-        for (;;) {
-            int32_t v[AHEAD];
+        // The parts that have such tokens, a lane each; a part is `group` units of a piece a thread.
+        const int parts = s.plan.parts, part_of = s.part[threadIdx.x & 63];
+        int part = 0, in_part = 0, at[AHEAD];            // the next unit; the units on their way (-1: none)
+        u32x4 coming[AHEAD];
+        auto fetch = [&] {
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) v[i] = unit() * NT2 + (int)threadIdx.x;
-            if (v[0] - (int)threadIdx.x >= units * NT2) break;
+            for (int i = 0; i < AHEAD; ++i) {
+                const int unit = __builtin_amdgcn_readlane(part_of, part < parts ? part : 0) * group + in_part;
+                at[i] = part < parts ? unit : -1;
+                coming[i] = in.load(unit * NT2 + (int)threadIdx.x);
+                in_part = in_part + 1 < group ? in_part + 1 : 0;
+                part += in_part == 0 ? 1 : 0;
+            }
+        };
+        const bool any = in.whole0 < in.whole1;
+        at[0] = -1;
+        if (any && parts > 0) fetch();
+#pragma unroll 1
+        while (at[0] >= 0) {
+            int32_t v[AHEAD];
             u32x4 raw[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) raw[i] = in.load(v[i]);
+            for (int i = 0; i < AHEAD; ++i) {
+                v[i] = at[i] < 0 ? -1 : at[i] * NT2 + (int)threadIdx.x;
+                raw[i] = coming[i];
+            }
+            fetch();
             uint32_t marks = 0;
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
@@ -310,7 +325,7 @@ struct Picker {
                 E::unpack(raw[i], x);
                 uint32_t mine = 0;
 #pragma unroll
-                for (int k = 0; k < E::V; ++k) mine |= meant(x[k]) ? 1u << k : 0u;
+                for (int k = E::V - 1; k >= 0; --k) mine = mine + mine + meant(x[k]);
                 marks |= in.is_whole(v[i]) ? mine << (E::V * i) : 0u;
             }
             if (!__any(marks != 0)) continue;
@@ -331,59 +346,63 @@ struct Picker {
             });
         }
         // the row's ends: elements in front of the first whole piece, and behind the last
-        const bool any = in.whole0 < in.whole1;
         const int32_t front = any ? in.first(in.whole0) : in.vocab, back = any ? in.first(in.whole1) : in.vocab;
         const int32_t e = (int)threadIdx.x < front ? (int)threadIdx.x : back + (int)threadIdx.x - front;
         const float x = in.one(e);
-        const uint32_t marks = meant(x) ? 1u : 0u;
+        const uint32_t marks = meant(x);
         if (__any(marks != 0)) take(marks, [&](int) { return order(x, e); });
     }
-    // f(order, logit, bin) for the tokens of the list, or of the row.
-    template <class F>
-    __device__ __forceinline__ void some(bool listed, F f) const
+    // The passes over the row's meant tokens, or the list of them (one function: its code is read in once):
+    enum Mode { kList, kParts, kFew };
+    // makes the list; the tokens of the plan's bin from `from` to `to` into 1024 parts, 2^shift orders each; those that the plan
+    // wants, into the few.
+    __device__ __forceinline__ void pass(Mode mode, bool listed, uint64_t from, uint64_t to, int shift) const
     {
-        auto look = [&](uint64_t o) {
+        const bool once = s.plan.once;
+        const int j = s.plan.j0, lane = threadIdx.x & 63;
+        auto act = [&](uint64_t o) {
             const float x = logit_of(o);
             const double b = below(x);
-            if (b >= 0.0 && b < (double)BINS) f(o, x, (int)b);
+            if (!(b >= 0.0 && b < (double)BINS) || o < from || o > to || !(once ? s.want[(int)b] : (int)b == j)) return;
+            if (mode == kParts) {
+                const int p = (int)((o - from) >> shift);
+                atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[p]), (unsigned long long)weight_units(x));
+                atomicAdd(&s.subcount[p], 1u);
+            } else {
+                const uint32_t at = atomicAdd(&s.n, 1u);
+                if (at < FEW) s.few[at] = o;
+            }
         };
         if (listed) {
             const int all = (int)s.listed;
 #pragma unroll 1
-            for (int i = threadIdx.x; i < all; i += NT2) look(s.list[i]);
-        } else {
-            each([&](uint32_t marks, auto order) {
-                while (marks) {
-                    look(order(__ffs((int)marks) - 1));
-                    marks &= marks - 1;
-                }
-            });
+            for (int i = threadIdx.x; i < all; i += NT2) act(s.list[i]);
+            return;
         }
-    }
-    // The list; false if it does not hold them all.
-    __device__ __forceinline__ bool make_list()
-    {
         each([&](uint32_t marks, auto order) {
-            // a place for every mark of the wave: the marks of the lanes in front, by the bits of their numbers
-            const int lane = threadIdx.x & 63, mine = __popc(marks);
-            uint32_t at = 0, all = 0;
+            uint32_t at = 0;
+            if (mode == kList) {
+                // a place for every mark of the wave: the marks of the lanes in front, by the bits of their numbers
+                const int mine = __popc(marks);
+                uint32_t all = 0, first = 0;
 #pragma unroll
-            for (int b = 0; b < 6; ++b) {
-                const uint64_t who = __ballot(mine >> b & 1);
-                at += (uint32_t)__popcll(who & ((1ull << lane) - 1)) << b;
-                all += (uint32_t)__popcll(who) << b;
+                for (int b = 0; b < 6; ++b) {
+                    const uint64_t who = __ballot(mine >> b & 1);
+                    at += (uint32_t)__popcll(who & ((1ull << lane) - 1)) << b;
+                    all += (uint32_t)__popcll(who) << b;
+                }
+                if (lane == 0) first = atomicAdd(&s.listed, all);
+                at += (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
             }
-            uint32_t first = 0;
-            if (lane == 0) first = atomicAdd(&s.listed, all);
-            at += (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
+#pragma unroll 1
             while (marks) {
-                if (at < CAP) s.list[at] = order(__ffs((int)marks) - 1);
-                ++at;
+                const uint64_t o = order(__ffs((int)marks) - 1);
                 marks &= marks - 1;
+                if (mode != kList) act(o);
+                else if (at < CAP) s.list[at] = o;
+                ++at;
             }
         });
-        __syncthreads();
-        return s.listed <= CAP;
     }
     // Sums over the workgroup in front of each thread.
     __device__ __forceinline__ void scan(double v, uint32_t c, double &front, uint32_t &cfront) const
@@ -463,89 +482,85 @@ struct Picker {
         }
         wave_sync();
     }
-    // The few: the tokens that the plan wants, at most FEW, in order.
-    __device__ __forceinline__ void look(bool listed)
+    // The few: the tokens that the plan wants, in order.  Of a bin that holds more than FEW, the part that the border is in.
+    __device__ __forceinline__ void look(bool make_list, bool &listed)
     {
-        uint64_t from = 0, to = s.plan.to;
-        if (!s.plan.once) narrow(listed, from, to);
+        const int j = s.plan.j0;
         const bool once = s.plan.once;
-        const int j = s.plan.j0;
-        some(listed, [&](uint64_t o, float, int b) {
-            if (o < from || o > to || !(once ? s.want[b] : b == j)) return;
-            const uint32_t at = atomicAdd(&s.n, 1u);
-            if (at < FEW) s.few[at] = o;
-        });
-        __syncthreads();
-        sort_few();
-    }
-    // While the bin holds more than FEW tokens from `from` to `to`: the part of them that the border is in.
-    __device__ __forceinline__ void narrow(bool listed, uint64_t &from, uint64_t &to)
-    {
-        const int j = s.plan.j0;
-        {
+        uint64_t from = 0, to = s.plan.to;
+        double front = through(j - 1);
+        uint32_t before = counted(j - 1), inside = counted(j) - before;
+        if (once) inside = 0;
+        const bool whole = inside <= FEW;
+        if (!whole) {
             float lo, hi;
             span(j, j, lo, hi);
             from = order_of(fminf(hi, kHighest) + 0.0f, 0);
             const uint64_t end = order_of(lo + 0.0f, -1);
             to = end < to ? end : to;
         }
-        double mass0 = through(j - 1);
-        uint32_t count0 = counted(j - 1), inside = counted(j) - count0;
         const double unit = s.factor[j] * (1.0 / kUnit);
-        const Border border = s.plan.border;
+        Mode mode = make_list ? kList : inside > FEW ? kParts : kFew;
 #pragma unroll 1
-        while (inside > FEW) {                           // a 1024th of the range each time
+        for (;;) {
             const int bits = 64 - __clzll((long long)(to - from)), shift = bits > 10 ? bits - 10 : 0;
-            __syncthreads();
-            s.sub[threadIdx.x] = 0;
-            s.subcount[threadIdx.x] = 0;
-            if (threadIdx.x == 0) s.n = 0xffffffffu;
-            __syncthreads();
-            some(listed, [&](uint64_t o, float x, int b) {
-                if (b != j || o < from || o > to) return;
-                const int p = (int)((o - from) >> shift);
-                atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[p]), (unsigned long long)weight_units(x));
-                atomicAdd(&s.subcount[p], 1u);
-            });
-            __syncthreads();
-            // whole numbers below 2^53 in units: these sums are exact
-            const double u = (double)s.sub[threadIdx.x];
-            const uint32_t c = s.subcount[threadIdx.x];
-            double u0;
-            uint32_t c0;
-            scan(u, c, u0, c0);
-            const uint64_t start = from + ((uint64_t)threadIdx.x << shift), end = start + ((1ull << shift) - 1);
-            // the first part that reaches the border, else (by rounding) the last that has tokens
-            const bool reaches = border.reached(mass0 + (u0 + u) * unit, count0 + c0 + c, end);
-            if (c > 0 && reaches) atomicMin(&s.n, (uint32_t)threadIdx.x);
-            __syncthreads();
-            if (s.n == 0xffffffffu) {
+            if (mode == kParts) {                        // a 1024th of the range each time
                 __syncthreads();
-                if (threadIdx.x == 0) s.n = 0;
-                __syncthreads();
-                if (c > 0) atomicMax(&s.n, (uint32_t)threadIdx.x);
+                s.sub[threadIdx.x] = 0;
+                s.subcount[threadIdx.x] = 0;
+                if (threadIdx.x == 0) s.n = 0xffffffffu;
                 __syncthreads();
             }
-            const uint32_t at = s.n;
-            if (threadIdx.x == at) {
-                s.wsum[0] = u0;
-                s.wcount[0] = c0;
-            }
+            pass(mode, listed, from, to, shift);
             __syncthreads();
-            mass0 += s.wsum[0] * unit;
-            count0 += s.wcount[0];
-            inside = s.subcount[at];
-            const uint64_t first = from + ((uint64_t)at << shift), last = first + ((1ull << shift) - 1);
-            from = first;
-            to = last < to ? last : to;
+            if (mode == kFew) break;
+            if (mode == kList) {
+                listed = s.listed <= CAP;
+            } else {
+                // whole numbers below 2^53 in units: these sums are exact
+                const double u = (double)s.sub[threadIdx.x];
+                const uint32_t c = s.subcount[threadIdx.x];
+                double u0;
+                uint32_t c0;
+                scan(u, c, u0, c0);
+                const uint64_t start = from + ((uint64_t)threadIdx.x << shift), end = start + ((1ull << shift) - 1);
+                // the first part that reaches the border, else (by rounding) the last that has tokens
+                const bool reaches = s.plan.border.reached(front + (u0 + u) * unit, before + c0 + c, end);
+                if (c > 0 && reaches) atomicMin(&s.n, (uint32_t)threadIdx.x);
+                __syncthreads();
+                if (s.n == 0xffffffffu) {
+                    __syncthreads();
+                    if (threadIdx.x == 0) s.n = 0;
+                    __syncthreads();
+                    if (c > 0) atomicMax(&s.n, (uint32_t)threadIdx.x);
+                    __syncthreads();
+                }
+                const uint32_t at = s.n;
+                if (threadIdx.x == at) {
+                    s.wsum[0] = u0;
+                    s.wcount[0] = c0;
+                }
+                __syncthreads();
+                front += s.wsum[0] * unit;
+                before += s.wcount[0];
+                inside = s.subcount[at];
+                const uint64_t first = from + ((uint64_t)at << shift), last = first + ((1ull << shift) - 1);
+                from = first;
+                to = last < to ? last : to;
+                if (inside <= FEW) {
+                    __syncthreads();
+                    if (threadIdx.x == 0) s.n = 0;
+                    __syncthreads();
+                }
+            }
+            mode = inside > FEW ? kParts : kFew;
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            s.n = 0;
-            s.plan.front = mass0;
-            s.plan.before = count0;
+        if (threadIdx.x == 0 && !whole) {
+            s.plan.front = front;
+            s.plan.before = before;
         }
-        __syncthreads();
+        if (threadIdx.x == 0 && whole) s.plan.before = before;
+        sort_few();
     }
     // (by one wave) The first of the few with is(i), which holds from some i on; n if none.
     template <class F>
@@ -566,8 +581,6 @@ template <class E>
 struct Chooser {
     const Picker<E> &p;
     float m;                    // the row's largest logit
-    double mass[4];             // through the bins 4 lane ..
-    uint32_t count[4];
     uint64_t last;              // min-p: the last order that stays
     int jk, jm, step;
     double mk, kept;
@@ -578,10 +591,10 @@ struct Chooser {
     __device__ __forceinline__ int bin_of(const Border &b) const
     {
         const int lane = threadIdx.x & 63;
-        int mine = 4 * lane + 3;
+        int mine = BINS;
 #pragma unroll
-        for (int i = 2; i >= 0; --i) mine = b.reached(mass[i], count[i], 0) ? 4 * lane + i : mine;
-        const uint64_t at = __ballot(b.reached(mass[3], count[3], 0));
+        for (int i = 3; i >= 0; --i) mine = b.reached(p.s.mass[4 * lane + i], p.s.count[4 * lane + i], 0) ? 4 * lane + i : mine;
+        const uint64_t at = __ballot(mine < BINS);
         int j = at ? __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)at) - 1) : BINS - 1;
         while (j > 0 && p.s.count[j] == p.s.count[j - 1]) --j;
         return j;
@@ -591,8 +604,8 @@ struct Chooser {
         Shared &s = p.s;
         const Row &r = p.r;
         const int lane = threadIdx.x & 63;
-        double v = 0.0;
-        uint32_t c = 0;
+        double v = 0.0, mass[4];                         // through the bins 4 lane ..
+        uint32_t c = 0, count[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v += (double)s.sub[4 * lane + i] * (1.0 / kUnit) * s.factor[4 * lane + i];
@@ -667,7 +680,7 @@ struct Chooser {
         kept = hi;                                       // (a filter that needs no looking keeps at least hi)
         // One reading of the row for all borders if their bins have not too many tokens, else one for each.
         uint32_t looked = 0, prev = __shfl_up(count[3], 1);
-        uint64_t units = 0;
+        uint64_t has = 0;
         ahead = 0;
         if (lane == 0) prev = 0;
 #pragma unroll
@@ -678,15 +691,16 @@ struct Chooser {
             looked += want ? count[i] - prev : 0;
             ahead += want && j < jk ? count[i] - prev : 0;   // the list's tokens in front of the bin jk
             prev = count[i];
-            units |= want ? s.units[j] : 0;
+            has |= want ? s.has[j] : 0;
         }
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) {
             looked += __shfl_xor(looked, off);
             ahead += __shfl_xor(ahead, off);
-            units |= __shfl_xor(units, off);
+            has |= __shfl_xor(has, off);
         }
         looked = (uint32_t)__builtin_amdgcn_readfirstlane((int)looked);
+        if (has >> lane & 1) s.part[__popcll(has & ((1ull << lane) - 1))] = lane;
         once = looked <= FEW;
         step = 0;
         // the bins' logits in two ranges: the token's, and the filters'
@@ -706,7 +720,7 @@ struct Chooser {
         if (lane == 0) {
             s.plan.once = once;
             s.plan.listed = !once && looked <= CAP * 2 / 3;      // (the ranges hold some more)
-            s.plan.units = units;
+            s.plan.parts = __popcll(has);
             s.plan.done = false;
             s.listed = 0;
         }
@@ -796,11 +810,13 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
     const ChunkHead *heads = static_cast<const ChunkHead *>(a.heads) + (int64_t)row * a.chunks;
     ChunkHead *near = reinterpret_cast<ChunkHead *>(s.list);
     float m = -INFINITY;
-    for (int c = threadIdx.x; c < a.chunks; c += NT2) {
-        const ChunkHead h = heads[c];
+    if ((int)threadIdx.x < a.chunks) {                   // the first ones stay at hand
+        const ChunkHead h = heads[threadIdx.x];
         m = fmaxf(m, h.max);
-        if (c < HEADS) near[c] = h;
+        near[threadIdx.x] = h;
     }
+#pragma unroll 1
+    for (int c = NT2 + threadIdx.x; c < a.chunks; c += NT2) m = fmaxf(m, heads[c].max);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
     if (lane == 0) wmax[threadIdx.x >> 6] = m;
@@ -808,7 +824,7 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
     if (threadIdx.x < BINS) {
         s.sub[threadIdx.x] = 0;
         s.subcount[threadIdx.x] = 0;
-        s.units[threadIdx.x] = 0;
+        s.has[threadIdx.x] = 0;
         s.factor[threadIdx.x] = exp(-0.125 * (int)threadIdx.x);
     }
     __syncthreads();
@@ -842,7 +858,7 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
         const int pieces = a.chunk / E::V;               // of a chunk: 256 to 2048
 #pragma unroll 4
         for (int c = threadIdx.x / BINS; c < a.chunks; c += PARTS) {
-            const ChunkHead h = c < HEADS ? near[c] : heads[c];
+            const ChunkHead h = c < NT2 ? near[c] : heads[c];
             const double off = top - h.top;
             const bool some = h.max != -INFINITY && off <= (double)bin;
             const uint64_t b = some ? bins[(int64_t)c * BINS + bin - (int)off] : 0;
@@ -850,19 +866,19 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
             count += (uint32_t)(b >> 49);
             if (b >> 49) has |= 1ull << (c * pieces / NT2 / group) | 1ull << (((c + 1) * pieces - 1) / NT2 / group);
         }
-        if (has) atomicOr(reinterpret_cast<unsigned long long *>(&s.units[bin]), (unsigned long long)has);
+        if (has) atomicOr(reinterpret_cast<unsigned long long *>(&s.has[bin]), (unsigned long long)has);
         atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[bin]), (unsigned long long)mass);
         atomicAdd(&s.subcount[bin], count);
     }
-    Picker<E> p = {s, r, in, top, far, units, group, 0};
+    Picker<E> p = {s, r, in, top, far, group, 0};
     Chooser<E> choose = {p, m};
     const bool chooses = threadIdx.x < 64;
     __syncthreads();
     if (chooses) choose.start();
     __syncthreads();
-    const bool listed = s.plan.listed && p.make_list();
-    for (;;) {
-        p.look(listed);
+    bool listed = false;
+    for (bool make = s.plan.listed;; make = false) {
+        p.look(make, listed);
         if (chooses) {
             const int at = choose.take();
             if (at >= 0 && lane == 0) {
