@@ -33,11 +33,11 @@ namespace {
 constexpr int NT = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Which keys a launch is over.  Whole: a sequence's own rows over all of its keys.  Where sequences of a
-// group share their first P tokens two launches share the work: Prefix takes all rows of a group over the
-// keys [0, P), read through the block table of its first sequence, Own a sequence's rows over the keys
-// from P on.  Both leave their share to the join.
-enum Side { kWhole, kOwn, kPrefix };
+// Which keys a launch is over.  kWhole: a sequence's own rows over all of its keys.  kShared: sequences of a group
+// share their first P tokens, and a block is of one of two sides: Prefix takes the rows of a whole group over the keys [0,
+// P), read through the block table of its first sequence, Own a sequence's rows over the keys from P on.  Both leave their
+// share to the join.
+enum Side { kWhole, kShared };
 
 // A block's rows: rows [m0, m0 + count) of sequence n, row m = (token i, head i_h); of a group, from
 // the first token of its first sequence n on.
@@ -45,8 +45,23 @@ struct Rows {
     int n, G;
     int32_t beg, kv, pos0;      // first token, cached tokens (Prefix: P), position of token 0
     int32_t m0, count;
-    int32_t from, behind;       // Own: P; Prefix: the sequence behind the group's last
+    // kShared
+    bool prefix;                // the side
+    int32_t from, behind;       // Own: P; Prefix: 0, the sequence behind the group's last
+    int32_t splits, split_keys, part;      // of the side; its first part
+    uint32_t block;             // the block's number in it
 };
+// The side of a block, and its number there: the prefixes' come first.
+template <Side S>
+__device__ __forceinline__ void find_side(const AttnArgs &a, Rows &r)
+{
+    r.block = blockIdx.x;
+    r.prefix = S == kShared && blockIdx.x < a.prefix_blocks;
+    r.splits = S == kShared && r.prefix ? a.prefix_splits : a.splits;
+    r.split_keys = S == kShared && r.prefix ? a.prefix_keys : a.split_keys;
+    r.part = S == kShared && !r.prefix ? a.prefix_splits : 0;
+    if (S == kShared && !r.prefix) r.block -= a.prefix_blocks;
+}
 __device__ __forceinline__ bool prefix_ok(const AttnArgs &a, int32_t P)
 {
     return kv_ok(P, a.max_prefix, a.page_size, a.max_pages);
@@ -107,7 +122,8 @@ template <Side S>
 __device__ __forceinline__ bool find_rows(const AttnArgs &a, int64_t tile, int rows, Rows &r)
 {
     r.G = a.h_q / a.h_kv;
-    if constexpr (S == kPrefix) return find_group(a, tile, rows, r);
+    if constexpr (S == kShared)
+        if (r.prefix) return find_group(a, tile, rows, r);
     r.from = 0;
     r.n = tile_sequence(a.cu, a.n_seqs, tile, r.G, rows);
     const int32_t b = a.cu[r.n], e = a.cu[r.n + 1];
@@ -118,7 +134,7 @@ __device__ __forceinline__ bool find_rows(const AttnArgs &a, int64_t tile, int r
         if (threadIdx.x == 0) set_status(a.status);
         return false;
     }
-    if constexpr (S == kOwn) {
+    if constexpr (S == kShared) {
         if (!find_prefix(a, r.n, r.kv, r.from)) {
             if (threadIdx.x == 0) set_status(a.status);
             return false;
@@ -147,16 +163,16 @@ __device__ __forceinline__ int32_t prefix_limit(const AttnArgs &a, const Rows &r
     const int64_t limit = (int64_t)a.kv_len[lo] - a.cu[lo + 1] + t + 1;
     return limit < 0 ? 0 : limit < r.kv ? (int32_t)limit : r.kv;
 }
-// The limits of NB tiles of 16 rows, for the row l % 16 of each, and the least of them (rows past the end
+// The keys that NB tiles of 16 rows see, for the row l % 16 of each, and the least of them (rows past the end
 // count as the last one).
 template <int NB>
-__device__ __forceinline__ int32_t prefix_limits(const AttnArgs &a, const Rows &r, int first, int lane, int32_t (&lim)[NB])
+__device__ __forceinline__ int32_t shared_limits(const AttnArgs &a, const Rows &r, int first, int lane, int32_t (&lim)[NB])
 {
-    int32_t least = r.kv;
+    int32_t least = 0x7fffffff;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const int m = first + 16 * b + (lane & 15);
-        lim[b] = prefix_limit(a, r, r.m0 + (m < r.count ? m : r.count - 1));
+        const int m = first + 16 * b + (lane & 15), mm = r.m0 + (m < r.count ? m : r.count - 1);
+        lim[b] = r.prefix ? prefix_limit(a, r, mm) : row_limit(r, mm);
         least = lim[b] < least ? lim[b] : least;
     }
 #pragma unroll
@@ -311,7 +327,7 @@ __device__ __forceinline__ void store_share(const AttnArgs &a, const Rows &r, in
         if (a.lse && d4 == 0) a.lse[t * a.h_q + h] = l > 0.0f ? mx * kLn2 + logf(l) : -INFINITY;
         return;
     }
-    const int64_t at = ((int64_t)(S == kWhole ? split : a.part_first + split) * a.total + t) * a.h_q + h;
+    const int64_t at = ((int64_t)(S == kWhole ? split : r.part + split) * a.total + t) * a.h_q + h;
     *reinterpret_cast<f32x4 *>(a.part_o + at * D + d4) = o;
     if (d4 == 0) *reinterpret_cast<f32x2 *>(a.part_ml + at * 2) = f32x2{mx, l};
 }
@@ -414,17 +430,18 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
-    const int hk = blockIdx.x % a.h_kv;
-    const int64_t tile = blockIdx.x / a.h_kv / a.splits;
+    Rows r;
+    find_side<S>(a, r);
+    const int hk = r.block % a.h_kv;
+    const int64_t tile = r.block / a.h_kv / r.splits;
     // turned by the tile's number: a multiple of 8 blocks for each would give all the first splits, which
     // no context is too short for, to the same XCD
-    const int split = (int)((blockIdx.x / a.h_kv + tile) % a.splits);
-    Rows r;
+    const int split = (int)((r.block / a.h_kv + tile) % r.splits);
     if (!find_rows<S>(a, tile, ROWS, r)) return;
-    const int32_t most = S == kPrefix ? r.kv : row_limit(r, r.m0 + r.count - 1);   // keys that the tile's last row sees
-    const int32_t k_beg = (S == kOwn ? r.from : 0) + split * a.split_keys;
-    if ((S != kWhole || split > 0) && k_beg >= most) return;      // nothing here for any row
-    const int32_t k_end = most < k_beg + a.split_keys ? most : k_beg + a.split_keys;
+    const int32_t most = S == kShared && r.prefix ? r.kv : row_limit(r, r.m0 + r.count - 1);   // keys that the tile's last row sees
+    const int32_t k_beg = (S == kShared ? r.from : 0) + split * r.split_keys;
+    if ((S == kShared || split > 0) && k_beg >= most) return;     // nothing here for any row
+    const int32_t k_end = most < k_beg + r.split_keys ? most : k_beg + r.split_keys;
     const int32_t *table = a.table + (int64_t)r.n * a.max_pages;
     const char *kc = reinterpret_cast<const char *>(static_cast<const T *>(a.kc) + hk * a.head_stride);
     const char *vc = reinterpret_cast<const char *>(static_cast<const T *>(a.vc) + hk * a.head_stride);
@@ -471,9 +488,9 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
         wait_loads<(2 * NI < 63 ? 2 * NI : 63)>();       // what is in registers is here
     }
     int32_t lim[NB], least;
-    if constexpr (S == kPrefix) least = prefix_limits<NB>(a, r, 0, lane, lim);
+    if constexpr (S == kShared) least = shared_limits<NB>(a, r, 0, lane, lim);
     else least = row_limit(r, r.m0);
-    auto limit = [&](int b) { return S == kPrefix ? lim[b] : row_limit(r, r.m0 + 16 * b + col); };
+    auto limit = [&](int b) { return S == kShared ? lim[b] : row_limit(r, r.m0 + 16 * b + col); };
     const float scale = score_scale(a);
     Soft<NB> sf;
     f32x4 o[NB][D / 16];
@@ -574,17 +591,18 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && threadIdx.x < 64) check_cu(a.cu, a.n_seqs, a.total, a.status);
-    const int hk = blockIdx.x % a.h_kv;
-    const int64_t tile = blockIdx.x / a.h_kv / a.splits;
     Rows r;
+    find_side<S>(a, r);
+    const int hk = r.block % a.h_kv;
+    const int64_t tile = r.block / a.h_kv / r.splits;
     if (!find_rows<S>(a, tile, ROWS, r)) return;
     // turned as above: by the sequence's number in bf16, so that the tiles of a sequence keep a split's keys
     // to one XCD; by the tile's in fp32, where only the even spread counts
-    const int split = (int)((blockIdx.x / a.h_kv + (M::V == 8 ? r.n : tile)) % a.splits);
-    const int32_t most = S == kPrefix ? r.kv : row_limit(r, r.m0 + r.count - 1);
-    const int32_t k_beg = (S == kOwn ? r.from : 0) + split * a.split_keys;
-    if ((S != kWhole || split > 0) && k_beg >= most) return;
-    const int32_t k_end = most < k_beg + a.split_keys ? most : k_beg + a.split_keys;
+    const int split = (int)((r.block / a.h_kv + (M::V == 8 ? r.n : tile)) % r.splits);
+    const int32_t most = S == kShared && r.prefix ? r.kv : row_limit(r, r.m0 + r.count - 1);
+    const int32_t k_beg = (S == kShared ? r.from : 0) + split * r.split_keys;
+    if ((S == kShared || split > 0) && k_beg >= most) return;
+    const int32_t k_end = most < k_beg + r.split_keys ? most : k_beg + r.split_keys;
     const int32_t *table = a.table + (int64_t)r.n * a.max_pages;
     const char *kc = reinterpret_cast<const char *>(static_cast<const T *>(a.kc) + hk * a.head_stride);
     const char *vc = reinterpret_cast<const char *>(static_cast<const T *>(a.vc) + hk * a.head_stride);
@@ -594,9 +612,9 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
     Frag q[NB][D / 32];
     load_q<M, D, NB>(a, r, hk, first, lane, q);
     int32_t lim[NB], least;
-    if constexpr (S == kPrefix) least = prefix_limits<NB>(a, r, first, lane, lim);
+    if constexpr (S == kShared) least = shared_limits<NB>(a, r, first, lane, lim);
     else least = row_limit(r, r.m0 + first);
-    auto limit = [&](int b) { return S == kPrefix ? lim[b] : row_limit(r, r.m0 + first + 16 * b + (int)here(col)); };
+    auto limit = [&](int b) { return S == kShared ? lim[b] : row_limit(r, r.m0 + first + 16 * b + (int)here(col)); };
     const float scale = score_scale(a);
     Soft<NB> sf;
     f32x4 o[NB][D / 16];
@@ -727,7 +745,7 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
     const int32_t kv = a.kv_len[n];
     if (!kv_ok(kv, a.max_kv, a.page_size, a.max_pages)) return;
     const int32_t limit = kv - (e - (int32_t)t) + 1;
-    // the parts that the row's keys are in: with a prefix its splits, then the row's own from part_first on
+    // the parts that the row's keys are in: with a prefix its splits, then the row's own behind them
     int act, pre = 0;
     if constexpr (SHARED) {
         int32_t P;
@@ -738,7 +756,7 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
     } else {
         act = limit > 0 ? (limit + a.split_keys - 1) / a.split_keys : 1;
     }
-    auto part_of = [&](int s) { return SHARED && s >= pre ? a.part_first + s - pre : s; };
+    auto part_of = [&](int s) { return SHARED && s >= pre ? a.prefix_splits + s - pre : s; };
     const int64_t step = a.total * a.h_q, row = t * a.h_q + (h < a.h_q ? h : a.h_q - 1);
     const f32x2 *ml = reinterpret_cast<const f32x2 *>(a.part_ml) + row;
     float mx = -INFINITY;

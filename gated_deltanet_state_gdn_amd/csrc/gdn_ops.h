@@ -83,8 +83,8 @@ struct AttnArgs {
     // shared prefixes: cu_groups [n_groups + 1], prefix_len [n_groups]
     const int32_t *groups, *prefix_len;
     int32_t n_groups, max_prefix, max_own;
-    int32_t part_first;         // the launch's first part; in the join, the first part of the own keys
-    int32_t prefix_keys;        // the join: keys of a prefix's split
+    uint32_t prefix_blocks;     // of this launch
+    int32_t prefix_splits, prefix_keys;    // of a prefix; splits and split_keys are the own keys' then
 };
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, int bf16, int d, hipStream_t stream);
 hipError_t launch_shared_attn(const AttnArgs &a, const SharedPlan &p, int bf16, int d, hipStream_t stream);

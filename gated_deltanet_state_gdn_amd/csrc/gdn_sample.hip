@@ -230,6 +230,7 @@ struct Plan {
     double front;               // mass and count in front of the part (-1: all earlier bins')
     uint32_t before;
     float lo[2], hi[2];         // the wanted tokens' logits are in one of these ranges,
+    int ranges;                 // (0: the first, to the highest; 1: the first; 2: both)
     int parts;                  // and they in so many parts of the row
     int j0;
     bool once, listed, done;
@@ -281,76 +282,66 @@ struct Picker {
         hi = hi >= kHighest ? INFINITY : hi;             // +inf counts as the highest value
     }
     // The tokens of the row whose logits are in the plan's ranges.  Few are: a thread marks those of some pieces without a
-    // branch, and takes them one at a time in a short loop, since code that is not in the instruction cache yet costs
-    // more than the tokens.  take(marks, order of mark k): called by whole waves.
+    // branch, and takes them one at a time in a short loop, which reads them again: a workgroup's waves are bound by the
+    // instructions here, and code that is not in the instruction cache yet costs more than the tokens.
+    // take(marks, order of mark k): called by whole waves.
     template <class F>
     __device__ __forceinline__ void each(F take) const
     {
         const float lo0 = s.plan.lo[0], hi0 = s.plan.hi[0], lo1 = s.plan.lo[1], hi1 = s.plan.hi[1];
+        const int ranges = __builtin_amdgcn_readfirstlane(s.plan.ranges);
         // (bits, not && and ||: no branch for each of them)
         auto meant = [&](float x) { return (uint32_t)(((x >= lo0) & (x <= hi0)) | ((x >= lo1) & (x <= hi1))); };
-        auto order = [](float x, int32_t i) { return order_of(fminf(x, kHighest) + 0.0f, i); };      // -0 counts as 0
-        constexpr int AHEAD = 4;
+        auto order = [&](int32_t i) { return order_of(fminf(in.one(i), kHighest) + 0.0f, i); };       // -0 counts as 0
         // The parts that have such tokens, a lane each; a part is `group` units of a piece a thread.
+        constexpr int AHEAD = 32 / E::V;
         const int parts = s.plan.parts, part_of = s.part[threadIdx.x & 63];
-        int part = 0, in_part = 0, at[AHEAD];            // the next unit; the units on their way (-1: none)
-        u32x4 coming[AHEAD];
-        auto fetch = [&] {
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int unit = __builtin_amdgcn_readlane(part_of, part < parts ? part : 0) * group + in_part;
-                at[i] = part < parts ? unit : -1;
-                coming[i] = in.load(unit * NT2 + (int)threadIdx.x);
-                in_part = in_part + 1 < group ? in_part + 1 : 0;
-                part += in_part == 0 ? 1 : 0;
-            }
-        };
-        const bool any = in.whole0 < in.whole1;
-        at[0] = -1;
-        if (any && parts > 0) fetch();
+        const char *from = reinterpret_cast<const char *>(in.base - in.lead);
+        int part = in.whole0 < in.whole1 ? 0 : parts, in_part = 0;
 #pragma unroll 1
-        while (at[0] >= 0) {
-            int32_t v[AHEAD];
+        while (part < parts) {
+            int32_t at[AHEAD];                           // the pieces of these units; -1: none
             u32x4 raw[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
-                v[i] = at[i] < 0 ? -1 : at[i] * NT2 + (int)threadIdx.x;
-                raw[i] = coming[i];
+                const int unit = __builtin_amdgcn_readlane(part_of, part < parts ? part : 0) * group + in_part;
+                const int32_t v = unit * NT2 + (int)threadIdx.x, last = in.whole1 - 1;
+                raw[i] = load16(from + (uint32_t)(v < in.whole0 ? in.whole0 : v < last ? v : last) * 16u);
+                at[i] = part < parts ? v : -1;
+                in_part = in_part + 1 < group ? in_part + 1 : 0;
+                part += in_part == 0 ? 1 : 0;
             }
-            fetch();
-            uint32_t marks = 0;
+            uint32_t marks = 0, whole = 0;
+            auto mark = [&](auto test) {
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                float x[E::V];
-                E::unpack(raw[i], x);
-                uint32_t mine = 0;
+                for (int i = AHEAD - 1; i >= 0; --i) {
+                    float x[E::V];
+                    E::unpack(raw[i], x);
 #pragma unroll
-                for (int k = E::V - 1; k >= 0; --k) mine = mine + mine + meant(x[k]);
-                marks |= in.is_whole(v[i]) ? mine << (E::V * i) : 0u;
-            }
+                    for (int k = E::V - 1; k >= 0; --k) marks = marks + marks + test(x[k]);
+                }
+            };
+            if (ranges == 0) mark([&](float x) { return (uint32_t)(x >= lo0); });
+            else if (ranges == 1) mark([&](float x) { return (uint32_t)((x >= lo0) & (x <= hi0)); });
+            else mark(meant);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) whole |= in.is_whole(at[i]) ? ((1u << E::V) - 1) << (E::V * i) : 0u;
+            marks &= whole;
             if (!__any(marks != 0)) continue;
             take(marks, [&](int k) {
-                const int at = k / (E::V / 4);           // of the 16 words
-                auto one_of = [](bool second, uint32_t a, uint32_t b) { return second ? b : a; };    // (values: an address would put them in memory)
-                auto one_of32 = [](bool second, int32_t a, int32_t b) { return second ? b : a; };
-                uint32_t w[4];
+                auto later = [](bool is, int32_t a, int32_t b) { return is ? b : a; };       // (values: addresses would put them in memory)
+                int32_t v = at[0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = one_of(at & 8, one_of(at & 4, raw[0][i], raw[1][i]), one_of(at & 4, raw[2][i], raw[3][i]));
-                const uint32_t word = one_of(at & 2, one_of(at & 1, w[0], w[1]), one_of(at & 1, w[2], w[3]));
-                float x;
-                if constexpr (E::V == 8) x = k & 1 ? bf16_hi(word) : bf16_lo(word);
-                else x = __uint_as_float(word);
-                const int i = k / E::V;
-                const int32_t piece = one_of32(i & 2, one_of32(i & 1, v[0], v[1]), one_of32(i & 1, v[2], v[3]));
-                return order(x, in.first(piece) + k % E::V);
+                for (int i = 1; i < AHEAD; ++i) v = later(k >= i * E::V, v, at[i]);
+                return order(in.first(v) + k % E::V);
             });
         }
         // the row's ends: elements in front of the first whole piece, and behind the last
+        const bool any = in.whole0 < in.whole1;
         const int32_t front = any ? in.first(in.whole0) : in.vocab, back = any ? in.first(in.whole1) : in.vocab;
         const int32_t e = (int)threadIdx.x < front ? (int)threadIdx.x : back + (int)threadIdx.x - front;
-        const float x = in.one(e);
-        const uint32_t marks = meant(x);
-        if (__any(marks != 0)) take(marks, [&](int) { return order(x, e); });
+        const uint32_t marks = meant(in.one(e));
+        if (__any(marks != 0)) take(marks, [&](int) { return order(e); });
     }
     // The passes over the row's meant tokens, or the list of them (one function: its code is read in once):
     enum Mode { kList, kParts, kFew };
@@ -708,19 +699,17 @@ struct Chooser {
         if (need_k) { j0 = jk < j0 ? jk : j0; j1 = jk > j1 ? jk : j1; }
         if (need_p) { j0 = jp0 < j0 ? jp0 : j0; j1 = jp1 > j1 ? jp1 : j1; }
         if (need_m) { j0 = jm < j0 ? jm : j0; j1 = jm > j1 ? jm : j1; }
-        if (j0 <= js1 + 1 && j1 >= js0 - 1) {            // they meet
-            j0 = j0 < js0 ? j0 : js0;
-            j1 = j1 > js1 ? j1 : js1;
-            range(0, j0, j1);
-            range(1, BINS, -1);
-        } else {
-            range(0, js0, js1);
-            range(1, j0, j1);
-        }
+        const int top0 = j0 < js0 ? j0 : js0, last1 = j1 > js1 ? j1 : js1;
+        // all of the first bins, if these are not too many; one range where the two meet
+        const bool from_top = (int)s.count[last1] <= (once ? 4 * FEW : CAP * 2 / 3);
+        const bool meet = from_top || j1 < 0 || (j0 <= js1 + 1 && j1 >= js0 - 1);
+        range(0, from_top ? 0 : meet ? top0 : js0, meet ? last1 : js1);
+        range(1, meet ? BINS : j0, meet ? -1 : j1);
         if (lane == 0) {
             s.plan.once = once;
-            s.plan.listed = !once && looked <= CAP * 2 / 3;      // (the ranges hold some more)
+            s.plan.listed = !once && looked <= CAP * 2 / 3;      // (the ranges hold more)
             s.plan.parts = __popcll(has);
+            s.plan.ranges = !meet ? 2 : from_top || top0 == 0 ? 0 : 1;
             s.plan.done = false;
             s.listed = 0;
         }

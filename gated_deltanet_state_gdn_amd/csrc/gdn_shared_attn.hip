@@ -14,51 +14,52 @@
 namespace gdn {
 namespace {
 
-template <class M, int D, int WAVES, Side S>
+template <class M, int D, int WAVES>
 hipError_t decode_n(const AttnArgs &a, const AttnPlan &p, int64_t blocks, hipStream_t stream)
 {
-    if (p.rows == 16) return start(decode_kernel<M, D, 1, WAVES, S>, blocks, a, stream, 64 * WAVES);
-    if constexpr (M::V == 8 && D != 128) return start(decode_kernel<M, D, 2, WAVES, S>, blocks, a, stream, 64 * WAVES);
+    if (p.rows == 16) return start(decode_kernel<M, D, 1, WAVES, kShared>, blocks, a, stream, 64 * WAVES);
+    if constexpr (M::V == 8 && D != 128) return start(decode_kernel<M, D, 2, WAVES, kShared>, blocks, a, stream, 64 * WAVES);
     return hipErrorNotSupported;                         // the plan has no such rows
 }
 
-template <class M, int D, Side S>
-hipError_t side(AttnArgs a, const AttnPlan &p, int32_t units, int32_t part_first, hipStream_t stream)
+// One launch of so many blocks of prefixes and of own keys, in a plan's form.
+template <class M, int D>
+hipError_t sides(AttnArgs a, const AttnPlan &p, int64_t prefix, int64_t own, hipStream_t stream)
 {
-    a.splits = p.splits;
-    a.split_keys = p.split_keys;
-    a.part_first = part_first;
-    const int64_t blocks = (a.total * (a.h_q / a.h_kv) / p.rows + units) * a.splits * a.h_kv;
+    const int64_t blocks = prefix + own;
+    a.prefix_blocks = (uint32_t)prefix;
     if (p.decode) {
         constexpr int WAVES = decode_waves(Tile<M, D>::RB);
-        if (p.waves == WAVES) return decode_n<M, D, WAVES, S>(a, p, blocks, stream);
-        if constexpr (decode_wide(Tile<M, D>::RB)) return decode_n<M, D, 2 * WAVES, S>(a, p, blocks, stream);
+        if (p.waves == WAVES) return decode_n<M, D, WAVES>(a, p, blocks, stream);
+        if constexpr (decode_wide(Tile<M, D>::RB)) return decode_n<M, D, 2 * WAVES>(a, p, blocks, stream);
         return hipErrorNotSupported;                     // the plan has no such waves
     }
-    if constexpr (M::V == 4) return start(prefill_kernel<M, D, 1, 4, 32, S>, blocks, a, stream, 256);
-    else if (p.rows == 256) return start(prefill_kernel<M, D, 2, 8, 64, S>, blocks, a, stream, 512);
-    else return start(prefill_kernel<M, D, 2, 4, 64, S>, blocks, a, stream, 256);
+    if constexpr (M::V == 4) return start(prefill_kernel<M, D, 1, 4, 32, kShared>, blocks, a, stream, 256);
+    else if (p.rows == 256) return start(prefill_kernel<M, D, 2, 8, 64, kShared>, blocks, a, stream, 512);
+    else return start(prefill_kernel<M, D, 2, 4, 64, kShared>, blocks, a, stream, 256);
 }
 
 template <class M, int D>
 hipError_t shared_d(AttnArgs a, const SharedPlan &p, hipStream_t stream)
 {
     constexpr int R = NT / (D / 4);                      // rows of a join's workgroup without slices
+    a.splits = p.own.splits;
+    a.split_keys = p.own.split_keys;
+    a.prefix_splits = p.prefix.splits;
+    a.prefix_keys = p.prefix.split_keys;
     const int splits = p.prefix.splits + p.own.splits;
     const bool sliced = splits > 8 || (splits > 2 && a.total * a.h_q <= 4096);
-    const int64_t joins = a.total * (sliced ? a.h_q : (a.h_q + R - 1) / R);
-    const int64_t G = a.h_q / a.h_kv;
-    if (!grid_ok(joins, NT)) return hipErrorInvalidConfiguration;
-    if (p.prefix.splits > 0 && !grid_ok((a.total * G / p.prefix.rows + a.n_groups) * p.prefix.splits * a.h_kv, 512)) return hipErrorInvalidConfiguration;
-    if (p.own.splits > 0 && !grid_ok((a.total * G / p.own.rows + a.n_seqs) * p.own.splits * a.h_kv, 512)) return hipErrorInvalidConfiguration;
+    const int64_t G = a.h_q / a.h_kv, joins = a.total * (sliced ? a.h_q : (a.h_q + R - 1) / R);
+    const int64_t prefix = (a.total * G / p.prefix.rows + a.n_groups) * p.prefix.splits * a.h_kv;
+    const int64_t own = (a.total * G / p.own.rows + a.n_seqs) * p.own.splits * a.h_kv;
+    if (!grid_ok(joins, NT) || !grid_ok(prefix + own + 1, 512)) return hipErrorInvalidConfiguration;
+    // one launch where both sides take the same form
+    const bool same = p.prefix.decode == p.own.decode && p.prefix.rows == p.own.rows && (!p.own.decode || p.prefix.waves == p.own.waves);
     hipError_t e = hipSuccess;
-    if (p.prefix.splits > 0) e = side<M, D, kPrefix>(a, p.prefix, a.n_groups, 0, stream);
-    if (e == hipSuccess && p.own.splits > 0) e = side<M, D, kOwn>(a, p.own, a.n_seqs, p.prefix.splits, stream);
+    if (same && prefix + own > 0) e = sides<M, D>(a, p.own, prefix, own, stream);
+    if (!same && prefix > 0) e = sides<M, D>(a, p.prefix, prefix, 0, stream);
+    if (!same && own > 0 && e == hipSuccess) e = sides<M, D>(a, p.own, 0, own, stream);
     if (e != hipSuccess) return e;
-    a.splits = splits;
-    a.split_keys = p.own.split_keys;
-    a.prefix_keys = p.prefix.split_keys;
-    a.part_first = p.prefix.splits;
     if (sliced) return start(join_kernel<M, D, R, true>, joins, a, stream, NT);
     return start(join_kernel<M, D, 1, true>, joins, a, stream, NT);
 }
