@@ -184,14 +184,96 @@ inline AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_
 struct SharedPlan {
     AttnPlan prefix, own;       // no splits: the side has no keys
 };
+
+// The form of few rows for one side of a call whose parts are joined in any case: the keys of a split that take the
+// least time, in microseconds.  `units` are groups or sequences, which have all their rows in as many tiles.
+// As short_splits, fitted with it: rounds of workgroups and their tiles; the reads from memory; and, where several
+// tiles of rows read the same keys, theirs from the caches.  256 rows on each of 2 cache heads of 128, bf16, 12000
+// keys, up to 300 own ones: 29.5 us in splits of 1024, 35.2 of 512, 41.4 of 256; 64 rows: 21.8, 19.6, 17.1.
+inline double few_rows_side(int64_t total, int64_t units, int32_t h_q, int32_t h_kv, int32_t d, int32_t most, int bf16, int32_t rows,
+                            int32_t waves, bool shared, int32_t &keys)
+{
+    const int row = d * (bf16 ? 2 : 4);
+    const int64_t G = h_q / h_kv, filled = (total * G + rows - 1) / rows, tiles = (filled > units ? filled : units) * h_kv;
+    const int64_t places = 192 * (waves * 64 * row <= 80 * 1024 ? 2 : 1);
+    const double tile = (bf16 ? 0.3 + 0.006 * d : 0.6 + 0.018 * d) * (waves == 8 ? 1.5 : 1.0) * (rows == 32 ? 1.3 : 1.0);
+    const double reads = (double)units * h_kv * most * row * (shared ? 2 : 1) / 5e6;           // own keys: half of the longest
+    const double caches = shared ? (double)tiles * most * row * 2 / 14e6 : 0.0;
+    const int64_t all = most > 0 ? ((int64_t)most + 32 * waves - 1) / (32 * waves) : 1;        // tiles of a wave
+    int64_t best = all;
+    double least = 0.0;
+    for (int64_t splits = 1; splits <= all && splits <= 512; splits += 1 + splits / 16) {
+        const int64_t k = (all + splits - 1) / splits;
+        const double products = (double)((tiles * splits + places - 1) / places) * (2.0 + (double)k * tile);
+        const double t = (products > caches ? products : caches) + reads + (double)total * h_q * (double)splits * d * 8 / 4e6;
+        if (splits > 1 && t >= least) continue;
+        least = t;
+        best = k;
+    }
+    const int64_t most_keys = (1LL << 30) / (32 * waves) * (32 * waves);
+    keys = (int32_t)(best * 32 * waves < most_keys ? best * 32 * waves : most_keys);
+    return least;
+}
+
+// The sides' forms.  Own keys: as without groups, few rows a sequence or many.  A prefix's rows are those of its group, but
+// their form of few rows costs only what it reads from the caches again for every 16 rows, and with the own keys in
+// the same form one launch takes both (two requests over 1024 tokens, 2 heads of 256: 14.0 us for 21.3).  bf16: the
+// form of many rows where its time, by long_splits' terms and another launch, is less: 512 rows on each of 2 heads of 256
+// over 31744 tokens take 92 us for 146; 256 rows over 12000 52.4 for 47.  fp32: up to 512 rows for d <= 128 (256 rows
+// of 128 over 12000: 66 us for 80), but not for 256, whose rows of 1 KB leave a workgroup two waves (141 for 197).
 inline SharedPlan shared_plan(int64_t total, int32_t n_seqs, int32_t n_groups, int32_t h_q, int32_t h_kv, int32_t d,
                               int32_t max_prefix, int32_t max_own, int bf16)
 {
     SharedPlan p;
     p.prefix = attn_plan(total, n_groups, h_q, h_kv, d, max_prefix, bf16);
     p.own = attn_plan(total, n_seqs, h_q, h_kv, d, max_own, bf16);
-    if (max_prefix == 0) p.prefix.splits = 0;
-    if (max_own == 0) p.own.splits = 0;
+    const int64_t rows = total * (h_q / h_kv);
+    const bool own_few = max_own == 0 ? rows <= 32 * (int64_t)n_groups : p.own.decode;
+    if (own_few) {
+        const int row = d * (bf16 ? 2 : 4), narrow = decode_waves(row);
+        const int32_t tile = max_own > 0 ? p.own.rows : p.prefix.decode ? p.prefix.rows : 16;
+        double least = 0.0, own_least = 0.0;
+        AttnPlan prefix = p.prefix, own = p.own, alone = p.own;    // own: next to the prefix's form of few rows; alone: without
+        for (int waves = narrow; waves <= (decode_wide(row) ? 2 * narrow : narrow); waves *= 2) {
+            int32_t pk, ok;
+            const double pt = max_prefix > 0 ? few_rows_side(total, n_groups, h_q, h_kv, d, max_prefix, bf16, tile, waves, true, pk) : (pk = 32, 0.0);
+            const double ot = max_own > 0 ? few_rows_side(total, n_seqs, h_q, h_kv, d, max_own, bf16, tile, waves, false, ok) : (ok = 32, 0.0);
+            if (waves == narrow || ot < own_least) {
+                own_least = ot;
+                alone.waves = waves;
+                alone.split_keys = ok;
+            }
+            if (waves > narrow && pt + ot >= least) continue;
+            least = pt + ot;
+            prefix.waves = own.waves = waves;
+            prefix.split_keys = pk;
+            own.split_keys = ok;
+        }
+        bool few = rows <= 32 * (int64_t)n_groups || (!bf16 && d <= 128 && rows <= 512 * (int64_t)n_groups);
+        if (bf16 && !few) {
+            int32_t keys;
+            const double one = few_rows_side(total, n_groups, h_q, h_kv, d, max_prefix, bf16, tile, prefix.waves, true, keys);
+            const int64_t filled = ((rows + p.prefix.rows - 1) / p.prefix.rows + (n_groups - 1) / 2) * h_kv, places = 256 * (256 / p.prefix.rows);
+            const double rounds = (double)((filled * p.prefix.splits + places - 1) / places);
+            const double many = rounds * (p.prefix.split_keys / 64 * 3.7 * d / 256 + 3.0) + (double)total * h_q * p.prefix.splits * d * 8 / 4e6 + 9.0;
+            few = one <= many;
+        }
+        if (!few) own = alone;
+        // contexts of 4096 keys and more may be ragged: splits that do not leave the longest alone
+        if (max_own >= 4096 && own.split_keys > p.own.split_keys) own.split_keys = p.own.split_keys;
+        p.own.rows = tile;
+        p.own.decode = true;
+        p.own.waves = own.waves;
+        p.own.split_keys = own.split_keys;
+        if (few) {
+            p.prefix.rows = tile;
+            p.prefix.decode = true;
+            p.prefix.waves = prefix.waves;
+            p.prefix.split_keys = prefix.split_keys;
+        }
+    }
+    p.prefix.splits = max_prefix > 0 ? (int32_t)(((int64_t)max_prefix + p.prefix.split_keys - 1) / p.prefix.split_keys) : 0;
+    p.own.splits = max_own > 0 ? (int32_t)(((int64_t)max_own + p.own.split_keys - 1) / p.own.split_keys) : 0;
     return p;
 }
 
