@@ -221,7 +221,8 @@ def gdn_cache_extend(new_len, kv_len, block_table, free_pages, free_at, page_siz
     ``prefix_of`` [n_seqs]: the prefix that a request starts behind, -1 for one that goes on (None: all);
     prefix_table [n_prefixes, max_prefix_pages] and prefix_len [n_prefixes], whole pages.  ``total_tokens``: a
     bound on the sum of new_len, and the length of slots and positions.  ``kv_out`` may be kv_len, ``free_out``
-    free_at.  ``slots`` (int64), ``positions``: a tensor, True (allocate) or None.
+    free_at.  ``slots`` (int64), ``positions``: a tensor, True (allocate) or None.  What the call allocates is in one
+    piece of memory, which lives as long as any of it.
     Returns (cu_seqlens, kv_out, free_out, slots, positions).
     """
     if stream is not None:

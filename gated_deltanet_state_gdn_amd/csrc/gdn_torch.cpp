@@ -134,6 +134,28 @@ struct Call {
     at::Tensor make(at::IntArrayRef shape, at::ScalarType dtype) const {
         return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
     }
+    // Outputs in one allocation, each of which costs 1.4 us of a call of 8.
+    struct Piece {
+        at::Tensor &out;
+        bool wanted;
+        int64_t n;
+        at::ScalarType dtype;
+    };
+    void make_pieces(std::initializer_list<Piece> pieces) const {
+        int64_t bytes = 0;
+        for (const Piece &p : pieces)
+            if (p.wanted) bytes += (p.n * (int64_t)c10::elementSize(p.dtype) + 15) / 16 * 16;
+        const at::Tensor all = make({bytes}, at::kByte);
+        int64_t at_byte = 0;
+        for (const Piece &p : pieces) {
+            if (!p.wanted) continue;
+            const int64_t size = (int64_t)c10::elementSize(p.dtype);
+            p.out = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(p.dtype));
+            p.out.unsafeGetTensorImpl()->set_storage_offset(at_byte / size);
+            p.out.unsafeGetTensorImpl()->set_sizes_contiguous({p.n});
+            at_byte += (p.n * size + 15) / 16 * 16;
+        }
+    }
     at::Tensor workspace(PyObject *o, size_t bytes) const {
         if (o == Py_None) return at::zeros({(int64_t)(bytes > 256 ? bytes : 256)}, at::TensorOptions().dtype(at::kByte).device(device));
         if (!THPVariable_Check(o)) refuse(GDN_ERR_SHAPE, "ws", "is not a tensor");
@@ -577,11 +599,8 @@ PyObject *extend(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
         if (pk == Out::given) c.whole(pos = c.tensor(v[14], "positions"), {T}, I32, "positions");
         c.on_gpu();
         c10::DeviceGuard guard(c.device);
-        if (!kvo.defined()) kvo = c.make({n}, I32);
-        if (!fo.defined()) fo = c.make({1}, I32);
-        if (!cu.defined()) cu = c.make({n + 1}, I32);
-        if (sk == Out::make) slots = c.make({T}, I64);
-        if (pk == Out::make) pos = c.make({T}, I32);
+        c.make_pieces({{slots, sk == Out::make, T, I64}, {pos, pk == Out::make, T, I32}, {cu, !cu.defined(), n + 1, I32},
+                       {kvo, !kvo.defined(), n, I32}, {fo, !fo.defined(), 1, I32}});
         const at::Tensor ws = c.workspace(v[15], v[15] == Py_None ? f_extend_ws(d.n_seqs) : 0);
         c.check(f_extend(&d, ptr<int32_t>(add), ptr<int32_t>(kv), ptr<int32_t>(table), ptr<int32_t>(pages), ptr<int32_t>(taken),
                          ptr<int32_t>(of), ptr<int32_t>(pt), ptr<int32_t>(pl), ptr<int32_t>(kvo), ptr<int32_t>(fo), ptr<int32_t>(cu),
