@@ -23,7 +23,7 @@
 namespace gdn {
 namespace {
 
-constexpr int BINS = kSampleBins, NT1 = 256, NT2 = 1024, CAP = 12288, FEW = 256;
+constexpr int BINS = kSampleBins, NT1 = 256, NT2 = 1024, CAP = 16384, FEW = 256;
 constexpr double kUnit = 34359738368.0;                  // 2^35 units: a weight of 1
 constexpr float kHighest = 3.402823466e38f;
 constexpr uint64_t kMass = (1ull << 49) - 1;             // a chunk's bin: mass below, count from bit 49
@@ -62,7 +62,7 @@ __device__ __forceinline__ uint64_t units_bits(double f)
     double p = 1.0 / 188743680.0;                        // 8^-6 / 6!
     p = fma(p, f, 1.0 / 3932160.0);
     p = fma(p, f, 1.0 / 98304.0);
-    p = fma(p, f, 1.0 / 3072.0);
+    p = fma(p, f, 1.0 / 6.0 / 512.0);
     p = fma(p, f, 1.0 / 128.0);
     p = fma(p, f, 1.0 / 8.0);
     p = fma(p, f, 1.0);
@@ -195,19 +195,6 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
 }
 
 // ------------------------------------------------------------- a row's token
-// Tokens in their order: smaller is earlier.
-__device__ __forceinline__ uint64_t order_of(float x, int32_t i)
-{
-    const uint32_t b = __float_as_uint(x);
-    return (uint64_t)(b >> 31 ? b : ~b & 0x7fffffffu) << 32 | (uint32_t)i;
-}
-__device__ __forceinline__ float logit_of(uint64_t o)
-{
-    const uint32_t k = (uint32_t)(o >> 32);
-    return __uint_as_float(k >> 31 ? k : ~k & 0x7fffffffu);
-}
-__device__ __forceinline__ int32_t index_of(uint64_t o) { return (int32_t)(uint32_t)o; }
-
 // Where a first part of the order ends: at its count-th token, at the first token through which the mass is at least or
 // more than so much, or behind the last token that is not behind `order`.
 struct Border {
@@ -229,9 +216,9 @@ struct Plan {
     uint64_t to;                // no token behind this
     double front;               // mass and count in front of the part (-1: all earlier bins')
     uint32_t before;
-    float lo[2], hi[2];         // the wanted tokens' logits are in one of these ranges,
-    int ranges;                 // (0: the first, to the highest; 1: the first; 2: both)
-    int parts;                  // and they in so many parts of the row
+    uint32_t from[4], width[4]; // the wanted tokens' logits have bits in [from, from + width),
+    int intervals;
+    int parts;                  // and they are in so many parts of the row
     int j0;
     bool once, listed, done;
 };
@@ -254,6 +241,71 @@ struct Shared {
     uint32_t n, listed;
 };
 
+// A logit's place in the order: smaller is earlier.  And marks of the elements of some pieces whose bits are in
+// [from, from + width).
+template <class E> struct Marks;
+template <> struct Marks<ElemBF16> {
+    static constexpr int PIECES = 4, APART = 2;          // (APART: 16 elements)
+    static __device__ __forceinline__ uint32_t key(float x)
+    {
+        const uint32_t b = __float_as_uint(x + 0.0f) >> 16;      // -0 counts as 0
+        return b >> 15 ? b : b ^ 0x7fffu;
+    }
+    static __device__ __forceinline__ float logit(uint32_t key)
+    {
+        return fminf(__uint_as_float((key >> 15 ? key : key ^ 0x7fffu) << 16), kHighest);
+    }
+    // the key of the last logit that is x or more
+    static __device__ __forceinline__ uint32_t last_key(float x) { return x > 0.0f ? least(x) ^ 0x7fffu : key(x); }
+    static constexpr uint32_t SIGN = 0x8000u;
+    static __device__ __forceinline__ uint32_t bits(const uint16_t *p) { return *p; }
+    // the bits of the least number from x on, and the largest up to x (x >= 0)
+    static __device__ __forceinline__ uint32_t least(float x) { return (__float_as_uint(x) + 0xffffu) >> 16; }
+    static __device__ __forceinline__ uint32_t most(float x) { return __float_as_uint(x) >> 16; }
+    // two elements at a time: their marks are 16 bits apart
+    static __device__ __forceinline__ uint32_t mark(const u32x4 *raw, uint32_t from, uint32_t width)
+    {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        const u16x2 f = {(unsigned short)from, (unsigned short)from}, w = {(unsigned short)width, (unsigned short)width};
+        const u16x2 one = {1, 1};
+        uint32_t marks = 0;
+#pragma unroll
+        for (int d = 0; d < 4 * PIECES; ++d) {
+            const u16x2 x = __builtin_bit_cast(u16x2, (uint32_t)raw[d / 4][d % 4]);
+            marks |= __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_elementwise_sub_sat(w, (u16x2)(x - f)), one)) << d;
+        }
+        return marks;
+    }
+    static __device__ __forceinline__ int piece(int mark) { return (mark & 15) >> 2; }
+    static __device__ __forceinline__ int element(int mark) { return 2 * (mark & 3) + (mark >> 4); }
+    static constexpr __device__ uint32_t of_piece(int i) { return 0x000f000fu << 4 * i; }
+};
+template <> struct Marks<ElemF32> {
+    static constexpr int PIECES = 4, APART = 4;
+    static __device__ __forceinline__ uint32_t key(float x)
+    {
+        const uint32_t b = __float_as_uint(fminf(x, kHighest) + 0.0f);
+        return b >> 31 ? b : b ^ 0x7fffffffu;
+    }
+    static __device__ __forceinline__ float logit(uint32_t key) { return __uint_as_float(key >> 31 ? key : key ^ 0x7fffffffu); }
+    static __device__ __forceinline__ uint32_t last_key(float x) { return key(x); }
+    static constexpr uint32_t SIGN = 0x80000000u;
+    static __device__ __forceinline__ uint32_t bits(const float *p) { return __float_as_uint(*p); }
+    static __device__ __forceinline__ uint32_t least(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ uint32_t most(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ uint32_t mark(const u32x4 *raw, uint32_t from, uint32_t width)
+    {
+        uint32_t marks = 0;
+#pragma unroll
+        for (int d = 4 * PIECES - 1; d >= 0; --d) marks = marks + marks + (uint32_t)(raw[d / 4][d % 4] - from < width);
+        return marks;
+    }
+    static __device__ __forceinline__ int piece(int mark) { return mark >> 2; }
+    static __device__ __forceinline__ int element(int mark) { return mark & 3; }
+    static constexpr __device__ uint32_t of_piece(int i) { return 0xfu << 4 * i; }
+};
+static_assert(NT2 * 16 <= CAP, "what is listed apart has places");
+
 template <class E>
 struct Picker {
     Shared &s;
@@ -262,8 +314,13 @@ struct Picker {
     double top;                 // the bin of the row's largest logit
     bool far;
     int group;                  // units of a piece a thread in a part of the row
+    int ibits;                  // of an index: the order of a token is its logit's key, and behind that its index
     int n;                      // tokens that are looked at
 
+    __device__ __forceinline__ uint64_t order_of(uint32_t key, int32_t i) const { return (uint64_t)key << ibits | (uint32_t)i; }
+    __device__ __forceinline__ int32_t last_index() const { return (int32_t)((1u << ibits) - 1); }
+    __device__ __forceinline__ float logit_of(uint64_t o) const { return Marks<E>::logit((uint32_t)(o >> ibits)); }
+    __device__ __forceinline__ int32_t index_of(uint64_t o) const { return (int32_t)o & last_index(); }
     __device__ __forceinline__ double through(int j) const { return j < 0 ? 0.0 : s.mass[j]; }
     __device__ __forceinline__ uint32_t counted(int j) const { return j < 0 ? 0u : s.count[j]; }
     __device__ __forceinline__ double below(float x) const { return top - bin_of_logit((double)x, r.scale, far); }
@@ -277,123 +334,157 @@ struct Picker {
     __device__ __forceinline__ void span(int j0, int j1, float &lo, float &hi) const
     {
         const double l = (top - j1 - 0.75) / r.scale, h = (top - j0 + 0.75) / r.scale;
-        lo = (float)(l - fabs(l) * 1e-6);
+        lo = fmaxf((float)(l - fabs(l) * 1e-6), -kHighest);      // (-inf is no token)
         hi = (float)(h + fabs(h) * 1e-6);
         hi = hi >= kHighest ? INFINITY : hi;             // +inf counts as the highest value
     }
-    // The tokens of the row whose logits are in the plan's ranges.  Few are: a thread marks those of some pieces without a
-    // branch, and takes them one at a time in a short loop, which reads them again: a workgroup's waves are bound by the
-    // instructions here, and code that is not in the instruction cache yet costs more than the tokens.
-    // take(marks, order of mark k): called by whole waves.
-    template <class F>
-    __device__ __forceinline__ void each(F take) const
+    // Lists the tokens of the row whose logits are in the plan's intervals, in no order; `apart`: those of the next 16 elements
+    // a thread, from piece `seq` of the parts that have such tokens on.  Whether there is more to list.
+    // A workgroup's waves are bound by the instructions here, and code that is not in the instruction cache yet costs more
+    // than the tokens.  So a thread first marks the tokens of four pieces, by their bits and without a branch, and writes
+    // down where the marked ones are; these are read again, many at a time, when all are known.
+    __device__ __forceinline__ bool list_tokens(bool apart, int &seq) const
     {
-        const float lo0 = s.plan.lo[0], hi0 = s.plan.hi[0], lo1 = s.plan.lo[1], hi1 = s.plan.hi[1];
-        const int ranges = __builtin_amdgcn_readfirstlane(s.plan.ranges);
-        // (bits, not && and ||: no branch for each of them)
-        auto meant = [&](float x) { return (uint32_t)(((x >= lo0) & (x <= hi0)) | ((x >= lo1) & (x <= hi1))); };
-        auto order = [&](int32_t i) { return order_of(fminf(in.one(i), kHighest) + 0.0f, i); };       // -0 counts as 0
-        // The parts that have such tokens, a lane each; a part is `group` units of a piece a thread.
-        constexpr int AHEAD = 32 / E::V;
-        const int parts = s.plan.parts, part_of = s.part[threadIdx.x & 63];
+        typedef Marks<E> M;
+        const int step = apart ? M::APART : M::PIECES, intervals = __builtin_amdgcn_readfirstlane(s.plan.intervals);
+        const int pieces = in.whole0 < in.whole1 ? __builtin_amdgcn_readfirstlane(s.plan.parts) * group : 0;
+        const int part_of = s.part[threadIdx.x & 63];
         const char *from = reinterpret_cast<const char *>(in.base - in.lead);
-        int part = in.whole0 < in.whole1 ? 0 : parts, in_part = 0;
-#pragma unroll 1
-        while (part < parts) {
-            int32_t at[AHEAD];                           // the pieces of these units; -1: none
-            u32x4 raw[AHEAD];
+        const uint32_t per_group = (1u << 20) / (uint32_t)group + 1;       // n per_group >> 20 = n / group, n < 4096 as it is
+        auto unit_of = [&](int n, auto part) {
+            if (group == 1) return part(n);
+            const int q = (int)((uint32_t)n * per_group >> 20);
+            return part(q) * group + n - q * group;
+        };
+        auto load = [&](int at, u32x4 (&raw)[M::PIECES]) {
+            uint32_t real = ~0u;
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int unit = __builtin_amdgcn_readlane(part_of, part < parts ? part : 0) * group + in_part;
+            for (int i = 0; i < M::PIECES; ++i) {
+                const bool wanted = i < step && at + i < pieces;
+                const int unit = unit_of(wanted ? at + i : 0, [&](int q) { return __builtin_amdgcn_readlane(part_of, q); });
                 const int32_t v = unit * NT2 + (int)threadIdx.x, last = in.whole1 - 1;
                 raw[i] = load16(from + (uint32_t)(v < in.whole0 ? in.whole0 : v < last ? v : last) * 16u);
-                at[i] = part < parts ? v : -1;
-                in_part = in_part + 1 < group ? in_part + 1 : 0;
-                part += in_part == 0 ? 1 : 0;
+                if (!wanted || unit == 0 || (unit + 1) * NT2 > in.whole1)        // (else all of the unit's pieces are whole)
+                    real &= wanted && in.is_whole(v) ? ~0u : ~M::of_piece(i);
             }
-            uint32_t marks = 0, whole = 0;
-            auto mark = [&](auto test) {
-#pragma unroll
-                for (int i = AHEAD - 1; i >= 0; --i) {
-                    float x[E::V];
-                    E::unpack(raw[i], x);
-#pragma unroll
-                    for (int k = E::V - 1; k >= 0; --k) marks = marks + marks + test(x[k]);
-                }
-            };
-            if (ranges == 0) mark([&](float x) { return (uint32_t)(x >= lo0); });
-            else if (ranges == 1) mark([&](float x) { return (uint32_t)((x >= lo0) & (x <= hi0)); });
-            else mark(meant);
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) whole |= in.is_whole(at[i]) ? ((1u << E::V) - 1) << (E::V * i) : 0u;
-            marks &= whole;
-            if (!__any(marks != 0)) continue;
-            take(marks, [&](int k) {
-                auto later = [](bool is, int32_t a, int32_t b) { return is ? b : a; };       // (values: addresses would put them in memory)
-                int32_t v = at[0];
-#pragma unroll
-                for (int i = 1; i < AHEAD; ++i) v = later(k >= i * E::V, v, at[i]);
-                return order(in.first(v) + k % E::V);
-            });
-        }
+            return real;
+        };
         // the row's ends: elements in front of the first whole piece, and behind the last
         const bool any = in.whole0 < in.whole1;
         const int32_t front = any ? in.first(in.whole0) : in.vocab, back = any ? in.first(in.whole1) : in.vocab;
-        const int32_t e = (int)threadIdx.x < front ? (int)threadIdx.x : back + (int)threadIdx.x - front;
-        const uint32_t marks = meant(in.one(e));
-        if (__any(marks != 0)) take(marks, [&](int) { return order(e); });
+        const int32_t end = (int)threadIdx.x < front ? (int)threadIdx.x : back + (int)threadIdx.x - front;
+        uint32_t marks, code, at_end = 0;
+        if (threadIdx.x < 16 && end < in.vocab) at_end = Marks<E>::bits(in.base + end);
+        auto put = [&] {
+            // places for the wave's marks, a lane's behind those of the lanes in front
+            uint32_t n = (uint32_t)__popc(marks), to = n;
+            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x111, 0xf, 0xf, false);      // lanes 1, 2, 4, 8 below in 16
+            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x112, 0xf, 0xf, false);
+            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x114, 0xf, 0xf, false);
+            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x118, 0xf, 0xf, false);
+            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x142, 0xa, 0xf, false);      // the 16 below's last
+            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x143, 0xc, 0xf, false);      // the 32 below's last
+            const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)to, 63);
+            if (all == 0) return;
+            uint32_t first = 0;
+            if ((threadIdx.x & 63) == 0) first = atomicAdd(&s.listed, all);
+            first = (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
+            if (first + all > CAP) return;               // too many
+            to += first - n;
+#pragma unroll 1
+            while (marks) {
+                s.list[to++] = code | (uint32_t)__builtin_ctz(marks);
+                marks &= marks - 1;
+            }
+        };
+        int at = seq;
+        if (at < pieces) {
+            u32x4 raw[M::PIECES];
+            uint32_t real = load(at, raw);
+#pragma unroll 1
+            for (;;) {
+                u32x4 next[M::PIECES];
+                const bool more = !apart && at + step < pieces;
+                // (without a branch: behind one, every load would be waited for)
+                const uint32_t next_real = load(at + step, next);
+                marks = 0;
+#pragma unroll 1
+                for (int k = 0; k < intervals; ++k)
+                    marks |= M::mark(raw, (uint32_t)__builtin_amdgcn_readfirstlane((int)s.plan.from[k]),
+                                     (uint32_t)__builtin_amdgcn_readfirstlane((int)s.plan.width[k]));
+                marks &= real;
+                code = (uint32_t)at << 15 | threadIdx.x << 5;
+                put();
+                at += step;
+                if (!more) break;
+                real = next_real;
+#pragma unroll
+                for (int i = 0; i < M::PIECES; ++i) raw[i] = next[i];
+            }
+        }
+        const bool more = at < pieces;
+        if (!more && threadIdx.x < 64) {
+            marks = 0;
+            for (int k = 0; k < intervals; ++k) marks |= at_end - s.plan.from[k] < s.plan.width[k] ? 1u : 0u;
+            if (threadIdx.x >= 16 || end >= in.vocab) marks = 0;
+            code = 1u << 31 | threadIdx.x << 5;
+            put();
+        }
+        seq = at;
+        __syncthreads();
+        const int all = s.listed <= CAP ? (int)s.listed : 0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < all; i += NT2) {
+            const uint32_t c = (uint32_t)s.list[i];
+            const int k = (int)(c & 31), t = (int)(c >> 5 & 1023);
+            const int unit = unit_of((int)(c >> 15 & 0xffff) + M::piece(k), [&](int q) { return s.part[q]; });
+            const int32_t e = c >> 31 ? (t < front ? t : back + t - front) : in.first(unit * NT2 + t) + M::element(k);
+            s.list[i] = order_of(M::key(E::one(in.base + e)), e);
+        }
+        return more;
     }
-    // The passes over the row's meant tokens, or the list of them (one function: its code is read in once):
+    // The passes over the listed tokens, or over the row's, listed 16 elements a thread at a time (one function: its code is read
+    // in once):
     enum Mode { kList, kParts, kFew };
     // makes the list; the tokens of the plan's bin from `from` to `to` into 1024 parts, 2^shift orders each; those that the plan
     // wants, into the few.
     __device__ __forceinline__ void pass(Mode mode, bool listed, uint64_t from, uint64_t to, int shift) const
     {
         const bool once = s.plan.once;
-        const int j = s.plan.j0, lane = threadIdx.x & 63;
-        auto act = [&](uint64_t o) {
-            const float x = logit_of(o);
-            const double b = below(x);
-            if (!(b >= 0.0 && b < (double)BINS) || o < from || o > to || !(once ? s.want[(int)b] : (int)b == j)) return;
-            if (mode == kParts) {
-                const int p = (int)((o - from) >> shift);
-                atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[p]), (unsigned long long)weight_units(x));
-                atomicAdd(&s.subcount[p], 1u);
-            } else {
-                const uint32_t at = atomicAdd(&s.n, 1u);
-                if (at < FEW) s.few[at] = o;
+        const int j = s.plan.j0;
+        int seq = 0;
+        bool more = !listed;
+#pragma unroll 1
+        for (;;) {
+            if (more) {
+                if (mode != kList) {
+                    __syncthreads();
+                    if (threadIdx.x == 0) s.listed = 0;
+                    __syncthreads();
+                }
+                more = list_tokens(mode != kList, seq);
+                if (mode == kList) return;
             }
-        };
-        if (listed) {
+            // (a thread takes the tokens that it wrote)
             const int all = (int)s.listed;
 #pragma unroll 1
-            for (int i = threadIdx.x; i < all; i += NT2) act(s.list[i]);
-            return;
-        }
-        each([&](uint32_t marks, auto order) {
-            uint32_t at = 0;
-            if (mode == kList) {
-                // a place for every mark of the wave: the marks of the lanes in front, by the bits of their numbers
-                const int mine = __popc(marks);
-                uint32_t all = 0, first = 0;
-#pragma unroll
-                for (int b = 0; b < 6; ++b) {
-                    const uint64_t who = __ballot(mine >> b & 1);
-                    at += (uint32_t)__popcll(who & ((1ull << lane) - 1)) << b;
-                    all += (uint32_t)__popcll(who) << b;
+            for (int i = threadIdx.x; i < all; i += NT2) {
+                const uint64_t o = s.list[i];
+                const float x = logit_of(o);
+                if (o < from || o > to) continue;
+                const double b = below(x);
+                if (!(b >= 0.0 && b < (double)BINS) || !(once ? s.want[(int)b] : (int)b == j)) continue;
+                if (mode == kParts) {
+                    const int p = (int)((o - from) >> shift);
+                    atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[p]), (unsigned long long)weight_units(x));
+                    atomicAdd(&s.subcount[p], 1u);
+                } else {
+                    const uint32_t at = atomicAdd(&s.n, 1u);
+                    if (at < FEW) s.few[at] = o;
                 }
-                if (lane == 0) first = atomicAdd(&s.listed, all);
-                at += (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
             }
-#pragma unroll 1
-            while (marks) {
-                const uint64_t o = order(__ffs((int)marks) - 1);
-                marks &= marks - 1;
-                if (mode != kList) act(o);
-                else if (at < CAP) s.list[at] = o;
-                ++at;
-            }
-        });
+            if (!more) return;
+        }
     }
     // Sums over the workgroup in front of each thread.
     __device__ __forceinline__ void scan(double v, uint32_t c, double &front, uint32_t &cfront) const
@@ -486,8 +577,8 @@ struct Picker {
         if (!whole) {
             float lo, hi;
             span(j, j, lo, hi);
-            from = order_of(fminf(hi, kHighest) + 0.0f, 0);
-            const uint64_t end = order_of(lo + 0.0f, -1);
+            from = order_of(Marks<E>::key(hi), 0);
+            const uint64_t end = order_of(Marks<E>::key(lo), last_index());
             to = end < to ? end : to;
         }
         const double unit = s.factor[j] * (1.0 / kUnit);
@@ -650,7 +741,7 @@ struct Chooser {
             const double least = (double)m + (double)r.T * log((double)r.min_p);
             float x = (float)least + 0.0f;
             if ((double)x < least) x = x < 0.0f ? __uint_as_float(__float_as_uint(x) - 1) : __uint_as_float(__float_as_uint(x) + 1);
-            last = order_of(x + 0.0f, -1);
+            last = p.order_of(Marks<E>::last_key(x), p.last_index());
             const double b = p.top - bin_of_logit(least, r.scale, p.far);
             by_m = b < (double)BINS;
             if (by_m) {
@@ -701,29 +792,38 @@ struct Chooser {
         if (need_m) { j0 = jm < j0 ? jm : j0; j1 = jm > j1 ? jm : j1; }
         const int top0 = j0 < js0 ? j0 : js0, last1 = j1 > js1 ? j1 : js1;
         // all of the first bins, if these are not too many; one range where the two meet
-        const bool from_top = (int)s.count[last1] <= (once ? 4 * FEW : CAP * 2 / 3);
+        const bool from_top = (int)s.count[last1] <= (once ? 4 * FEW : CAP * 3 / 4);
         const bool meet = from_top || j1 < 0 || (j0 <= js1 + 1 && j1 >= js0 - 1);
-        range(0, from_top ? 0 : meet ? top0 : js0, meet ? last1 : js1);
-        range(1, meet ? BINS : j0, meet ? -1 : j1);
+        int intervals = range(0, from_top ? 0 : meet ? top0 : js0, meet ? last1 : js1);
+        if (!meet) intervals = range(intervals, j0, j1);
         if (lane == 0) {
             s.plan.once = once;
-            s.plan.listed = !once && looked <= CAP * 2 / 3;      // (the ranges hold more)
             s.plan.parts = __popcll(has);
-            s.plan.ranges = !meet ? 2 : from_top || top0 == 0 ? 0 : 1;
+            s.plan.intervals = intervals;
+            s.plan.listed = looked <= CAP * 3 / 4;       // (the ranges hold more)
             s.plan.done = false;
             s.listed = 0;
         }
         if (once) ask(0, Border{Border::kCount, 0, 0.0, 0});
         else next();
     }
-    __device__ __forceinline__ void range(int i, int j0, int j1)
+    // The bins' logits as intervals of their bits, from number n on: those that are not negative, and the others.
+    __device__ __forceinline__ int range(int n, int j0, int j1)
     {
-        float lo = INFINITY, hi = -INFINITY;
-        if (j0 <= j1) p.span(j0, j1, lo, hi);
-        if ((threadIdx.x & 63) == 0) {
-            p.s.plan.lo[i] = lo;
-            p.s.plan.hi[i] = hi;
-        }
+        float lo, hi;
+        p.span(j0, j1, lo, hi);
+        auto add = [&](uint32_t sign, float a, float b) {        // magnitudes from a to b
+            const uint32_t from = Marks<E>::least(a), to = Marks<E>::most(b);
+            if (!(a <= b) || from > to) return;
+            if ((threadIdx.x & 63) == 0) {
+                p.s.plan.from[n] = sign | from;
+                p.s.plan.width[n] = to - from + 1;
+            }
+            ++n;
+        };
+        if (hi >= 0.0f) add(0, fmaxf(lo, 0.0f), hi);
+        if (lo <= 0.0f) add(Marks<E>::SIGN, fmaxf(-hi, 0.0f), -lo);
+        return n;
     }
     __device__ __forceinline__ void ask(int j, Border b)
     {
@@ -859,7 +959,7 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
         atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[bin]), (unsigned long long)mass);
         atomicAdd(&s.subcount[bin], count);
     }
-    Picker<E> p = {s, r, in, top, far, group, 0};
+    Picker<E> p = {s, r, in, top, far, group, 32 - __clz(a.vocab), 0};
     Chooser<E> choose = {p, m};
     const bool chooses = threadIdx.x < 64;
     __syncthreads();
@@ -872,9 +972,9 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
             const int at = choose.take();
             if (at >= 0 && lane == 0) {
                 const uint64_t o = s.few[at];
-                a.token[row] = index_of(o);
+                a.token[row] = p.index_of(o);
                 // masses are relative to the centre of the first bin
-                if (a.logprob) a.logprob[row] = (float)((far ? 0.0 : 0.125 * fma((double)logit_of(o), r.scale, -top)) - log(choose.kept));
+                if (a.logprob) a.logprob[row] = (float)((far ? 0.0 : 0.125 * fma((double)p.logit_of(o), r.scale, -top)) - log(choose.kept));
                 s.plan.done = true;
             }
         }
