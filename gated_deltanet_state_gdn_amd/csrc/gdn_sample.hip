@@ -57,17 +57,26 @@ __device__ __forceinline__ Row settings(const SampleArgs &a, int row)
 
 // exp(f / 8) in units, |f| <= 1/2, as the low 52 bits of a number of exponent 2^52: the series to the sixth power,
 // off by 7.4e-13 = 2^-40 at most.
-__device__ __forceinline__ uint64_t units_bits(double f)
-{
-    double p = 1.0 / 188743680.0;                        // 8^-6 / 6!
-    p = fma(p, f, 1.0 / 3932160.0);
-    p = fma(p, f, 1.0 / 98304.0);
-    p = fma(p, f, 1.0 / 6.0 / 512.0);
-    p = fma(p, f, 1.0 / 128.0);
-    p = fma(p, f, 1.0 / 8.0);
-    p = fma(p, f, 1.0);
-    return (uint64_t)__double_as_longlong(fma(p, kUnit, 4503599627370496.0));
-}
+struct Series {
+    double c6 = 1.0 / 188743680.0;                       // 8^-6 / 6!
+    double c5 = 1.0 / 3932160.0, c4 = 1.0 / 98304.0, c3 = 1.0 / 6.0 / 512.0, c2 = 1.0 / 128.0, c1 = 1.0 / 8.0;
+    double unit = kUnit, exp52 = 4503599627370496.0;
+    // In registers, one operand of each product and sum in scalar ones: as constants, every use costs two moves.
+    __device__ __forceinline__ void hold()
+    {
+        asm("" : "+v"(c6), "+s"(c5), "+s"(c4), "+s"(c3), "+s"(c2), "+s"(c1), "+v"(unit), "+s"(exp52));
+    }
+    __device__ __forceinline__ uint64_t units_bits(double f) const
+    {
+        double p = fma(c6, f, c5);
+        p = fma(p, f, c4);
+        p = fma(p, f, c3);
+        p = fma(p, f, c2);
+        p = fma(p, f, c1);
+        p = fma(p, f, 1.0);
+        return (uint64_t)__double_as_longlong(fma(p, unit, exp52));
+    }
+};
 constexpr uint64_t kExp52 = 0x4330000000000000ull;       // the bits of 2^52
 
 // Bins so far from 0 that neighbouring values of x are many apart: all tokens of the first 256 are equal.
@@ -177,13 +186,17 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
         if (r.min_p > 0.0f && r.top_p >= 1.0f) below = fmin(below, -1.001 * (double)r.T * log((double)r.min_p));
         const float low = (float)((double)m - below - 1e-6 * fabs((double)m));
         const uint32_t top_bits = (uint32_t)__double_as_longlong(top + kRound);
+        Series series;
+        double round = kRound;
+        series.hold();
+        asm("" : "+s"(round));
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (x[i] >= low) {
-                const double d = (double)fminf(x[i], kHighest), k = fma(d, r.scale, kRound);
+                const double d = (double)__builtin_amdgcn_fmed3f(x[i], low, kHighest), k = fma(d, r.scale, round);
                 const uint32_t at = top_bits - (uint32_t)__double_as_longlong(k);
                 atomicAdd(reinterpret_cast<u64 *>(&bins[at < BINS ? at : BINS]),
-                          (u64)(units_bits(fma(d, r.scale, kRound - k)) + ((1ull << 49) - kExp52)));
+                          (u64)(series.units_bits(fma(d, r.scale, round - k)) + ((1ull << 49) - kExp52)));
             }
     }
     __syncthreads();
@@ -327,7 +340,7 @@ struct Picker {
     __device__ __forceinline__ uint64_t weight_units(float x) const
     {
         const double d = (double)x;
-        return far ? 1ull << 35 : units_bits(fma(d, r.scale, -bin_of_logit(d, r.scale, false))) - kExp52;
+        return far ? 1ull << 35 : Series().units_bits(fma(d, r.scale, -bin_of_logit(d, r.scale, false))) - kExp52;
     }
     static __device__ __forceinline__ int some_bin(double b) { return b >= 0.0 && b < (double)BINS ? (int)b : 0; }
     // All logits of the bins [j0, j1] are in [lo, hi], which is little wider.
