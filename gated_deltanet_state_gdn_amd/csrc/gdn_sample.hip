@@ -89,6 +89,37 @@ __device__ __forceinline__ double bin_of_logit(double d, double scale, bool far)
     return far ? rint(d * scale) : fma(d, scale, kRound) - kRound;
 }
 
+// The wave's sums through each lane, by moves between lanes within an instruction (through LDS each step waits for its
+// answer).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lane_moved(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lane_moved(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)lane_moved<CTRL, ROWS>((uint32_t)(b >> 32)) << 32 | lane_moved<CTRL, ROWS>((uint32_t)b)));
+}
+template <class V>
+__device__ __forceinline__ void scan16(V &v)
+{
+    v += lane_moved<0x111, 0xf>(v);                      // from 1, 2, 4, 8 lanes below in the 16
+    v += lane_moved<0x112, 0xf>(v);
+    v += lane_moved<0x114, 0xf>(v);
+    v += lane_moved<0x118, 0xf>(v);
+}
+template <class V>
+__device__ __forceinline__ void scan64(V &v)
+{
+    scan16(v);
+    v += lane_moved<0x142, 0xa>(v);                      // the last of the 16 below, to the second and fourth
+    v += lane_moved<0x143, 0xc>(v);                      // the last of the first 32, to the others
+}
+template <class V>
+__device__ __forceinline__ V from_below(V v) { return lane_moved<0x138, 0xf>(v); }      // lane 0: zero
+
 // A row's tokens in 16-byte pieces: piece v holds the elements [v V - lead, v V - lead + V), at the row's ends in
 // part (rows start anywhere).  Elements that are not the row's are -inf.
 template <class E>
@@ -391,12 +422,7 @@ struct Picker {
         auto put = [&] {
             // places for the wave's marks, a lane's behind those of the lanes in front
             uint32_t n = (uint32_t)__popc(marks), to = n;
-            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x111, 0xf, 0xf, false);      // lanes 1, 2, 4, 8 below in 16
-            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x112, 0xf, 0xf, false);
-            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x114, 0xf, 0xf, false);
-            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x118, 0xf, 0xf, false);
-            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x142, 0xa, 0xf, false);      // the 16 below's last
-            to += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)to, 0x143, 0xc, 0xf, false);      // the 32 below's last
+            scan64(to);
             const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)to, 63);
             if (all == 0) return;
             uint32_t first = 0;
@@ -502,31 +528,25 @@ struct Picker {
     // Sums over the workgroup in front of each thread.
     __device__ __forceinline__ void scan(double v, uint32_t c, double &front, uint32_t &cfront) const
     {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         double t = v;
         uint32_t n = c;
-#pragma unroll 1
-        for (int off = 1; off < 64; off <<= 1) {
-            const double o = __shfl_up(t, off);
-            const uint32_t on = __shfl_up(n, off);
-            if (lane >= off) {
-                t += o;
-                n += on;
-            }
-        }
-        __syncthreads();
+        scan64(t);
+        scan64(n);
         if (lane == 63) {
             s.wsum[wave] = t;
             s.wcount[wave] = n;
         }
-        front = __shfl_up(t, 1);
+        front = from_below(t);
         cfront = n - c;
-        if (lane == 0) front = 0.0;
         __syncthreads();
-#pragma unroll 1
-        for (int w = 0; w < wave; ++w) {
-            front += s.wsum[w];
-            cfront += s.wcount[w];
+        double all = s.wsum[lane & 15];                  // through wave lane % 16
+        uint32_t call = s.wcount[lane & 15];
+        scan16(all);
+        scan16(call);
+        if (wave > 0) {
+            front += __shfl(all, wave - 1);
+            cfront += (uint32_t)__builtin_amdgcn_readlane((int)call, wave - 1);
         }
     }
     // The mass that a token brings: its own, and that of the bins in front of it that none of the few is of.
@@ -566,11 +586,7 @@ struct Picker {
         for (int i0 = 0; i0 < n; i0 += 64) {
             const int i = i0 + (int)threadIdx.x;
             double w = i < n ? brings(i) : 0.0;
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const double o = __shfl_up(w, off);
-                if ((int)threadIdx.x >= off) w += o;
-            }
+            scan64(w);
             w += run;
             if (i < n) s.run[i] = w;
             run = __shfl(w, 63);
@@ -621,13 +637,15 @@ struct Picker {
                 const uint64_t start = from + ((uint64_t)threadIdx.x << shift), end = start + ((1ull << shift) - 1);
                 // the first part that reaches the border, else (by rounding) the last that has tokens
                 const bool reaches = s.plan.border.reached(front + (u0 + u) * unit, before + c0 + c, end);
-                if (c > 0 && reaches) atomicMin(&s.n, (uint32_t)threadIdx.x);
+                const uint32_t wave0 = threadIdx.x & ~63u;
+                const uint64_t here = __ballot(c > 0), there = __ballot(c > 0 && reaches);
+                if (threadIdx.x == wave0 && there) atomicMin(&s.n, wave0 + (uint32_t)__builtin_ctzll(there));
                 __syncthreads();
                 if (s.n == 0xffffffffu) {
                     __syncthreads();
                     if (threadIdx.x == 0) s.n = 0;
                     __syncthreads();
-                    if (c > 0) atomicMax(&s.n, (uint32_t)threadIdx.x);
+                    if (threadIdx.x == wave0 && here) atomicMax(&s.n, wave0 + 63 - (uint32_t)__builtin_clzll(here));
                     __syncthreads();
                 }
                 const uint32_t at = s.n;
@@ -642,11 +660,8 @@ struct Picker {
                 const uint64_t first = from + ((uint64_t)at << shift), last = first + ((1ull << shift) - 1);
                 from = first;
                 to = last < to ? last : to;
-                if (inside <= FEW) {
-                    __syncthreads();
-                    if (threadIdx.x == 0) s.n = 0;
-                    __syncthreads();
-                }
+                if (threadIdx.x == 0) s.n = 0;
+                __syncthreads();
             }
             mode = inside > FEW ? kParts : kFew;
         }
@@ -708,21 +723,14 @@ struct Chooser {
             mass[i] = v;
             count[i] = c;
         }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const double o = __shfl_up(v, off);
-            const uint32_t oc = __shfl_up(c, off);
-            if (lane >= off) {
-                v += o;
-                c += oc;
-            }
-        }
-        v = __shfl_up(v, 1);
-        c = __shfl_up(c, 1);
+        scan64(v);
+        scan64(c);
+        v = from_below(v);
+        c = from_below(c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            mass[i] += lane ? v : 0.0;
-            count[i] += lane ? c : 0;
+            mass[i] += v;
+            count[i] += c;
             s.mass[4 * lane + i] = mass[i];
             s.count[4 * lane + i] = count[i];
         }
