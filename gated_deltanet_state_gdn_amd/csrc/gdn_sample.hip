@@ -162,8 +162,6 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
     __shared__ float wmax[NT1 / 64];
     __shared__ int first;
     const int row = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
-    const Row r = settings(a, row);
-    if (!r.ok) return;
     const RowReader<E> in(a, row);
     const int32_t v0 = c * PIECES * NT1 + (int)threadIdx.x;
     u32x4 raw[PIECES];
@@ -172,6 +170,8 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
     if (in.whole0 < in.whole1)
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) raw[i] = in.load(v0 + i * NT1);
+    const Row r = settings(a, row);                      // (behind the loads: they do not wait for these)
+    if (!r.ok) return;
     float x[N];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) in.unpack(v0 + i * NT1, raw[i], x + i * E::V);
@@ -908,6 +908,8 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
     __shared__ float wmax[NT2 / 64];
     __shared__ int first;
     const int row = blockIdx.x, lane = threadIdx.x & 63;
+    const ChunkHead *heads = static_cast<const ChunkHead *>(a.heads) + (int64_t)row * a.chunks;
+    const ChunkHead mine = heads[(int)threadIdx.x < a.chunks ? threadIdx.x : 0];      // (does not wait for the settings)
     const Row r = settings(a, row);
     if (!r.ok) {
         if (threadIdx.x == 0) {
@@ -917,13 +919,11 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
         }
         return;
     }
-    const ChunkHead *heads = static_cast<const ChunkHead *>(a.heads) + (int64_t)row * a.chunks;
     ChunkHead *near = reinterpret_cast<ChunkHead *>(s.list);
     float m = -INFINITY;
     if ((int)threadIdx.x < a.chunks) {                   // the first ones stay at hand
-        const ChunkHead h = heads[threadIdx.x];
-        m = fmaxf(m, h.max);
-        near[threadIdx.x] = h;
+        m = fmaxf(m, mine.max);
+        near[threadIdx.x] = mine;
     }
 #pragma unroll 1
     for (int c = NT2 + threadIdx.x; c < a.chunks; c += NT2) m = fmaxf(m, heads[c].max);
@@ -966,15 +966,28 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
         uint64_t mass = 0, has = 0;
         uint32_t count = 0;
         const int pieces = a.chunk / E::V;               // of a chunk: 256 to 2048
-#pragma unroll 4
-        for (int c = threadIdx.x / BINS; c < a.chunks; c += PARTS) {
-            const ChunkHead h = c < NT2 ? near[c] : heads[c];
-            const double off = top - h.top;
-            const bool some = h.max != -INFINITY && off <= (double)bin;
-            const uint64_t b = some ? bins[(int64_t)c * BINS + bin - (int)off] : 0;
-            mass += b & kMass;
-            count += (uint32_t)(b >> 49);
-            if (b >> 49) has |= 1ull << (c * pieces / NT2 / group) | 1ull << (((c + 1) * pieces - 1) / NT2 / group);
+        auto part = [&](int unit) { return 1ull << (group == 1 ? unit : unit / group); };
+#pragma unroll 1
+        for (int c0 = __builtin_amdgcn_readfirstlane((int)threadIdx.x / BINS); c0 < a.chunks; c0 += 8 * PARTS) {
+            uint64_t b[8];
+            bool some[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = c0 + i * PARTS < a.chunks ? c0 + i * PARTS : c0;
+                const ChunkHead h = c < NT2 ? near[c] : heads[c];
+                const double off = top - h.top;
+                some[i] = c0 + i * PARTS < a.chunks && h.max != -INFINITY && off <= (double)bin;
+                b[i] = bins[(int64_t)c * BINS + (some[i] ? bin - (int)off : 0)];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = c0 + i * PARTS < a.chunks ? c0 + i * PARTS : c0;
+                const uint64_t parts = part(c * pieces / NT2) | part(((c + 1) * pieces - 1) / NT2);
+                b[i] = some[i] ? b[i] : 0;
+                mass += b[i] & kMass;
+                count += (uint32_t)(b[i] >> 49);
+                has |= b[i] >> 49 ? parts : 0;
+            }
         }
         if (has) atomicOr(reinterpret_cast<unsigned long long *>(&s.has[bin]), (unsigned long long)has);
         atomicAdd(reinterpret_cast<unsigned long long *>(&s.sub[bin]), (unsigned long long)mass);
