@@ -683,7 +683,9 @@ struct Picker {
         }
         return n;
     }
-    __device__ __forceinline__ double mass_at(int i) const { return s.run[i < n ? i : n - 1]; }
+    // The mass in front of the few.  There may be none: tokens of a bin that min-p drops are not wanted.
+    __device__ __forceinline__ double in_front() const { return s.plan.front >= 0.0 ? s.plan.front : through(s.plan.j0 - 1); }
+    __device__ __forceinline__ double mass_at(int i) const { return n == 0 ? in_front() : s.run[i < n ? i : n - 1]; }
 };
 
 // The first wave's part: borders, the tokens to look at, and the token.
@@ -768,7 +770,7 @@ struct Chooser {
             if (by_m) {
                 jm = b > 0.0 ? __builtin_amdgcn_readfirstlane((int)b) : 0;
                 mlo = p.through(jm - 1);
-                mhi = p.through(jm);
+                mhi = p.counted(jm) > p.counted(jm - 1) ? p.through(jm) : mlo;      // (sums through empty bins may differ by roundings)
             }
         }
         const double hi = fmin(fmin(khi, phi), mhi), lo = fmin(fmin(klo, plo), mlo);
@@ -812,10 +814,9 @@ struct Chooser {
         if (need_p) { j0 = jp0 < j0 ? jp0 : j0; j1 = jp1 > j1 ? jp1 : j1; }
         if (need_m) { j0 = jm < j0 ? jm : j0; j1 = jm > j1 ? jm : j1; }
         const int top0 = j0 < js0 ? j0 : js0, last1 = j1 > js1 ? j1 : js1;
-        // all of the first bins, if these are not too many; one range where the two meet
-        const bool from_top = (int)s.count[last1] <= (once ? 4 * FEW : CAP * 3 / 4);
-        const bool meet = from_top || j1 < 0 || (j0 <= js1 + 1 && j1 >= js0 - 1);
-        int intervals = range(0, from_top ? 0 : meet ? top0 : js0, meet ? last1 : js1);
+        // one range where the two meet
+        const bool meet = j1 < 0 || (j0 <= js1 + 1 && j1 >= js0 - 1);
+        int intervals = range(0, meet ? top0 : js0, meet ? last1 : js1);
         if (!meet) intervals = range(intervals, j0, j1);
         if (lane == 0) {
             s.plan.once = once;
@@ -886,7 +887,7 @@ struct Chooser {
                 kept = fmin(kept, p.mass_at(p.first_that([&](int i) { return s.run[i] >= want; })));
             } else if (step == 2) {
                 const int end = p.first_that([&](int i) { return s.few[i] > last; });
-                kept = fmin(kept, fmax(end > 0 ? p.mass_at(end - 1) : 0.0, once ? p.through(jm - 1) : s.plan.front));
+                kept = fmin(kept, fmax(end > 0 ? p.mass_at(end - 1) : 0.0, once ? p.through(jm - 1) : p.in_front()));
             } else {
                 const double want = (double)p.r.u * kept;
                 const int at = p.first_that([&](int i) { return s.run[i] > want; });

@@ -147,6 +147,22 @@ def test_sample_borders_far_apart(dt, sign):
 
 
 @TYPES
+def test_sample_bins_of_what_min_p_drops(dt):
+    # min-p's border, and top-k's, in a bin whose tokens are all behind it.  They are counted, for their chunk's largest
+    # logit is lower than the row's; the token's own bin holds too many for one look at both
+    rows, vocab = 4, 5000
+    r = Rand(76)
+    x = torch.full((rows, vocab), -9.0)
+    x[:, 3] = 0.0
+    x[:, 2500:3100] = -0.5 + (torch.randint(0, 12, (rows, 600), generator=r.g) - 6) * 2.0 ** -8
+    x[:, 4000:4010] = -1.03125
+    u = torch.tensor([0.1, 0.5, 0.9, 0.999], device="cuda")
+    for k in (0, 603, 611):
+        for T, m in ((1.0, math.exp(-1.0)), (2.0, math.exp(-0.5))):
+            draw_check(x.to(dt).cuda(), u, settings(rows, T=T, m=m, k=k))
+
+
+@TYPES
 def test_sample_rows_behind_32_bits(dt):
     rows, vocab, stride = 3, 5000, 2 ** 30 + 8
     r = Rand(74)
