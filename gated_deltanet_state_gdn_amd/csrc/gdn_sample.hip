@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
         int at = 0x7fffffff;
 #pragma unroll
         for (int i = N - 1; i >= 0; --i)
-            if (fminf(x[i], kHighest) == m) at = in.first(v0 + i / E::V * NT1) + i % E::V;
+            if (x[i] >= m) at = in.first(v0 + i / E::V * NT1) + i % E::V;
         if (at != 0x7fffffff) atomicMin(&first, at);
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
     if (far) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (fminf(x[i], kHighest) == m) atomicAdd(reinterpret_cast<u64 *>(&bins[0]), (u64)((1ull << 49) + (1ull << 35)));
+            if (x[i] >= m) atomicAdd(reinterpret_cast<u64 *>(&bins[0]), (u64)((1ull << 49) + (1ull << 35)));
     } else {
         // what lies below has no bin; with min-p and without top-p, which wants the mass of all, what min-p drops
         double below = 33.0 * (double)r.T;

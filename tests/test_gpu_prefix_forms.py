@@ -163,6 +163,20 @@ def test_sample_bins_of_what_min_p_drops(dt):
 
 
 @TYPES
+def test_sample_nan_beside_infinity(dt):
+    # NaN is no token, also where the row's largest logit is +inf
+    r = Rand(77)
+    x = r.n(4, 3000).to(dt)
+    x[0, 5], x[0, 2500] = math.nan, math.inf
+    x[1, 100], x[1, 99] = math.inf, math.nan
+    x[2, :] = math.nan
+    x[2, 2999] = math.inf
+    x[3, 7], x[3, 8] = math.nan, torch.finfo(dt).max
+    for T in (0.0, 1e-3, 1.0):
+        draw_check(x, torch.tensor([0.1, 0.4, 0.6, 0.9], device="cuda"), settings(4, T=T)), draw_check(x, torch.rand(4).cuda(), settings(4, T=T, k=4, p=0.9))
+
+
+@TYPES
 def test_sample_rows_behind_32_bits(dt):
     rows, vocab, stride = 3, 5000, 2 ** 30 + 8
     r = Rand(74)
