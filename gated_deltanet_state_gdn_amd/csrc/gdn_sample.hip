@@ -879,8 +879,10 @@ struct Chooser {
         for (;; ++step) {
             if (!needed()) continue;
             if (step == 0) {
-                // the count-th token: in the list the tokens of the wanted bins in front of its own, and of its own, are before it
+                // the count-th token: in the list the tokens of the wanted bins in front of its own, and of its own, are before it;
+                // where it is none of the few, for min-p drops it, those of its bin that stay
                 mk = p.mass_at((int)((uint32_t)p.r.top_k - 1 + (once ? ahead - p.counted(jk - 1) : 0u - s.plan.before)));
+                mk = fmax(mk, once ? p.through(jk - 1) : p.in_front());
                 kept = fmin(kept, mk);
             } else if (step == 1) {
                 const double want = (double)p.r.top_p * mk;

@@ -163,6 +163,21 @@ def test_sample_bins_of_what_min_p_drops(dt):
 
 
 @TYPES
+def test_sample_few_tokens_of_which_min_p_drops_some(dt):
+    # as above, with few tokens: all borders are looked at together, and a bin between the token's and theirs is not
+    rows, vocab = 5, 5000
+    x = torch.full((rows, vocab), -9.0)
+    x[:, 3] = 0.0
+    x[:, 2500:2505] = -0.5
+    x[:, 3000:3004] = -0.75
+    x[:, 4000:4010] = -1.03125
+    u = torch.tensor([0.1, 0.3, 0.5, 0.9, 0.999], device="cuda")
+    for k in (0, 1, 5, 8, 10, 12, 19):
+        for T, m in ((1.0, math.exp(-1.0)), (2.0, math.exp(-0.5)), (1.0, 0.999), (1.0, math.exp(-0.52))):
+            draw_check(x.to(dt).cuda(), u, settings(rows, T=T, m=m, k=k))
+
+
+@TYPES
 def test_sample_nan_beside_infinity(dt):
     # NaN is no token, also where the row's largest logit is +inf
     r = Rand(77)
