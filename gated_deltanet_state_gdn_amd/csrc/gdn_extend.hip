@@ -114,7 +114,8 @@ __device__ __forceinline__ void put_nothing(const ExtendArgs &a, int64_t t)
 }
 
 // Up to kAlone requests, and tokens and table entries together: every sum fits 32 bits, and the scans' results LDS.
-// 64 requests with a token each: 5.2 us (9.4 with the results in memory, whose latency every step of a search then has).
+// Bound by the latency of its dependent loads and barriers.  64 requests with a token each: 4.2 us; the call 5.6, 8.8 by the
+// two launches below; 1000 of them 9.3 and 11.8, and 64 prompts of 900 tokens together 6.6 and 9.5.
 __global__ void __launch_bounds__(NA) alone_kernel(ExtendArgs a)
 {
     constexpr int PER = kAlone / NA;
@@ -196,44 +197,37 @@ __global__ void __launch_bounds__(NT) plan_kernel(ExtendArgs a)
     const int32_t at = *a.free_at;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
-    const bool once = a.n_seqs <= NT;                    // a request a thread: one pass
+    // so many neighbouring requests a thread, looked at twice if they are more than one (2000 requests: 13.8 us for 19.6 in
+    // rounds of one a thread, with a scan each)
+    const int per = (a.n_seqs + NT - 1) / NT, n0 = (int)threadIdx.x * per;
+    const int n1 = n0 + per < a.n_seqs ? n0 + per : a.n_seqs;
     Wants w = {};
-    Three<int64_t> all = {{0, 0, 0}}, before = {{0, 0, 0}};
-    {
-        Three<int64_t> mine = {{0, 0, 0}};
-        bool ok = true;
-        for (int n = threadIdx.x; n < a.n_seqs; n += NT) {
-            w = wants(a, n);
-            ok &= w.ok;
-            mine.x[0] += w.tokens;
-            mine.x[1] += w.need;
-            mine.x[2] += w.entries;
-        }
-        if (!ok) bad = 1;
-        before = scan<NT>(mine, all, part);
+    Three<int64_t> mine = {{0, 0, 0}}, all;
+    bool ok = true;
+    for (int n = n0; n < n1; ++n) {
+        w = wants(a, n);
+        ok &= w.ok;
+        mine.x[0] += w.tokens;
+        mine.x[1] += w.need;
+        mine.x[2] += w.entries;
     }
+    if (!ok) bad = 1;
+    Three<int64_t> s = scan<NT>(mine, all, part);        // (its barriers show `bad` to all)
     const bool fits = !bad && at >= 0 && at <= a.n_free && all.x[0] <= a.total && all.x[1] <= a.n_free - at;
-    Three<int64_t> done = {{0, 0, 0}};
     Request *req = requests(a);
-    for (int n0 = 0; n0 < a.n_seqs; n0 += NT) {
-        const int n = n0 + threadIdx.x;
-        Three<int64_t> sum = all, s = before;
-        if (!once) {
-            w = Wants{};
-            if (n < a.n_seqs) w = wants(a, n);
-            s = scan<NT>(Three<int64_t>{{w.tokens, w.need, w.entries}}, sum, part);
-        }
-        if (n < a.n_seqs && fits) {
-            req[n] = Request{w.base, (int32_t)(at + done.x[1] + s.x[1]), done.x[2] + s.x[2]};
-            a.cu[n] = (int32_t)(done.x[0] + s.x[0]);
+    for (int n = n0; n < n1; ++n) {
+        if (per > 1) w = wants(a, n);
+        if (fits) {
+            req[n] = Request{w.base, (int32_t)(at + s.x[1]), s.x[2]};
+            a.cu[n] = (int32_t)s.x[0];
             a.kv_out[n] = w.base + w.tokens;
-        }
-        if (n < a.n_seqs && !fits) {
+        } else {
             a.cu[n] = 0;
             a.kv_out[n] = a.kv_len[n];
         }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) done.x[i] += sum.x[i];
+        s.x[0] += w.tokens;
+        s.x[1] += w.need;
+        s.x[2] += w.entries;
     }
     if (threadIdx.x == 0) {
         if (!fits) set_status(a.status);
