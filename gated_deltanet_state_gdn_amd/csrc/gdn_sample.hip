@@ -549,12 +549,16 @@ struct Picker {
             cfront += (uint32_t)__builtin_amdgcn_readlane((int)call, wave - 1);
         }
     }
+    __device__ __forceinline__ double mass_of(float x) const
+    {
+        return (double)weight_units(x) * (1.0 / kUnit) * s.factor[some_bin(below(x))];
+    }
     // The mass that a token brings: its own, and that of the bins in front of it that none of the few is of.
     __device__ __forceinline__ double brings(int i) const
     {
         const float x = logit_of(s.few[i]);
         const double b = below(x);
-        double w = (double)weight_units(x) * (1.0 / kUnit) * s.factor[some_bin(b)];
+        double w = mass_of(x);
         if (i == 0) {
             w += s.plan.front >= 0.0 ? s.plan.front : through(some_bin(b) - 1);
         } else {
@@ -1010,8 +1014,8 @@ __global__ void __launch_bounds__(NT2) pick_kernel(SampleArgs a)
             if (at >= 0 && lane == 0) {
                 const uint64_t o = s.few[at];
                 a.token[row] = p.index_of(o);
-                // masses are relative to the centre of the first bin
-                if (a.logprob) a.logprob[row] = (float)((far ? 0.0 : 0.125 * fma((double)p.logit_of(o), r.scale, -top)) - log(choose.kept));
+                // by the weight that its mass has: zero where it is the only one
+                if (a.logprob) a.logprob[row] = (float)(0.0 - log(choose.kept / p.mass_of(p.logit_of(o))));
                 s.plan.done = true;
             }
         }

@@ -178,6 +178,19 @@ def test_sample_few_tokens_of_which_min_p_drops_some(dt):
 
 
 @TYPES
+def test_sample_logprob_of_the_only_token_is_zero(dt):
+    r = Rand(78)
+    for vocab in (5, 3000, 70000):
+        x = r.n(12, vocab, scale=3.0).to(dt)
+        x[:, 2] = 40.0 + 0.25 * torch.arange(12).cuda()          # anywhere in a bin
+        x[6:, 4] = 0.5 * x[6:, 2]                                # one more, of little weight
+        u = torch.rand(12, generator=r.g).cuda()
+        for kw in (dict(k=1), dict(p=1e-6), dict(m=1.0), dict(m=0.9, T=0.7), dict(k=1, p=0.5, m=0.1, T=3.0), dict(T=0.0), dict(T=1e-12)):
+            token, lp = G().gdn_sample(x, u, logprob=True, **settings(12, **kw))
+            assert (token == 2).all() and (lp == 0).all(), (vocab, kw, lp.tolist())
+
+
+@TYPES
 def test_sample_nan_beside_infinity(dt):
     # NaN is no token, also where the row's largest logit is +inf
     r = Rand(77)
