@@ -201,13 +201,13 @@ __global__ void __launch_bounds__(NT) plan_kernel(ExtendArgs a)
     __syncthreads();
     // so many neighbouring requests a thread, looked at twice if they are more than one (2000 requests: 13.8 us for 19.6 in
     // rounds of one a thread, with a scan each)
-    const int per = (a.n_seqs + NT - 1) / NT, n0 = (int)threadIdx.x * per;
-    const int n1 = n0 + per < a.n_seqs ? n0 + per : a.n_seqs;
+    const int64_t per = ((int64_t)a.n_seqs + NT - 1) / NT, n0 = (int64_t)threadIdx.x * per;
+    const int64_t n1 = n0 + per < a.n_seqs ? n0 + per : a.n_seqs;
     Wants w = {};
     Three<int64_t> mine = {{0, 0, 0}}, all;
     bool ok = true;
-    for (int n = n0; n < n1; ++n) {
-        w = wants(a, n);
+    for (int64_t n = n0; n < n1; ++n) {
+        w = wants(a, (int)n);
         ok &= w.ok;
         mine.x[0] += w.tokens;
         mine.x[1] += w.need;
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(NT) plan_kernel(ExtendArgs a)
     Three<int64_t> s = scan<NT>(mine, all, part);        // (its barriers show `bad` to all)
     const bool fits = !bad && at >= 0 && at <= a.n_free && all.x[0] <= a.total && all.x[1] <= a.n_free - at;
     Request *req = requests(a);
-    for (int n = n0; n < n1; ++n) {
-        if (per > 1) w = wants(a, n);
+    for (int64_t n = n0; n < n1; ++n) {
+        if (per > 1) w = wants(a, (int)n);
         if (fits) {
             req[n] = Request{w.base, (int32_t)(at + s.x[1]), s.x[2]};
             a.cu[n] = (int32_t)s.x[0];

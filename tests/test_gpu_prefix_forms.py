@@ -205,6 +205,42 @@ def test_sample_nan_beside_infinity(dt):
 
 
 @TYPES
+def test_sample_of_the_largest_vocabulary(dt):
+    # 2^24 tokens, rows that start inside 16 bytes: every part of a row's bookkeeping at its end.  The order and the sums are
+    # torch's in 64 bits; what a border of 2^-34 of the mass or nearer would decide is left out
+    vocab = 1 << 24
+    r = Rand(79)
+    wide = r.n(3, vocab + 3, scale=1.5).to(dt)
+    wide[1] = torch.rand(vocab + 3, generator=r.g).cuda().to(dt)
+    x = wide[:, 3:]
+    x[2, :] = -30.0
+    x[2, vocab - 1], x[2, 5] = 1.0, -3.0
+    u = torch.tensor([0.37, 0.81, 1.0 - 2.0 ** -20], device="cuda")
+    for T, k, p, m in ((1.0, 0, 1.0, 0.0), (1.0, 9000000, 0.7, 0.0), (0.8, 0, 0.999, 0.01), (0.0, 0, 1.0, 0.0)):
+        token, lp = G().gdn_sample(x, u, logprob=True, **settings(3, T=T, k=k, p=p, m=m))
+        for i in range(3):
+            if T == 0.0:
+                assert token[i].item() == int(x[i].float().argmax()) if i == 2 else x[i, token[i]] == x[i].max()
+                continue
+            v, order = torch.sort(x[i].double(), descending=True, stable=True)
+            w = ((v - v[0]) / T).exp().cpu()
+            c = w.cumsum(0)
+            n = min(k or vocab, vocab)
+            if p < 1.0:
+                n = int((c[:n] < c[n - 1] * settings(1, p=p)["top_p"].double().item()).sum()) + 1
+            if m > 0.0:
+                n = min(n, int((w >= settings(1, m=m)["min_p"].double().item()).sum()))
+            want = u[i].double().item() * c[n - 1].item()
+            at = int((c[:n] <= want).sum())
+            near = min(abs(c[j].item() - want) for j in (at - 1, at) if j >= 0) / c[n - 1].item()
+            say("  T %g k %d p %g m %g row %d: token %d of the order, %.1e from a border" % (T, k, p, m, i, at, near))
+            # the sums here carry 2^24 roundings of 2^-53 and bins of so many tokens theirs, and p's border moves u's
+            if near > 2.0 ** -26:
+                assert token[i].item() == order[at].item()
+            assert abs(lp[i].item() - math.log(w[at].item() / c[n - 1].item())) <= R.U32 * 20 + 2.0 ** -20
+
+
+@TYPES
 def test_sample_rows_behind_32_bits(dt):
     rows, vocab, stride = 3, 5000, 2 ** 30 + 8
     r = Rand(74)
