@@ -30,7 +30,9 @@
 namespace gdn {
 namespace {
 
-constexpr int BINS = kSampleBins, NT1 = 256, NT2 = 1024, CAP = 16384, FEW = 256;
+constexpr int BINS = kSampleBins, NT1 = 256, NT2 = 1024, FEW = 256;
+// of the list: one turn's marks, 16 a thread, and the elements outside of a row's whole pieces, at most 7 at either end
+constexpr int ENDS = 2 * 7, CAP = NT2 * 16 + ENDS;
 constexpr double kUnit = 34359738368.0;                  // 2^35 units: a weight of 1
 constexpr float kHighest = 3.402823466e38f;
 constexpr uint64_t kMass = (1ull << 49) - 1;             // a chunk's bin: mass below, count from bit 49
@@ -248,7 +250,8 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
 
 // ------------------------------------------------------------- a row's token
 // Looking for wanted tokens: 4 instructions for two bf16 elements of an interval, 3 for one of fp32.  CAP: all that one
-// turn of a workgroup can mark, so that rows with more are looked through that much at a time (no list at all: 64 rows of
+// turn of a workgroup can mark and the row's ends, which the last turn lists too, so that rows with more are looked through
+// that much at a time (no list at all: 64 rows of
 // 131072 90 us for 44, 256 with filters 222 for 77).  FEW: what one workgroup sorts by counting.
 // Where a first part of the order ends: at its count-th token, at the first token through which the mass is at least or
 // more than so much, or behind the last token that is not behind `order`.
@@ -359,7 +362,9 @@ template <> struct Marks<ElemF32> {
     static __device__ __forceinline__ int element(int mark) { return mark & 3; }
     static constexpr __device__ uint32_t of_piece(int i) { return 0xfu << 4 * i; }
 };
-static_assert(NT2 * 16 <= CAP, "what is listed apart has places");
+template <class E>
+constexpr bool apart_fits = Marks<E>::APART * E::V * NT2 + 2 * (E::V - 1) <= CAP && 2 * (E::V - 1) <= 16;
+static_assert(apart_fits<ElemBF16> && apart_fits<ElemF32>, "what is listed apart has places, and each of the ends a thread");
 
 template <class E>
 struct Picker {
@@ -516,7 +521,7 @@ struct Picker {
                 if (mode == kList) return;
             }
             // (a thread takes the tokens that it wrote)
-            const int all = (int)s.listed;
+            const int all = s.listed <= CAP ? (int)s.listed : 0;
 #pragma unroll 1
             for (int i = threadIdx.x; i < all; i += NT2) {
                 const uint64_t o = s.list[i];
