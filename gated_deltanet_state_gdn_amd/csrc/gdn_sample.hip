@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(NT1) bins_kernel(SampleArgs a)
         // what lies below has no bin; with min-p and without top-p, which wants the mass of all, what min-p drops
         double below = 33.0 * (double)r.T;
         if (r.min_p > 0.0f && r.top_p >= 1.0f) below = fmin(below, -1.001 * (double)r.T * log((double)r.min_p));
-        const float low = (float)((double)m - below - 1e-6 * fabs((double)m));
+        // (at least the lowest number: beyond that -inf, which is no token, would have a weight)
+        const float low = fmaxf((float)((double)m - below - 1e-6 * fabs((double)m)), -kHighest);
         const uint32_t top_bits = (uint32_t)__double_as_longlong(top + kRound);
         Series series;
         double round = kRound;

@@ -1,7 +1,11 @@
 """GPU: calls at the limits of what the operators around a prefix cache allow."""
+import math
+
 import pytest
 import torch
 
+import ops_reference as R
+import prefix_reference as PR
 from gpu_helpers import say
 from test_gpu_ops import BF, F32, TYPES, Rand  # noqa: F401
 from test_gpu_prefix import draw_check, settings
@@ -53,3 +57,36 @@ def test_sample_flat_rows_of_odd_length(dt):
         x = torch.zeros(9, vocab, dtype=dt, device="cuda")
         say("flat", dt, vocab)
         assert G().gdn_sample(x, u).tolist() == [int(v * vocab) for v in u.double().tolist()]
+
+
+@TYPES
+@pytest.mark.parametrize("vocab", [5, 1000, 2049, 40000])
+def test_sample_at_the_highest_temperatures(dt, vocab):
+    # 33 T passes the largest number: -inf, in the row and where its last chunk has no elements, is still no token
+    rows = 6
+    x = Rand(vocab).n(rows, vocab + 1, scale=2.0).to(dt)[:, 1:]
+    top = torch.finfo(dt).max
+    x[1, 1::2] = -math.inf
+    x[2, 3:] = -math.inf
+    x[3, 1:] = -top                                              # weights of 1 and, at T = 3.4e38, 1 / e
+    x[3, 0] = 0.0
+    x[4] = -top
+    x[4, ::3] = -math.inf
+    x[5, 0], x[5, 1] = top, -top
+    u = torch.tensor([0.9, 0.6, 0.999, 0.3, 0.7, 0.45], device="cuda")
+    # what counts as 0, weights under e^-32 of the largest, is less than vocab e^-32 of the mass (at T = 1e37 the lowest
+    # numbers weigh e^-33.9 beside 0): a border is so much further off, in mass, and a logprob ln(1 + that) at most
+    lost = vocab * math.exp(-32.0)
+    for T in (1e25, 1.0e37, 1.04e37, 1e38, torch.finfo(F32).max):
+        for kw in (dict(), dict(k=vocab - 1), dict(k=3), dict(p=0.6), dict(m=0.5), dict(m=0.2, p=0.9, k=vocab - 1)):
+            s = settings(rows, T=T, **kw)
+            token, lp = G().gdn_sample(x, u, logprob=True, **s)
+            for i in range(rows):
+                want, l, margin = PR.draw(x[i], u[i].item(), *(0 if s[n] is None and n == "top_k" else {"top_p": 1.0, "min_p": 0.0}[n] if s[n] is None
+                                                              else s[n][i].item() for n in ("temperature", "top_k", "top_p", "min_p")))
+                what = "T %r %r row %d: %d %r, want %d %r" % (T, kw, i, token[i].item(), lp[i].item(), want, l)
+                # equal weights meet borders exactly; else what lies nearer than the documented accuracy is left out
+                if 0.0 < margin < 2.0 ** -34 + lost:
+                    continue
+                assert token[i].item() == want, what
+                assert abs(lp[i].item() - l) <= R.U32 * abs(l) + 3 * 2.0 ** -36 + lost, what
