@@ -743,13 +743,20 @@ __global__ void __launch_bounds__(NT) join_kernel(AttnArgs a)
     const int32_t b = a.cu[n], e = a.cu[n + 1];
     if (!range_ok(b, e, a.total) || t < b || t >= e) return;
     const int32_t kv = a.kv_len[n];
-    if (!kv_ok(kv, a.max_kv, a.page_size, a.max_pages)) return;
+    // (shared: recorded here, for there may be no block of own keys that would)
+    if (!kv_ok(kv, a.max_kv, a.page_size, a.max_pages)) {
+        if (SHARED && threadIdx.x == 0) set_status(a.status);
+        return;
+    }
     const int32_t limit = kv - (e - (int32_t)t) + 1;
     // the parts that the row's keys are in: with a prefix its splits, then the row's own behind them
     int act, pre = 0;
     if constexpr (SHARED) {
         int32_t P;
-        if (!find_prefix(a, n, kv, P)) return;
+        if (!find_prefix(a, n, kv, P)) {
+            if (threadIdx.x == 0) set_status(a.status);
+            return;
+        }
         const int32_t seen = limit < 0 ? 0 : limit < P ? limit : P;
         pre = (int)(((int64_t)seen + a.prefix_keys - 1) / a.prefix_keys);
         act = pre + (limit > P ? (int)(((int64_t)limit - P + a.split_keys - 1) / a.split_keys) : 0);

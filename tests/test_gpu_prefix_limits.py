@@ -7,8 +7,8 @@ import torch
 import ops_reference as R
 import prefix_reference as PR
 from gpu_helpers import say
-from test_gpu_ops import BF, F32, TYPES, Rand  # noqa: F401
-from test_gpu_prefix import draw_check, settings
+from test_gpu_ops import BF, F32, TYPES, Rand, cu_of, ints, new_ws  # noqa: F401
+from test_gpu_prefix import SharedCache, draw_check, settings, shared_check
 
 pytestmark = pytest.mark.gpu
 
@@ -24,6 +24,36 @@ def _gpu():
 def G():
     import gated_deltanet_state_gdn_amd as gdn
     return gdn
+
+
+# ------------------------------------------------------------------ shared prefixes
+@TYPES
+@pytest.mark.parametrize("lens", [[1, 1, 1], [40, 1, 2]])
+def test_shared_attention_reports_bad_input_without_own_keys(dt, lens):
+    # the bounds leave no own keys, or no keys at all: no block but the join's looks at a sequence
+    hq, hk, dim, pre = 4, 2, 64, [40, 30]
+    kv = [40, 40, 30]
+    c = SharedCache(Rand(3), [(40, kv[:2]), (30, kv[2:])], 16, hk, dim, dt)
+    q = Rand(4).n(sum(lens), hq, dim, dt=dt)
+
+    def status(kv_len, prefix=pre, groups=(0, 2, 3), max_kv_len=40, max_prefix_len=40):
+        ws = new_ws(1 << 22)
+        o, lse = G().gdn_shared_attn(q, c.k, c.v, c.table, ints(cu_of(lens)), ints(kv_len), ints(list(groups)), ints(prefix), lse=True, ws=ws,
+                                     max_kv_len=max_kv_len, max_prefix_len=max_prefix_len, max_own_len=0)
+        return G().gdn_device_status(ws), o, lse
+
+    bad = G().GDN_ERR_DEVICE_INPUT
+    st, o, lse = status(kv)
+    assert st == 0
+    shared_check(c, q, o, lse, lens, kv, dim ** -0.5, dt)
+    for i in range(3):
+        for v in (-1, kv[i] + 1, 41, 1000):                      # negative, longer than its prefix, than max_kv_len
+            assert status(kv[:i] + [v] + kv[i + 1:])[0] == bad, (i, v)
+    for p in ([-1, 30], [41, 30], [40, 29]):
+        assert status(kv, p)[0] == bad, p
+    assert status([0, 0, 0], [0, 0], max_kv_len=0, max_prefix_len=0)[0] == 0
+    for k, p in (([0, 0, 1], [0, 0]), ([-1, 0, 0], [0, 0]), ([0, 0, 0], [0, 1]), ([0, 0, 0], [-1, 0])):
+        assert status(k, p, max_kv_len=0, max_prefix_len=0)[0] == bad, (k, p)
 
 
 # ------------------------------------------------------------------ the next token
