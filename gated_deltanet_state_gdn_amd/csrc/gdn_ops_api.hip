@@ -414,8 +414,9 @@ int32_t gdn_shared_attn(const gdn_shared_desc *s, const void *q, const void *k_c
     const int64_t row = (int64_t)d->h_q * d->d;
     if (!stride_ok(d->q_stride, row, d->dtype) || !stride_ok(d->o_stride, row, d->dtype))
         return refuse(GDN_ERR_ALIGN, "q and output strides: at least a token's row, a multiple of 16 bytes");
+    // (a prefix may be longer than any kv_len, and its keys are read even where no token sees them)
     if (!cu || !kv_len || !cu_groups || !prefix_len || (d->total_tokens > 0 && (!q || !o)) ||
-        (d->total_tokens > 0 && d->max_kv_len > 0 && (!k_cache || !v_cache || !block_table)))
+        (d->total_tokens > 0 && (d->max_kv_len > 0 || s->max_prefix_len > 0) && (!k_cache || !v_cache || !block_table)))
         return GDN_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(lse) || !aligned4(block_table) ||
         !aligned4(cu) || !aligned4(kv_len) || !aligned4(cu_groups) || !aligned4(prefix_len))
