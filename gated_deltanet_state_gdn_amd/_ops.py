@@ -238,9 +238,9 @@ def make_shared_desc(q, k_cache, block_table, n_seqs, n_groups, *, max_kv_len=No
                      max_own_len=None) -> GdnSharedDesc:
     """Sizes of a gdn_shared_attn call, for its workspace; the bounds as that call takes them."""
     cache = make_paged_desc(q, k_cache, block_table, n_seqs, max_kv_len=max_kv_len)
-    most = cache.max_kv_len
+    most, hold = cache.max_kv_len, min(cache.max_pages * cache.page_size, 1 << 30)
     return GdnSharedDesc(cache=cache, n_groups=int(n_groups),
-                         max_prefix_len=most if max_prefix_len is None else min(int(max_prefix_len), most),
+                         max_prefix_len=most if max_prefix_len is None else min(int(max_prefix_len), hold),
                          max_own_len=most if max_own_len is None else min(int(max_own_len), most))
 
 
@@ -254,7 +254,8 @@ def gdn_shared_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_len, cu_gro
     (cu_groups [n_groups + 1], prefix_len [n_groups], int32): a prefix is read once for its group.
 
     ``max_prefix_len``, ``max_own_len``: no prefix_len, no kv_len - prefix_len is larger (None: max_kv_len;
-    tight bounds spread the work better and need less workspace).  ``ws``, when given, holds
+    tight bounds spread the work better and need less workspace).  A prefix may be longer than any kv_len of its
+    sequences: where max_kv_len is below it, max_prefix_len has to be given.  ``ws``, when given, holds
     gdn_shared_workspace_bytes(make_shared_desc(...)) bytes.  The rest as gdn_paged_attn.
     """
     if stream is not None:

@@ -430,6 +430,7 @@ PyObject *step(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
 struct Paged {
     const at::Tensor &q, &kc, &vc, &table, &cu, &kv;
     gdn_paged_desc d = {};
+    int32_t holds;              // cached tokens of a row of the block table, at most 2^30
     Paged(Call &c, PyObject *q_, PyObject *kc_, PyObject *vc_, PyObject *table_, PyObject *cu_, PyObject *kv_, PyObject *max_kv)
         : q(c.tensor(q_, "q")), kc(c.tensor(kc_, "k_cache")), vc(c.tensor(vc_, "v_cache")), table(c.tensor(table_, "block_table")),
           cu(c.tensor(cu_, "cu_seqlens")), kv(c.tensor(kv_, "kv_len")) {
@@ -449,6 +450,7 @@ struct Paged {
         d.page_size = c.size32(kc.size(1)); d.n_pages = c.size32(kc.size(0)); d.max_pages = c.size32(most);
         const int64_t hold = most * kc.size(1);
         int64_t bound = hold < (1 << 30) ? hold : 1 << 30;
+        holds = (int32_t)bound;
         if (max_kv != Py_None) {
             const int64_t m = integer(max_kv);
             c.need(m >= 0 && m <= (1 << 30), "max_kv_len out of range");
@@ -528,12 +530,12 @@ PyObject *attn(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
     });
 }
 
-// A bound on a device array's values, at most `most`.
-int32_t bound(const Call &c, PyObject *o, int32_t most, const char *arg) {
+// A bound on a device array's values, `most` if none is given; more than the block table `holds` is as good as that.
+int32_t bound(const Call &c, PyObject *o, int32_t most, int32_t holds, const char *arg) {
     if (o == Py_None) return most;
     const int64_t v = integer(o);
     if (v < 0 || v > (1 << 30)) c.refuse(GDN_ERR_SHAPE, arg, "out of range");
-    return v < most ? (int32_t)v : most;
+    return v < holds ? (int32_t)v : holds;
 }
 
 // q, k_cache, v_cache, table, cu, kv_len, cu_groups, prefix_len, max_kv, max_prefix, max_own, scale, o, lse, ws
@@ -552,8 +554,9 @@ PyObject *shared(PyObject *, PyObject *const *v, Py_ssize_t nargs) {
         if (v[12] != Py_None) p.d.o_stride = c.rows(o = c.tensor(v[12], "o"), {T, p.d.h_q, p.d.d}, e, "o");
         const Out kind = out_kind(v[13]);
         if (kind == Out::given) c.whole(lse = c.tensor(v[13], "lse"), {T, p.d.h_q}, F32, "lse");
+        // a prefix may be longer than any kv_len, own keys may not
         const int32_t most = p.d.max_kv_len;
-        gdn_shared_desc d = {p.d, c.size32(n), bound(c, v[9], most, "max_prefix_len"), bound(c, v[10], most, "max_own_len")};
+        gdn_shared_desc d = {p.d, c.size32(n), bound(c, v[9], most, p.holds, "max_prefix_len"), bound(c, v[10], most, most, "max_own_len")};
         c.on_gpu();
         c10::DeviceGuard guard(c.device);
         if (!o.defined()) o = c.make({T, p.d.h_q, p.d.d}, e);

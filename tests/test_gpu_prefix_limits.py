@@ -56,6 +56,27 @@ def test_shared_attention_reports_bad_input_without_own_keys(dt, lens):
         assert status(k, p, max_kv_len=0, max_prefix_len=0)[0] == bad, (k, p)
 
 
+@TYPES
+@pytest.mark.parametrize("hq,dim,lens,kv,pre,of", [
+    (8, 64, [1, 1], [30, 35], [40], [0, 2]),                     # every kv_len below the prefix
+    (8, 64, [3, 40, 1, 2], [30, 70, 5, 90], [100, 64], [0, 2, 4]),
+    (4, 256, [1, 2, 1], [1, 500, 90], [600], [0, 3]),
+    (2, 128, [1, 1, 1], [0, 0, 0], [64], [0, 3]),                # nothing is cached yet
+])
+def test_shared_attention_with_tight_bounds_below_the_prefix(dt, hq, dim, lens, kv, pre, of):
+    r = Rand(dim + len(kv))
+    c = SharedCache(r, [(p, kv[of[i]:of[i + 1]]) for i, p in enumerate(pre)], 16, 1, dim, dt)
+    q = r.n(sum(lens), hq, dim, dt=dt)
+    own = max(max(k - pre[i], 0) for i in range(len(pre)) for k in kv[of[i]:of[i + 1]])
+    for bounds in (dict(max_kv_len=max(kv), max_prefix_len=max(pre), max_own_len=own), dict(max_kv_len=max(kv), max_prefix_len=max(pre)),
+                   dict(max_kv_len=max(kv), max_prefix_len=1 << 20, max_own_len=1 << 20), dict(max_prefix_len=max(pre), max_own_len=own)):
+        say("tight", dt, hq, dim, kv, pre, bounds)
+        ws = new_ws(G().gdn_shared_workspace_bytes(G().make_shared_desc(q, c.k, c.table, len(kv), len(pre), **bounds)))
+        o, lse = G().gdn_shared_attn(q, c.k, c.v, c.table, ints(cu_of(lens)), ints(kv), ints(of), ints(pre), lse=True, ws=ws, **bounds)
+        assert G().gdn_device_status(ws) == 0, bounds
+        shared_check(c, q, o, lse, lens, kv, dim ** -0.5, dt)
+
+
 # ------------------------------------------------------------------ the next token
 @TYPES
 @pytest.mark.parametrize("width", [32768, 131072])
