@@ -464,7 +464,7 @@ int32_t gdn_cache_extend(const gdn_extend_desc *d, const int32_t *new_len, const
     if (st != GDN_OK) return st;
     gdn::ExtendArgs a = {};
     a.new_len = new_len; a.kv_len = kv_len; a.free_pages = free_pages; a.free_at = free_at;
-    a.prefix_of = d->n_prefixes > 0 ? prefix_of : nullptr; a.prefix_table = prefix_table; a.prefix_len = prefix_len;
+    a.prefix_of = prefix_of; a.prefix_table = prefix_table; a.prefix_len = prefix_len;
     a.table = block_table; a.kv_out = kv_out; a.free_out = free_out; a.cu = cu_seqlens; a.slots = slots; a.positions = positions;
     a.status = static_cast<int32_t *>(ws);
     a.plan = reinterpret_cast<int64_t *>(static_cast<char *>(ws) + kWorkspaceBytes);

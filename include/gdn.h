@@ -395,7 +395,7 @@ int32_t gdn_paged_attn(const gdn_paged_desc *desc, const void *q, const void *k_
  *   slots (nullable) [total_tokens] int64   page * page_size + place in the page of each new token,
  *   positions (nullable) [total_tokens]     and its position; -1 in both behind the last new token.
  * total_tokens: at least the sum of new_len (known on the host as a bound; larger under a captured graph).
- * A step that does not fit (a length or prefix out of range, a prefix that ends inside a page, more than
+ * A step that does not fit (a length or prefix out of range, which without prefixes is every one but -1, a prefix that ends inside a page, more than
  * max_pages, n_free or total_tokens) sets the status bit and takes nothing: tables as they were, kv_out =
  * kv_len, free_out = free_at, cu_seqlens 0, slots and positions -1.  Page numbers are taken as they are. */
 typedef struct {

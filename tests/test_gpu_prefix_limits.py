@@ -8,7 +8,7 @@ import ops_reference as R
 import prefix_reference as PR
 from gpu_helpers import say
 from test_gpu_ops import BF, F32, TYPES, Rand, cu_of, ints, new_ws  # noqa: F401
-from test_gpu_prefix import SharedCache, draw_check, settings, shared_check
+from test_gpu_prefix import SharedCache, extend_call, extend_case, draw_check, settings, shared_check
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,27 @@ def test_sample_at_the_highest_temperatures(dt, vocab):
                     continue
                 assert token[i].item() == want, what
                 assert abs(lp[i].item() - l) <= R.U32 * abs(l) + 3 * 2.0 ** -36 + lost, what
+
+
+# ------------------------------------------------------------------ block tables
+@pytest.mark.parametrize("n,total", [(20, 0), (20, 5000), (1500, 0)])
+def test_extend_with_an_empty_prefix_table(n, total):
+    # no prefix is there: a request that names one is out of range, and -1 is none as ever
+    c = extend_case(101, n, 16, 6)
+    T = max(sum(c["new"]), total)
+    z = torch.zeros(0, dtype=torch.int32, device="cuda")
+    for shape in ((0, 4), (0, 0)):
+        for hit, where in ((-1, 0), (0, 0), (0, n - 1), (3, n // 2), (-2, 1)):
+            of = [-1] * n
+            of[where] = hit
+            ws = new_ws(G().gdn_extend_workspace_bytes(n))
+            out = extend_call(c, T, ws, prefix_of=ints(of), prefix_table=z.view(*shape), prefix_len=z)
+            if hit == -1:
+                assert G().gdn_device_status(ws) == 0
+                want = PR.extend(c["new"], c["kv"], c["table"], c["free"], c["at"], 16, T)
+                assert [x.tolist() for x in out] == [[w] if i == 3 else w for i, w in enumerate(want)]
+            else:
+                assert G().gdn_device_status(ws) == G().GDN_ERR_DEVICE_INPUT, (n, hit, where)
+                table, cu, kv, at, slots, positions = out
+                assert table.tolist() == c["table"] and cu.tolist() == [0] * (n + 1) and kv.tolist() == c["kv"] and at.tolist() == [c["at"]]
+                assert (slots == -1).all() and (positions == -1).all()
