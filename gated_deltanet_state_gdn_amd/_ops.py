@@ -275,6 +275,7 @@ def make_sample_desc(logits) -> GdnSampleDesc:
 
 
 def gdn_sample_workspace_bytes(desc: GdnSampleDesc) -> int:
+    """Bytes of a gdn_sample call's workspace, enough for fewer rows of the same vocabulary and type too."""
     return int(load().gdn_sample_workspace_bytes(ctypes.byref(desc)))
 
 

@@ -180,16 +180,23 @@ struct SamplePlan {
     int32_t chunk, chunks;
     size_t bins, bytes;
 };
-SamplePlan sample_plan(const gdn_sample_desc *d)
+SamplePlan sample_plan(int64_t rows, const gdn_sample_desc *d)
 {
     SamplePlan p;
-    p.chunk = gdn::sample_chunk(d->rows, d->vocab);
+    p.chunk = gdn::sample_chunk(rows, d->vocab);
     // a row may start inside a 16-byte piece
     p.chunks = (int32_t)((d->vocab + 16 / elem_bytes(d->dtype) - 1 + p.chunk - 1) / p.chunk);
-    const size_t all = (size_t)d->rows * (size_t)p.chunks;
+    const size_t all = (size_t)rows * (size_t)p.chunks;
     p.bins = kWorkspaceBytes + up256(all * 16);
     p.bytes = p.bins + all * gdn::kSampleBins * sizeof(uint64_t);
     return p;
+}
+// Enough for fewer rows too: those whose chunks are small may need more (57 rows of 49999 2.9 MB, 58 0.84).
+size_t sample_bytes(const gdn_sample_desc *d)
+{
+    const int64_t small = gdn::sample_small_rows(d->vocab);
+    const size_t all = sample_plan(d->rows, d).bytes, fewer = sample_plan(d->rows < small ? d->rows : small, d).bytes;
+    return all > fewer ? all : fewer;
 }
 
 }  // namespace
@@ -476,7 +483,7 @@ int32_t gdn_cache_extend(const gdn_extend_desc *d, const int32_t *new_len, const
 
 size_t gdn_sample_workspace_bytes(const gdn_sample_desc *d)
 {
-    return check_sample(d) == GDN_OK ? sample_plan(d).bytes : 0;
+    return check_sample(d) == GDN_OK ? sample_bytes(d) : 0;
 }
 
 int32_t gdn_sample(const gdn_sample_desc *d, const void *logits, const float *u, const float *temperature, const int32_t *top_k,
@@ -488,7 +495,7 @@ int32_t gdn_sample(const gdn_sample_desc *d, const void *logits, const float *u,
     if (((uintptr_t)logits & (uintptr_t)(elem_bytes(d->dtype) - 1)) || !aligned4(u) || !aligned4(temperature) || !aligned4(top_k) ||
         !aligned4(top_p) || !aligned4(min_p) || !aligned4(token) || !aligned4(logprob))
         return refuse(GDN_ERR_ALIGN, "pointer alignment: an element's");
-    const SamplePlan p = sample_plan(d);
+    const SamplePlan p = sample_plan(d->rows, d);
     st = check_ws(ws, ws_bytes, p.bytes);
     if (st != GDN_OK || d->rows == 0) return st;
     char *w = static_cast<char *>(ws);

@@ -283,9 +283,8 @@ constexpr int kSampleBins = 256;
 // Elements of a chunk, one workgroup's.  Small ones are read by more workgroups, sooner; a row's many of them take its
 // workgroup longer to join, and all of them more to write.  bf16, 2048 against 8192: one row of 32768 takes 19.8 us and 21.3,
 // of 100000 22.8 and 21.6; 48 rows of 50000 36.5 and 36.8, 100 rows 39.5 and 38.0; 32 rows of 262144 62 and 51.
-inline int32_t sample_chunk(int64_t rows, int32_t vocab)
-{
-    return vocab <= 65536 && rows * ((vocab + 8191) / 8192) < 400 ? 2048 : 8192;
-}
+// So many rows have small ones, of up to 65536 elements: those of fewer than 400 large ones.
+inline int64_t sample_small_rows(int32_t vocab) { return vocab <= 65536 ? 399 / ((vocab + 8191) / 8192) : 0; }
+inline int32_t sample_chunk(int64_t rows, int32_t vocab) { return rows <= sample_small_rows(vocab) ? 2048 : 8192; }
 
 }  // namespace gdn

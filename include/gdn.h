@@ -448,6 +448,7 @@ typedef struct {
     int32_t dtype;             /* gdn_dtype of the logits */
     int64_t stride;
 } gdn_sample_desc;
+/* Enough for any fewer rows of the same vocabulary and type, too. */
 size_t gdn_sample_workspace_bytes(const gdn_sample_desc *desc);
 int32_t gdn_sample(const gdn_sample_desc *desc, const void *logits, const float *u, const float *temperature,
                    const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *logprob,

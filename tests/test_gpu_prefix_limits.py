@@ -143,6 +143,18 @@ def test_sample_at_the_highest_temperatures(dt, vocab):
                 assert abs(lp[i].item() - l) <= R.U32 * abs(l) + 3 * 2.0 ** -36 + lost, what
 
 
+@TYPES
+def test_sample_workspace_of_the_largest_batch(dt):
+    r = Rand(49999)
+    x, u = r.n(60, 49999, scale=2.0).to(dt), torch.rand(60, generator=r.g).cuda()
+    st = settings(60, T=0.9, k=50, p=0.9)
+    ws = new_ws(G().gdn_sample_workspace_bytes(G().make_sample_desc(x)))
+    want = G().gdn_sample(x, u, **st)
+    for rows in (60, 57, 20, 1):
+        assert torch.equal(G().gdn_sample(x[:rows], u[:rows], ws=ws, **{n: v if v is None else v[:rows] for n, v in st.items()}), want[:rows])
+    assert G().gdn_device_status(ws) == 0
+
+
 # ------------------------------------------------------------------ block tables
 @pytest.mark.parametrize("n,total", [(20, 0), (20, 5000), (1500, 0)])
 def test_extend_with_an_empty_prefix_table(n, total):
