@@ -20,9 +20,10 @@
 //
 // Precision: scores, maximum, sum, O are fp32.  With bf16 elements the products take q, k and v as
 // they are; P is rounded to bf16 once where the products are the bound (half a bf16 step of each term p v; a
-// second term would be half as many products again), and taken in two bf16 terms where memory is.  The
-// sum l takes the unrounded P.  Relative error of the outputs, 2-norm, in the measured cases: 2.3e-3 with one
-// term, 1.7e-3 with two, which is the outputs' own rounding.
+// second term would be half as many products again), and taken in two bf16 terms in the form of few rows, where memory is,
+// and where a batch of few rows a sequence has a prefix in the form of many: which form that takes is the plan's
+// choice, not the caller's.  The sum l takes the unrounded P.  Relative error of the outputs, 2-norm, in the measured
+// cases: 2.3e-3 with one term, 1.7e-3 with two, which is the outputs' own rounding.
 // Keys behind kv_len are never read: whatever a page holds there (or an unused page) does not matter.
 #pragma once
 #include "gdn_mfma.h"
@@ -576,7 +577,8 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
 // on 2 of 256 over 31744 cached ones: 485 to 500 us with the join (16), 1080 to 1115 TFLOP/s (a large
 // matrix product: 1355), matrix cores 48 % busy; fp32, 9 ragged sequences, 1501 tokens of 16 heads on 4 of 64,
 // up to 4000 cached: 133 us, 76 TFLOP/s (153), the join 7.
-template <class M, int D, int NB, int WAVES, int KT, Side S>
+// TERMS: of P, as in step.  64 requests behind one prefix of 31744, 8 heads on each of 2 of 256: 89 us with one, 97 with two.
+template <class M, int D, int NB, int WAVES, int KT, Side S, int TERMS = 1>
 __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 {
     typedef typename M::T T;
@@ -668,8 +670,8 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
                 __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_s_setprio(0);
-            Frag p[NB][1];
-            sf.template step<M, D, 1>(st, scale, k0 + k + 4 * g, limit, k0 + k + 32 > least, o, p);
+            Frag p[NB][TERMS];
+            sf.template step<M, D, TERMS>(st, scale, k0 + k + 4 * g, limit, k0 + k + 32 > least, o, p);
 #pragma unroll
             for (int i = 0; i < PRE; ++i) ring[i] = Tl::value(Vb, k, i, va);
             __builtin_amdgcn_s_setprio(2);
@@ -677,7 +679,9 @@ __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) o[b][d] = M::mma(o[b][d], ring[d % PRE], p[b][0]);
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int term = TERMS - 1; term >= 0; --term) o[b][d] = M::mma(o[b][d], ring[d % PRE], p[b][term]);
                 if (d + PRE < D / 16) ring[d % PRE] = Tl::value(Vb, k, d + PRE, va);
                 __builtin_amdgcn_sched_barrier(0);
             }

@@ -183,6 +183,7 @@ inline AttnPlan attn_plan(int64_t total, int32_t n_seqs, int32_t h_q, int32_t h_
 // ------------------------------------------------------------- attention behind shared prefixes
 struct SharedPlan {
     AttnPlan prefix, own;       // no splits: the side has no keys
+    bool fine;                  // probabilities of 16 bits whatever the form: few rows a sequence, as without groups
 };
 
 // The form of few rows for one side of a call whose parts are joined in any case: the keys of a split that take the
@@ -219,7 +220,7 @@ inline double few_rows_side(int64_t total, int64_t units, int32_t h_q, int32_t h
 // their form of few rows costs only what it reads from the caches again for every 16 rows, and with the own keys in
 // the same form one launch takes both (two requests over 1024 tokens, 2 heads of 256: 14.0 us for 21.3).  bf16: the
 // form of many rows where its time, by long_splits' terms and another launch, is less: 512 rows on each of 2 heads of 256
-// over 31744 tokens take 92 us for 146; 256 rows over 12000 52.4 for 47.  fp32: up to 512 rows for d <= 128 (256 rows
+// over 31744 tokens, and up to 1024 own ones, take 97 us for 177; 256 rows over 12288, up to 300, 53.7 for 48.4.  fp32: up to 512 rows for d <= 128 (256 rows
 // of 128 over 12000: 66 us for 80), but not for 256, whose rows of 1 KB leave a workgroup two waves (141 for 197).
 inline SharedPlan shared_plan(int64_t total, int32_t n_seqs, int32_t n_groups, int32_t h_q, int32_t h_kv, int32_t d,
                               int32_t max_prefix, int32_t max_own, int bf16)
@@ -228,6 +229,7 @@ inline SharedPlan shared_plan(int64_t total, int32_t n_seqs, int32_t n_groups, i
     p.prefix = attn_plan(total, n_groups, h_q, h_kv, d, max_prefix, bf16);
     p.own = attn_plan(total, n_seqs, h_q, h_kv, d, max_own, bf16);
     const int64_t rows = total * (h_q / h_kv);
+    p.fine = rows <= 32 * (int64_t)n_seqs;
     const bool own_few = max_own == 0 ? rows <= 32 * (int64_t)n_groups : p.own.decode;
     if (own_few) {
         const int row = d * (bf16 ? 2 : 4), narrow = decode_waves(row);

@@ -28,9 +28,10 @@ hipError_t decode_n(const AttnArgs &a, const AttnPlan &p, int64_t blocks, hipStr
     return hipErrorNotSupported;                         // the plan has no such rows
 }
 
-// One launch of so many blocks of prefixes and of own keys, in a plan's form.
+// One launch of so many blocks of prefixes and of own keys, in a plan's form.  fine: probabilities in two bf16 terms, as the
+// form of few rows always has them.
 template <class M, int D>
-hipError_t sides(AttnArgs a, const AttnPlan &p, int64_t prefix, int64_t own, hipStream_t stream)
+hipError_t sides(AttnArgs a, const AttnPlan &p, bool fine, int64_t prefix, int64_t own, hipStream_t stream)
 {
     const int64_t blocks = prefix + own;
     a.prefix_blocks = (uint32_t)prefix;
@@ -41,8 +42,8 @@ hipError_t sides(AttnArgs a, const AttnPlan &p, int64_t prefix, int64_t own, hip
         return hipErrorNotSupported;                     // the plan has no such waves
     }
     if constexpr (M::V == 4) return start(prefill_kernel<M, D, 1, 4, 32, kShared>, blocks, a, stream, 256);
-    else if (p.rows == 256) return start(prefill_kernel<M, D, 2, 8, 64, kShared>, blocks, a, stream, 512);
-    else return start(prefill_kernel<M, D, 2, 4, 64, kShared>, blocks, a, stream, 256);
+    else if (p.rows == 256) return start(fine ? prefill_kernel<M, D, 2, 8, 64, kShared, 2> : prefill_kernel<M, D, 2, 8, 64, kShared>, blocks, a, stream, 512);
+    else return start(fine ? prefill_kernel<M, D, 2, 4, 64, kShared, 2> : prefill_kernel<M, D, 2, 4, 64, kShared>, blocks, a, stream, 256);
 }
 
 template <class M, int D>
@@ -62,9 +63,9 @@ hipError_t shared_d(AttnArgs a, const SharedPlan &p, hipStream_t stream)
     // one launch where both sides take the same form
     const bool same = p.prefix.decode == p.own.decode && p.prefix.rows == p.own.rows && (!p.own.decode || p.prefix.waves == p.own.waves);
     hipError_t e = hipSuccess;
-    if (same && prefix + own > 0) e = sides<M, D>(a, p.own, prefix, own, stream);
-    if (!same && prefix > 0) e = sides<M, D>(a, p.prefix, prefix, 0, stream);
-    if (!same && own > 0 && e == hipSuccess) e = sides<M, D>(a, p.own, 0, own, stream);
+    if (same && prefix + own > 0) e = sides<M, D>(a, p.own, p.fine, prefix, own, stream);
+    if (!same && prefix > 0) e = sides<M, D>(a, p.prefix, p.fine, prefix, 0, stream);
+    if (!same && own > 0 && e == hipSuccess) e = sides<M, D>(a, p.own, p.fine, 0, own, stream);
     if (e != hipSuccess) return e;
     if (sliced) return start(join_kernel<M, D, R, true>, joins, a, stream, NT);
     return start(join_kernel<M, D, 1, true>, joins, a, stream, NT);

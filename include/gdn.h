@@ -419,7 +419,8 @@ int32_t gdn_cache_extend(const gdn_extend_desc *desc, const int32_t *new_len, co
  * in it sees the keys at its position and before, and its sequence's kv_len may be less than the prefix.  The
  * first sequence's table names all of the prefix's pages even then, or if it has no new token.  A bad cu_groups,
  * prefix_len, cu_seqlens, kv_len or page sets the status bit; the outputs of those groups are unspecified.
- * Precision as of gdn_paged_attn, the rows of a prefix being those of its group. */
+ * Precision as of gdn_paged_attn: bf16 probabilities have 16 bits in batches of up to 32 rows a sequence on average,
+ * behind a prefix too, however many rows its group has. */
 typedef struct {
     gdn_paged_desc cache;
     int32_t n_groups;

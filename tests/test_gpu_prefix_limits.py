@@ -77,6 +77,43 @@ def test_shared_attention_with_tight_bounds_below_the_prefix(dt, hq, dim, lens, 
         shared_check(c, q, o, lse, lens, kv, dim ** -0.5, dt)
 
 
+FINE = [  # h_kv, query heads of each, d, requests, groups: a token of each, whose prefix takes the form of 128 or 256 rows
+    (2, 8, 64, 32, 2), (2, 8, 64, 64, 1), (1, 8, 128, 32, 4), (1, 8, 128, 64, 1), (1, 8, 256, 32, 2), (1, 8, 256, 64, 1)]
+
+
+@pytest.mark.parametrize("hk,per,dim,n,n_groups", FINE)
+def test_shared_attention_keeps_the_precision_of_few_rows(hk, per, dim, n, n_groups):
+    # Two kinds of keys in turn, of probabilities 1 and 0.5016 before the division.  0.5016 is nearly half a bf16 step off
+    # 0.5, and the values, 1 and -0.5, nearly cancel, so that rounding P to bf16 once would be off by as much as the output
+    # itself, 1e-3.  Probabilities of 16 bits are off by 2^-16 relatively, 7e-6 of these outputs' sum of absolutes.
+    ps, P, scale = 16, 700, 0.69003
+    kc, vc = torch.zeros(9, ps, hk, dim, dtype=BF, device="cuda"), torch.full((9, ps, hk, dim), -0.5, dtype=BF, device="cuda")
+    kc[:, 1::2, :, 0] = 1.0                                      # every page holds the same
+    vc[:, 0::2] = 1.0
+    vc[..., 1::2] *= -1.0
+    q = torch.zeros(n, hk * per, dim, dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    table = (torch.arange(n * 2000, dtype=torch.int32) * 7 % 9).view(n, 2000).cuda()
+    kv = [P + 1 + i % 5 for i in range(n)]
+    cu, of = cu_of([1] * n), [n // n_groups * g for g in range(n_groups + 1)]
+    for pre in (P, 37):
+        ws = new_ws(1 << 28)
+        # the bound decides the form
+        o = G().gdn_shared_attn(q, kc, vc, table, ints(cu), ints(kv), ints(of), ints([pre] * n_groups), scale=scale, ws=ws, max_prefix_len=31744,
+                                max_own_len=700, max_kv_len=31744)
+        assert G().gdn_device_status(ws) == 0
+        whole = G().gdn_paged_attn(q, kc, vc, table, ints(cu), ints(kv), scale=scale, max_kv_len=max(kv))
+        for i in range(5):
+            keys, vals = (R.d(c[table[i, :45].long()].flatten(0, 1)[:kv[i]]) for c in (kc, vc))
+            ref, oa, _, big = R.attend(R.d(q[i]), keys, vals, kv[i] - 1, scale)
+            # as attn_tols, but for 16 bits of P where that counts 8
+            off = 2 * (dim + 4) * R.U32 * big + (kv[i] + 8) * R.U32
+            tol = R.u(BF) * ref.abs() + (off[:, None] + 2.0 ** -16) * (1 + 2 ** -6) * oa
+            for j in range(i, n, 5):
+                R.within(o[j], ref, tol, "request %d" % j)
+                R.within(whole[j], ref, tol, "request %d, without groups" % j)
+
+
 # ------------------------------------------------------------------ the next token
 @TYPES
 @pytest.mark.parametrize("width", [32768, 131072])

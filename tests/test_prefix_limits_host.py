@@ -1,4 +1,10 @@
 """Host-side checks at the limits of what the operators around a prefix cache allow (no GPU: no call here reaches a kernel)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
 from test_ops_host import NULL, _call, _i, _z, gdn  # noqa: F401
 from test_prefix_host import _sample, _shared
 
@@ -29,3 +35,44 @@ def test_sample_workspace_serves_fewer_rows(gdn):  # noqa: F811
         for vocab in (1, 100, 2049, 8192, 8193, 32000, 49999, 65536, 65537, 131072, 1 << 24):
             need = [gdn.gdn_sample_workspace_bytes(_sample(gdn, rows=r, vocab=vocab, stride=vocab, dtype=dtype)) for r in range(0, 500)]
             assert need == sorted(need), (dtype, vocab)
+
+
+PROGRAM = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "gdn_plan.h"
+using namespace gdn;
+int main()
+{
+    // bf16 probabilities are as fine as without groups: by the rows of a sequence, whatever form a prefix takes
+    for (int64_t t : {1LL, 64LL, 65LL, 1501LL}) for (int n : {1, 16, 64, 100}) for (int g : {1, 4, 100}) for (int h : {1, 8}) for (int rep : {1, 8, 32})
+        for (int d : {64, 128, 256}) for (int pre : {0, 700, 31744}) for (int own : {0, 40, 5000}) {
+            const SharedPlan p = shared_plan(t, n, g, h * rep, h, d, pre, own, 1);
+            if (p.fine != attn_plan(t, n, h * rep, h, d, pre + own, 1).decode) return 1;
+            if (own > 0 && p.own.decode != p.fine) return 2;
+        }
+    // what the test on the GPU of that relies on
+    const int at[][6] = {%s};
+    for (auto &c : at) {
+        const SharedPlan p = shared_plan(c[3], c[3], c[4], c[0] * c[1], c[0], c[2], 31744, 700, 1);
+        if (p.prefix.decode || p.prefix.rows != c[5] || !p.fine) {
+            printf("d %%d, %%d requests: decode %%d, rows %%d\n", c[2], c[3], p.prefix.decode, p.prefix.rows);
+            return 3;
+        }
+    }
+    puts("plans: ok");
+    return 0;
+}
+"""
+
+
+def test_plans_keep_the_precision_of_few_rows(tmp_path):
+    from test_gpu_prefix_limits import FINE
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, exe = tmp_path / "plans.cpp", str(tmp_path / "plans")
+    src.write_text(PROGRAM % ", ".join("{%d, %d, %d, %d, %d, %d}" % (*c, 128 if c[3] == 32 else 256) for c in FINE))
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-I", os.path.join(root, "gated_deltanet_state_gdn_amd", "csrc"), str(src), "-o", exe])
+    p = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert p.returncode == 0, (p.returncode, p.stdout)
