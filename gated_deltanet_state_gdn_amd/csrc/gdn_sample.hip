@@ -15,9 +15,10 @@
 //
 // Precision: 8 x / T and exp are taken in 64 bits (which run at the rate of 32 here).  A token's weight
 // enters its bin as an integer of units 2^-35 relative to the bin's centre, so that the sums do not depend
-// on the order of the atomics; a bin's mass is off by half a unit a token, 2^-36 of it at most, and by
-// less the more tokens it has.  A token of the true border's neighbourhood is taken for it only where u (or
-// p) lies that close.
+// on the order of the atomics.  It is off by half a unit, and by 2^-40 for the series: by e = 1.13 2^-36 of itself at most,
+// for it is at least e^(-1/16) of the centre's.  All masses are, so that the mass in front of a border and the mass u M (or
+// p M) that it is compared with differ by 2 e M at most from the formula's, 2^-34.8 M: a token next to the true one is taken
+// for it only where u (or p) lies within 2^-34 of the border.  The sums of bins and their factors, 2^-50, are beside that.
 //
 // Bound by instructions and by the latency of dependent steps, not by memory: 64 rows of 131072 fp32 logits (33.5 MB, 7
 // us of a large copy) take 11 us in the first launch and some 40 in the second, whose workgroups are one a row and whose

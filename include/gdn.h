@@ -442,8 +442,8 @@ int32_t gdn_shared_attn(const gdn_shared_desc *desc, const void *q, const void *
  * (nullable): ln of the token's share of the mass that stayed, 0 for T = 0.  Logits of -inf are never
  * drawn; NaN counts as -inf and +inf as the highest fp32 value.  A row without any other gives -1, and
  * a logprob of -inf; so does one whose settings are out of range, which also sets the status bit.
- * Computed in 64 bits: the token is the formula's unless u or top_p is closer than about 2^-36 to where
- * the next one begins; weights under e^-32 of the largest count as 0. */
+ * Computed in 64 bits: the token is the formula's unless u or top_p is within 2^-34 of where another one begins, as
+ * shares of the mass; weights under e^-31.8 of the largest may count as 0. */
 typedef struct {
     int32_t rows, vocab;       /* vocab at most 2^24 */
     int32_t dtype;             /* gdn_dtype of the logits */

@@ -192,6 +192,62 @@ def test_sample_workspace_of_the_largest_batch(dt):
     assert G().gdn_device_status(ws) == 0
 
 
+def draw_of_classes(values, counts, u, T, k, p, m):
+    """The draw from counts[c] tokens of each of the falling logits values[c] -> (class, place in it, how far u and p are from
+    a border, in mass).  Sums of few products, exact to 2^-50 however many tokens there are."""
+    w = [math.exp((v - values[0]) / T) for v in values]
+    n, left = [], k or sum(counts)
+    for c in counts:
+        n.append(min(c, left))
+        left -= n[-1]
+
+    def border(target):
+        front = 0.0
+        for c, (a, b) in enumerate(zip(n, w)):
+            if front + a * b > target:
+                return c, (target - front) / b
+            front = math.fsum(x * y for x, y in zip(n[:c + 1], w))
+        return len(n) - 1, float(n[-1])
+
+    margin = 1.0
+    if p < 1.0:
+        mass = math.fsum(a * b for a, b in zip(n, w))
+        c, at = border(p * mass)
+        margin = abs(at - round(at)) * w[c] / mass
+        n = n[:c] + [math.ceil(at)]                              # the first so many that reach p of the mass
+    n = [a if b >= m else 0 for a, b in zip(n, w)]
+    mass = math.fsum(a * b for a, b in zip(n, w))
+    c, at = border(u * mass)
+    return c, math.floor(at), min(margin, abs(at - round(at)) * w[c] / mass), math.log(w[c] / mass)
+
+
+@TYPES
+def test_sample_accuracy_of_the_largest_vocabulary(dt):
+    # the stated 2^-34, at 2^24 tokens: of few thousand different logits, whose masses are known exactly from their counts
+    rows, vocab = 3, 1 << 24
+    r = Rand(24)
+    x = (r.n(rows, vocab + 3, scale=1.5).to(BF) + 0.0).to(dt)[:, 3:]
+    x[1] = (x[1] * 0.25).to(BF).to(dt) + 0.0
+    classes = [torch.unique(row.float(), return_counts=True) for row in x]
+    classes = [(v.flip(0).tolist(), c.flip(0).tolist()) for v, c in classes]
+    near = 0
+    for T, k, p, m in ((1.0, 0, 1.0, 0.0), (0.8, 9000000, 0.7, 0.0), (1.3, 0, 0.999, 0.01), (1.0, 0, 1.0, 0.2)):
+        for _ in range(3):
+            u = torch.rand(rows, generator=r.g).cuda()
+            s = settings(rows, T=T, k=k, p=p, m=m)
+            token, lp = G().gdn_sample(x, u, logprob=True, **s)
+            for i, (values, counts) in enumerate(classes):
+                c, at, margin, l = draw_of_classes(values, counts, u[i].item(), *(s[a][i].item() for a in ("temperature", "top_k", "top_p", "min_p")))
+                say("  T %g k %d p %g m %g row %d: place %d of %d, %.1e from a border" % (T, k, p, m, i, at, counts[c], margin))
+                if margin < 2.0 ** -34:
+                    near += 1
+                    continue
+                assert token[i].item() == (x[i].float() == values[c]).nonzero()[at].item(), (T, k, p, m, i)
+                # the rounding to fp32, and the weight's and the mass's 1.13 2^-36 each
+                assert abs(lp[i].item() - l) <= R.U32 * abs(l) + 3 * 2.0 ** -36
+    assert near <= 3
+
+
 # ------------------------------------------------------------------ block tables
 @pytest.mark.parametrize("n,total", [(20, 0), (20, 5000), (1500, 0)])
 def test_extend_with_an_empty_prefix_table(n, total):
