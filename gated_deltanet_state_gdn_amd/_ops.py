@@ -4,7 +4,9 @@ As the rest of the package: the functions carry the names of the C entry points 
 arguments.  Checks of dtypes, shapes, strides and devices, output allocation and the call itself are
 in the native module (csrc/gdn_torch.cpp): a refusal raises GdnError with the matching status before
 anything is enqueued.  ``ws`` is a zero-filled uint8 workspace that the caller keeps (one for each
-stream or graph that may run at the same time); a call without it makes a new one.  Calls run on
+stream or graph that may run at the same time); a call without it makes a new one.  Where a call's work is
+split over workgroups (gdn_ssm_scan, gdn_paged_attn, gdn_shared_attn), fewer or shorter sequences may need more of it: a
+workspace for calls of several sizes has the most of what each of them needs.  Calls run on
 torch's current stream of the tensors' device, or on ``stream``.  As everywhere in this package, autograd is
 not involved: outputs carry no gradient, whatever the inputs require, and what is updated in place (states,
 caches, given outputs) is so without a new version of the tensor.

@@ -241,9 +241,11 @@ int32_t gdn_device_status(const void *workspace, void *stream, int32_t *status_h
  * errors before anything is enqueued, device-resident integers checked by the kernels into the
  * workspace's status word.  A workspace starts zero-filled; its first 256 bytes are the status
  * word.  Two calls that may run at the same time (two streams, two graphs) need a workspace
- * each.  Rows of x, y, q, k, v may be columns of a wider buffer: a stride field gives the
- * elements from one token's row to the next, the rows themselves are contiguous and start on
- * 16 bytes.  Outputs must not overlap inputs except where it is said.  Rows behind the last
+ * each.  Its bytes are those of the sizes that are asked for: where a call's work is split over
+ * workgroups, fewer or shorter sequences may need more, so a workspace for calls of several sizes
+ * has the most of what each of them needs.  Rows of x, y, q, k, v may be columns of a wider
+ * buffer: a stride field gives the elements from one token's row to the next, the rows themselves
+ * are contiguous and start on 16 bytes.  Outputs must not overlap inputs except where it is said.  Rows behind the last
  * sequence (tokens at or after cu_seqlens[n_seqs]) are left as they were.  Non-finite inputs
  * are not checked: a token's reach the outputs of its own sequence only, but may reach those of
  * the same call's earlier tokens too.  What a cache holds behind a sequence's kv_len is never read.
@@ -419,6 +421,8 @@ int32_t gdn_cache_extend(const gdn_extend_desc *desc, const int32_t *new_len, co
  * in it sees the keys at its position and before, and its sequence's kv_len may be less than the prefix.  The
  * first sequence's table names all of the prefix's pages even then, or if it has no new token.  A bad cu_groups,
  * prefix_len, cu_seqlens, kv_len or page sets the status bit; the outputs of those groups are unspecified.
+ * Non-finite keys or values of a prefix may reach every output of its group, those of sequences whose kv_len ends in
+ * front of them too.
  * Precision as of gdn_paged_attn: bf16 probabilities have 16 bits in batches of up to 32 rows a sequence on average,
  * behind a prefix too, however many rows its group has. */
 typedef struct {
