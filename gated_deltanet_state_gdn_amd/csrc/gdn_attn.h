@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) decode_kernel(At
 // on 2 of 256 over 31744 cached ones: 485 to 500 us with the join (16), 1080 to 1115 TFLOP/s (a large
 // matrix product: 1355), matrix cores 48 % busy; fp32, 9 ragged sequences, 1501 tokens of 16 heads on 4 of 64,
 // up to 4000 cached: 133 us, 76 TFLOP/s (153), the join 7.
-// TERMS: of P, as in step.  64 requests behind one prefix of 31744, 8 heads on each of 2 of 256: 89 us with one, 97 with two.
+// TERMS: of P, as in step.  A prefix of 31744 of 64 requests, 8 heads on each of 2 of 256: 55 us with one, 65 with two.
 template <class M, int D, int NB, int WAVES, int KT, Side S, int TERMS = 1>
 __global__ void __launch_bounds__(64 * WAVES) prefill_kernel(AttnArgs a)
 {

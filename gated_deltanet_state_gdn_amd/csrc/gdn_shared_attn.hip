@@ -13,8 +13,9 @@
 // Bound as attention without groups is: few rows by the reads of keys and values, or at the smallest calls by two
 // launches, many rows by the matrix products; and by the splits' shares, which are written and read in fp32 (16 heads
 // of 256, 64 tokens in 64 splits: 67 MB each way).  Measured, bf16: the next token of two requests behind 1024 tokens
-// 13.5 us (9.4 and the join's 4.1 to 5); of 64 behind 31744, 16 heads on 2 of 256, 98 (prefix 55, own 22, join 15);
-// of 96 behind 7 prefixes of up to 8192, 32 heads on 8 of 128, 129 (45, 71, 12); 12 prompts, 1501 tokens behind 16384, 411.
+// 13.5 us (9.4 and the join's 4.1 to 5); of 64 behind 31744, 16 heads on 2 of 256, 108 (prefix 65, own 22, join 15);
+// of 96 behind 7 prefixes of up to 8192, 32 heads on 8 of 128, 135 (52, 73, 12); 12 prompts, 1501 tokens behind 16384,
+// 411 to 429.
 #include "gdn_attn.h"
 
 namespace gdn {
